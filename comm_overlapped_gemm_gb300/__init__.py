@@ -1,6 +1,7 @@
 """Python binding of libtdx (tile-pipelined collective+GEMM kernels on sm_103a: AllGather+GEMM,
 GEMM+ReduceScatter, GEMM+AllReduce, mixture-of-experts AllToAll dispatch + grouped GEMM and grouped
-GEMM + combine).
+GEMM + combine) and of the row-wise operators around them (root-mean-square norm, routing to
+experts, gated SiLU, each with its gradient).
 
 Argument marshalling only: every function below converts its arguments (torch tensors or raw
 device pointers) into the plain pointers and sizes of the C ABI in ``include/tdx.h`` and calls the
@@ -21,6 +22,7 @@ TDX_ERR_WORKSPACE, TDX_ERR_CUDA, TDX_ERR_TIMEOUT, TDX_ERR_STALE_EPOCH = 4, 5, 6,
 TDX_BF16, TDX_FP8_E4M3, TDX_FP32 = 0, 1, 2
 TDX_FUSED, TDX_GEMM_ONLY, TDX_MOVE_ONLY, TDX_CONSUMER_ONLY = 0, 1, 2, 3
 TDX_PRODUCER_SM, TDX_PRODUCER_COPY_ENGINE = 0, 1
+TDX_SCORE_SOFTMAX, TDX_SCORE_SIGMOID = 0, 1
 OP_AG, OP_RS, OP_AR = 0, 1, 2
 TDX_EPOCH_DEVICE = 0xFFFFFFFF
 
@@ -28,7 +30,9 @@ EXPORTED = ["tdx_opts_default", "tdx_workspace_size", "tdx_workspace_init", "tdx
             "tdx_read_device_status", "tdx_trace_size", "tdx_status_string", "tdx_version", "tdx_plan_info",
             "tdx_ag_gemm_noalloc", "tdx_gemm_ar", "tdx_moe_workspace_size", "tdx_moe_plan_info",
             "tdx_moe_dispatch_gemm", "tdx_moe_combine_workspace_size", "tdx_moe_combine_plan_info",
-            "tdx_moe_gemm_combine"]
+            "tdx_moe_gemm_combine", "tdx_norm_opts_default", "tdx_rmsnorm", "tdx_rmsnorm_bwd_workspace_size",
+            "tdx_rmsnorm_bwd", "tdx_route_opts_default", "tdx_moe_route", "tdx_moe_route_bwd",
+            "tdx_act_opts_default", "tdx_swiglu", "tdx_swiglu_bwd"]
 
 
 class tdx_opts(ctypes.Structure):
@@ -53,6 +57,40 @@ class tdx_opts(ctypes.Structure):
     ]
 
 
+class tdx_norm_opts(ctypes.Structure):
+    _fields_ = [
+        ("out_dtype", ctypes.c_int),
+        ("eps", ctypes.c_float),
+        ("out_scale", ctypes.c_float),
+        ("ld_x", ctypes.c_int64),
+        ("ld_residual", ctypes.c_int64),
+        ("ld_h", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64),
+    ]
+
+
+class tdx_route_opts(ctypes.Structure):
+    _fields_ = [
+        ("score", ctypes.c_int),
+        ("n_group", ctypes.c_int),
+        ("topk_group", ctypes.c_int),
+        ("group_top", ctypes.c_int),
+        ("renorm", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("ld_logits", ctypes.c_int64),
+    ]
+
+
+class tdx_act_opts(ctypes.Structure):
+    _fields_ = [
+        ("out_dtype", ctypes.c_int),
+        ("out_scale", ctypes.c_float),
+        ("topk", ctypes.c_int),
+        ("ld_y", ctypes.c_int64),
+        ("ld_out", ctypes.c_int64),
+    ]
+
+
 class TdxError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -66,6 +104,7 @@ def _load():
     P, I, U32, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32, ctypes.c_size_t
     PP = ctypes.POINTER(ctypes.c_void_p)
     OP = ctypes.POINTER(tdx_opts)
+    NP, RP, AP = ctypes.POINTER(tdx_norm_opts), ctypes.POINTER(tdx_route_opts), ctypes.POINTER(tdx_act_opts)
     sig = {
         "tdx_opts_default": (I, [OP]),
         "tdx_workspace_size": (I, [I, I, I, I, I, I, OP, ctypes.POINTER(SZ)]),
@@ -85,6 +124,16 @@ def _load():
         "tdx_moe_combine_workspace_size": (I, [I, I, I, I, I, I, I, OP, ctypes.POINTER(SZ)]),
         "tdx_moe_combine_plan_info": (I, [I, I, I, I, I, I, I, OP, ctypes.POINTER(ctypes.c_int64)]),
         "tdx_moe_gemm_combine": (I, [P, PP, P, PP, PP, P, SZ, I, I, I, I, I, I, I, OP, P]),
+        "tdx_norm_opts_default": (I, [NP]),
+        "tdx_rmsnorm": (I, [P, P, P, P, P, P, P, I, I, I, NP, P]),
+        "tdx_rmsnorm_bwd_workspace_size": (I, [I, I, I, ctypes.POINTER(SZ)]),
+        "tdx_rmsnorm_bwd": (I, [P, P, P, P, P, P, P, P, SZ, I, I, I, NP, P]),
+        "tdx_route_opts_default": (I, [RP]),
+        "tdx_moe_route": (I, [P, P, P, P, P, I, I, I, I, RP, P]),
+        "tdx_moe_route_bwd": (I, [P, P, P, P, I, I, I, I, RP, P]),
+        "tdx_act_opts_default": (I, [AP]),
+        "tdx_swiglu": (I, [P, P, P, P, I, I, I, AP, P]),
+        "tdx_swiglu_bwd": (I, [P, P, P, I, I, I, AP, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -296,3 +345,81 @@ def tdx_moe_gemm_combine(Hd, topk_idx, B_experts, gates, out, workspace, W: int,
     return int(_lib.tdx_moe_gemm_combine(_ptr(Hd), _ptr_array(topk_idx), _ptr(B_experts), _ptr_array(gates),
                                          _ptr_array(out), _ptr(workspace), wsb, W, T, F, H, E, topk, dtype,
                                          _opts_ref(opts), _stream(stream)))
+
+
+# ------------------------------------------------- row-wise operators around the products
+def _fill_opts(o, default, kw):
+    default(ctypes.byref(o))
+    for k, v in kw.items():
+        if k not in {f[0] for f in o._fields_}:
+            raise TypeError(f"{type(o).__name__} has no field {k}")
+        setattr(o, k, v)
+    return o
+
+
+def make_norm_opts(**kw) -> tdx_norm_opts:
+    """A tdx_norm_opts filled with the library defaults, then the given fields."""
+    return _fill_opts(tdx_norm_opts(), _lib.tdx_norm_opts_default, kw)
+
+
+def make_route_opts(**kw) -> tdx_route_opts:
+    """A tdx_route_opts filled with the library defaults, then the given fields."""
+    return _fill_opts(tdx_route_opts(), _lib.tdx_route_opts_default, kw)
+
+
+def make_act_opts(**kw) -> tdx_act_opts:
+    """A tdx_act_opts filled with the library defaults, then the given fields."""
+    return _fill_opts(tdx_act_opts(), _lib.tdx_act_opts_default, kw)
+
+
+def tdx_norm_opts_default() -> tdx_norm_opts:
+    return make_norm_opts()
+
+
+def tdx_route_opts_default() -> tdx_route_opts:
+    return make_route_opts()
+
+
+def tdx_act_opts_default() -> tdx_act_opts:
+    return make_act_opts()
+
+
+def tdx_rmsnorm(x, residual, weight, h_out, y, row_scale, rstd, T: int, H: int, dtype: int, opts=None,
+                stream=None) -> int:
+    return _lib.tdx_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(h_out), _ptr(y), _ptr(row_scale), _ptr(rstd),
+                            T, H, dtype, opts, _stream(stream))
+
+
+def tdx_rmsnorm_bwd_workspace_size(T: int, H: int, dtype: int) -> int:
+    out = ctypes.c_size_t(0)
+    st = _lib.tdx_rmsnorm_bwd_workspace_size(T, H, dtype, ctypes.byref(out))
+    if st != TDX_OK:
+        raise TdxError(st, "tdx_rmsnorm_bwd_workspace_size")
+    return int(out.value)
+
+
+def tdx_rmsnorm_bwd(dy, h, weight, rstd, dres, dx, dweight, workspace, T: int, H: int, dtype: int, opts=None,
+                    stream=None, workspace_bytes: int | None = None) -> int:
+    wsb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    return _lib.tdx_rmsnorm_bwd(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dres), _ptr(dx), _ptr(dweight),
+                                _ptr(workspace), wsb, T, H, dtype, opts, _stream(stream))
+
+
+def tdx_moe_route(logits, bias, topk_idx, gates, counts, T: int, E: int, topk: int, dtype: int, opts=None,
+                  stream=None) -> int:
+    return _lib.tdx_moe_route(_ptr(logits), _ptr(bias), _ptr(topk_idx), _ptr(gates), _ptr(counts), T, E, topk, dtype,
+                              opts, _stream(stream))
+
+
+def tdx_moe_route_bwd(logits, topk_idx, dgates, dlogits, T: int, E: int, topk: int, dtype: int, opts=None,
+                      stream=None) -> int:
+    return _lib.tdx_moe_route_bwd(_ptr(logits), _ptr(topk_idx), _ptr(dgates), _ptr(dlogits), T, E, topk, dtype, opts,
+                                  _stream(stream))
+
+
+def tdx_swiglu(y, out, row_scale, dest, R: int, I: int, dtype: int, opts=None, stream=None) -> int:
+    return _lib.tdx_swiglu(_ptr(y), _ptr(out), _ptr(row_scale), _ptr(dest), R, I, dtype, opts, _stream(stream))
+
+
+def tdx_swiglu_bwd(y, dout, dy, R: int, I: int, dtype: int, opts=None, stream=None) -> int:
+    return _lib.tdx_swiglu_bwd(_ptr(y), _ptr(dout), _ptr(dy), R, I, dtype, opts, _stream(stream))

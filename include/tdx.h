@@ -1,7 +1,8 @@
 /*
  * tdx.h -- C ABI of the tile-pipelined collective+GEMM library (sm_103a): AllGather+GEMM,
- * GEMM+ReduceScatter, GEMM+AllReduce and the mixture-of-experts AllToAll dispatch + grouped GEMM
- * and grouped GEMM + combine.
+ * GEMM+ReduceScatter, GEMM+AllReduce, the mixture-of-experts AllToAll dispatch + grouped GEMM and
+ * grouped GEMM + combine, and the row-wise operators around these products (root-mean-square norm,
+ * routing to experts, gated SiLU, with their gradients).
  *
  * What the operations are. The Triton-distributed article on cronfeed.work ("Triton-distributed
  * is turning communication into compiler territory"), section "The first move was to expose the
@@ -320,6 +321,123 @@ tdx_status tdx_moe_gemm_combine(const void* Hd, const int32_t* const* topk_idx, 
 /* Plan of one combine call: the 16 words of tdx_moe_plan_info, [10] = Z, [13] and [14] set. */
 tdx_status tdx_moe_combine_plan_info(int W, int T, int F, int H, int E, int topk, tdx_dtype dtype,
                                      const tdx_opts* opts, int64_t* info);
+
+/* ---------------------------------------------------------------------------------------------
+ * The row-wise operators around the products: root-mean-square norm, routing to experts, gated
+ * SiLU, each with its gradient. They read one tensor per operand; W ranks whose tensors lie in one
+ * buffer, rank after rank, are one call on W*T rows. All arithmetic is fp32; every output is
+ * rounded once (RNE; e4m3 saturates at +-448). Except tdx_rmsnorm_bwd they need no workspace, and
+ * they record nothing in a device status word: ids and indexes read on the device are bounds-checked
+ * there. Rows of 0 elements are invalid; 0 rows launch nothing (tdx_rmsnorm_bwd still zeroes
+ * dweight). Row strides are in elements, 0 = dense; a stride below the row's length is
+ * TDX_ERR_INVALID_ARG. Unless said otherwise pointers are 16-byte aligned and rows and strides are
+ * multiples of 16 bytes (TDX_ERR_ALIGNMENT).
+ *
+ * Root-mean-square norm of x + residual:
+ *   h = x + residual (x alone if residual is NULL), rstd = 1 / sqrt(mean(h^2) + eps),
+ *   y = h * rstd * weight; the sum h is normalised before it is rounded to `dtype` for h_out.
+ *  x, residual, h_out  device, T x H of `dtype` (TDX_BF16 or TDX_FP32). residual optional; h_out (the
+ *             residual stream for the next layer) optional, only with residual. h_out may be x or
+ *             residual itself (same stride); otherwise outputs overlap no input.
+ *  weight     device, H of `dtype`.
+ *  y          device, T x H of opts->out_dtype (TDX_BF16, TDX_FP32 or TDX_FP8_E4M3).
+ *  row_scale  device, T fp32 (4-byte aligned), e4m3 output only: row t is stored as
+ *             y[t] / row_scale[t] with row_scale[t] = max|y[t]| / 448 (1 if that is 0). NULL: e4m3
+ *             output is y / opts->out_scale, one scale per tensor as the e4m3 products take it.
+ *  rstd       optional, T fp32 (4-byte aligned), for tdx_rmsnorm_bwd.
+ * A row holding a NaN or an infinity gives the NaNs the formula gives; others are not touched. */
+typedef struct tdx_norm_opts {
+  tdx_dtype out_dtype;       /* default TDX_BF16 */
+  float eps;                 /* default 1e-6; finite, >= 0 */
+  float out_scale;           /* default 1; finite, > 0 */
+  int64_t ld_x, ld_residual, ld_h, ld_y;   /* row strides (tdx_rmsnorm_bwd: ld_x of dy, ld_residual
+                                of dres, ld_h of h, ld_y of dx) */
+} tdx_norm_opts;
+tdx_status tdx_norm_opts_default(tdx_norm_opts* opts);
+tdx_status tdx_rmsnorm(const void* x, const void* residual, const void* weight, void* h_out, void* y,
+                       float* row_scale, float* rstd, int T, int H, tdx_dtype dtype,
+                       const tdx_norm_opts* opts, void* stream);
+
+/* Its gradient: with g = dy * weight and n = h * rstd,
+ *   dx = rstd * (g - n * mean(g * n)) + dres,   dweight = sum_t dy[t] * n[t].
+ * dx is the gradient of x and of residual alike; dres (optional) is the one that reaches h_out.
+ *  dy, h, dres, dx  device, T x H of `dtype`; dx may be dy or dres itself (same stride).
+ *  rstd       device, T fp32, as the forward call left it.
+ *  dweight    device, H fp32 (16-byte aligned), overwritten. Partial sums over rows are added in a
+ *             fixed order: the bits do not change from call to call.
+ *  workspace  tdx_rmsnorm_bwd_workspace_size() bytes, 256-byte aligned; needs no initialisation.
+ * H <= 32768 (TDX_ERR_UNSUPPORTED beyond). */
+tdx_status tdx_rmsnorm_bwd_workspace_size(int T, int H, tdx_dtype dtype, size_t* bytes);
+tdx_status tdx_rmsnorm_bwd(const void* dy, const void* h, const void* weight, const float* rstd,
+                           const void* dres, void* dx, float* dweight, void* workspace,
+                           size_t workspace_bytes, int T, int H, tdx_dtype dtype,
+                           const tdx_norm_opts* opts, void* stream);
+
+/* Routing of T tokens to topk of E experts, in the layout tdx_moe_dispatch_gemm and
+ * tdx_moe_gemm_combine read (T x topk int32 ids, T x topk fp32 gates).
+ *   score s = softmax(x) over the E logits of a row, or sigmoid(x) = 1 / (1 + exp(-x));
+ *   key = s + bias (the bias steers the choice only and has no gradient); softmax without a bias
+ *   compares the logits themselves, whose order is the same.
+ *   Groups: E / n_group consecutive experts form a group; its score is the largest key
+ *   (group_top 1) or the sum of the two largest (group_top 2; softmax without a bias: of
+ *   exp(x - max)); only the experts of the topk_group best groups remain.
+ *   The topk largest keys are taken in descending order; equal keys (and groups) go to the lowest
+ *   index; a NaN key comes after every other.
+ *   gate_j = scale * s_j / (renorm ? sum of the chosen s : 1), 0 where that sum is 0 or, with softmax
+ *   scores, the logits it runs over are all -inf.
+ * Every step up to the keys rounds to fp32 as written, so ids do not depend on the kernel.
+ *  logits     device, T x E of `dtype` (TDX_BF16 or TDX_FP32), aligned to the element, any stride.
+ *  bias       optional, E fp32 (4-byte aligned).
+ *  topk_idx   device, T x topk int32 (4-byte aligned); gates: T x topk fp32 (4-byte aligned).
+ *  counts     optional, E int32 (4-byte aligned): the number of tokens sent to each expert is ADDED
+ *             (for balancing the bias over the calls of a step; clear it when the step begins).
+ *  1 <= topk <= 16, topk <= topk_group * (E / n_group), E <= 512, n_group <= 32 dividing E. */
+typedef enum { TDX_SCORE_SOFTMAX = 0, TDX_SCORE_SIGMOID = 1 } tdx_score;
+typedef struct tdx_route_opts {
+  tdx_score score;           /* default TDX_SCORE_SOFTMAX */
+  int n_group, topk_group;   /* default 1, 1 (no groups) */
+  int group_top;             /* 1 or 2; default 1 */
+  int renorm;                /* default 1 */
+  float scale;               /* default 1; finite */
+  int64_t ld_logits;         /* row stride of logits (and, backwards, of dlogits) */
+} tdx_route_opts;
+tdx_status tdx_route_opts_default(tdx_route_opts* opts);
+tdx_status tdx_moe_route(const void* logits, const float* bias, int32_t* topk_idx, float* gates,
+                         int32_t* counts, int T, int E, int topk, tdx_dtype dtype,
+                         const tdx_route_opts* opts, void* stream);
+
+/* Its gradient: dlogits = the gradient of sum(gates * dgates) by the logits, the chosen ids held
+ * fixed (score, renorm and scale as in the forward call; groups and bias play no part). All of
+ * dlogits (T x E of `dtype`) is written. An id outside [0, E) contributes nothing. */
+tdx_status tdx_moe_route_bwd(const void* logits, const int32_t* topk_idx, const float* dgates,
+                             void* dlogits, int T, int E, int topk, tdx_dtype dtype,
+                             const tdx_route_opts* opts, void* stream);
+
+/* Gated SiLU between two products (the experts' or a dense block's):
+ *   out[r] = g * sigmoid(g) * u,  g = c * y[r][0 .. I), u = c * y[r][I .. 2I).
+ *  y          device, R x 2I of `dtype` (TDX_BF16 or TDX_FP32).
+ *  out        device, R x I of opts->out_dtype (TDX_BF16, TDX_FP32, or TDX_FP8_E4M3 stored as
+ *             out / opts->out_scale, the one scale an e4m3 product takes).
+ *  row_scale  optional, fp32 scales of the rows (c = 1 if NULL), for rows whose product was taken of
+ *             tokens scaled one by one (tdx_rmsnorm's row_scale). With opts->topk = 0 row r takes
+ *             row_scale[r]; with opts->topk = k the R rows are those of R / k tokens in the order of
+ *             dest (R int32, as tdx_moe_dispatch_gemm writes it): row dest[i] takes row_scale[i / k],
+ *             and a row that dest does not name is not written. Entries outside [0, R) are skipped.
+ *  dest       given exactly when opts->topk > 0. Both 4-byte aligned. */
+typedef struct tdx_act_opts {
+  tdx_dtype out_dtype;       /* default TDX_BF16 */
+  float out_scale;           /* default 1; finite, > 0 */
+  int topk;                  /* slots per token for row_scale and dest; default 0; divides R */
+  int64_t ld_y, ld_out;      /* row strides (backwards: of y and dy, and of dout) */
+} tdx_act_opts;
+tdx_status tdx_act_opts_default(tdx_act_opts* opts);
+tdx_status tdx_swiglu(const void* y, void* out, const float* row_scale, const int32_t* dest, int R,
+                      int I, tdx_dtype dtype, const tdx_act_opts* opts, void* stream);
+
+/* Its gradient (c = 1): dy[r] = { dout * u * s * (1 + g * (1 - s)), dout * g * s }, s = sigmoid(g).
+ *  y, dy      device, R x 2I of `dtype`; dy may be y itself. dout: R x I of `dtype`. */
+tdx_status tdx_swiglu_bwd(const void* y, const void* dout, void* dy, int R, int I, tdx_dtype dtype,
+                          const tdx_act_opts* opts, void* stream);
 
 /* Synchronise `stream`, then read the workspace's device status word into *out (TDX_OK, or the
  * first device-side error since tdx_workspace_init). If detail is not NULL it receives 8 words:
