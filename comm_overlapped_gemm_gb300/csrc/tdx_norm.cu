@@ -1,4 +1,6 @@
 // Root-mean-square norm of x + residual and its gradient (tdx_rmsnorm, tdx_rmsnorm_bwd).
+#include <algorithm>
+
 #include "tdx_rows.cuh"
 
 namespace tdx {
@@ -48,8 +50,98 @@ __device__ float block_reduce(float v, float* sm) {
   return r;
 }
 
-// One block per row: a pass for the sum of squares, a pass for the largest |y| where the row's scale
-// is wanted, a pass that stores.
+// A row held in registers, E of its elements per thread in 16-byte vectors: one read of x and residual,
+// one reduction for the sum of squares and (where the row's scale is wanted) max|h * weight|, whose
+// product with rstd is max|y|, one write of h and y.
+// kLanes 8, 16, 32: that many lanes of a warp per row (short rows; the reduction is shuffles alone); 0: a
+// block per row, whose reduction takes one barrier.
+// Bound by HBM: 32768 x 7168 bf16 with the residual 272 us (6.9 TB/s, a plain copy's rate 281), 1000000 x
+// 128 152 us (6.9 TB/s); with a warp per row of 128, half of its lanes idle, 200 us. 1024 x 7168 to
+// e4m3 with row scales takes 11.4 us of 7.7 (the launch's ramp and tail). Rows through a ring of cp.async
+// stages in shared memory, as the gradient takes them, came out slower here (311 us): the many
+// independent blocks keep more loads in flight than one block per SM does between two sums.
+template <typename T, typename O, int E, int kLanes>
+__global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E) tdx_rmsnorm_rows_kernel(const __grid_constant__ NormParams p) {
+  constexpr int N = kVec<T>;
+  constexpr int V = E / N;
+  __shared__ float2 sm[32];
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int width = kLanes ? kLanes : blockDim.x;                                       // threads of a row
+  const int at = (kLanes ? threadIdx.x % (kLanes ? kLanes : 1) : threadIdx.x) * N;      // the thread's first column
+  const int64_t t = kLanes ? static_cast<int64_t>(blockIdx.x) * (kThreads / (kLanes ? kLanes : 1)) +
+                                 threadIdx.x / (kLanes ? kLanes : 1)
+                           : blockIdx.x;
+  const int H = t < p.T ? p.H : 0;   // a row past the end takes part in the shuffles only
+  const T* x = static_cast<const T*>(p.x) + t * p.ld_x + at;
+  const T* r = static_cast<const T*>(p.residual) + t * p.ld_r + at;
+  const T* w = static_cast<const T*>(p.weight) + at;
+  T* h = static_cast<T*>(p.h) + t * p.ld_h + at;
+  O* y = static_cast<O*>(p.y) + t * p.ld_y + at;
+  uint4 qx[V], qr[V], qw[V];
+  float v[V][N];
+  griddep_wait();
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (at + i * width * N < H) {
+      qx[i] = __ldcs(reinterpret_cast<const uint4*>(x + i * width * N));
+      if (p.residual != nullptr) qr[i] = __ldcs(reinterpret_cast<const uint4*>(r + i * width * N));
+      qw[i] = *reinterpret_cast<const uint4*>(w + i * width * N);
+    }
+  }
+  const bool scaled = p.row_scale != nullptr;
+  float ss = 0.0f, m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (at + i * width * N < H) {
+      unpack(qx[i], v[i], T{});
+      if (p.residual != nullptr) {
+        float a[N];
+        unpack(qr[i], a, T{});
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[i][k] += a[k];
+        if (p.h != nullptr) store_vec(h + i * width * N, v[i]);
+      }
+      float g[N];
+      unpack(qw[i], g, T{});
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        ss = fmaf(v[i][k], v[i][k], ss);
+        v[i][k] *= g[k];
+        m = fmaxf(m, fabsf(v[i][k]));
+      }
+    }
+  }
+  ss = lanes_sum<kLanes ? kLanes : 32>(ss);
+  if (scaled) m = lanes_max<kLanes ? kLanes : 32>(m);
+  if (!kLanes) {
+    if (lane == 0) sm[warp] = make_float2(ss, m);
+    __syncthreads();
+    const float2 a = lane < width / 32 ? sm[lane] : make_float2(0.0f, 0.0f);
+    ss = warp_sum(a.x);
+    if (scaled) m = warp_max(a.y);
+  }
+  const float rstd = 1.0f / sqrtf(ss / static_cast<float>(p.H) + p.eps);
+  float inv = rstd * p.inv_scale;
+  if (scaled) {
+    m *= rstd;
+    const float s = m > 0.0f ? m / 448.0f : 1.0f;
+    inv = rstd / s;
+    if (at == 0 && H > 0) p.row_scale[t] = s;
+  }
+  if (at == 0 && H > 0 && p.rstd != nullptr) p.rstd[t] = rstd;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (at + i * width * N < H) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[i][k] *= inv;
+      store_vec(y + i * width * N, v[i]);
+    }
+  }
+}
+
+// Rows too long for that: one block per row, a pass for the sum of squares, a pass for the largest |y|
+// where the row's scale is wanted, a pass that stores; all but the first read the row from L1 / L2.
 template <typename T, typename O>
 __global__ void __launch_bounds__(kThreads) tdx_rmsnorm_kernel(const __grid_constant__ NormParams p) {
   constexpr int N = kVec<T>;
@@ -119,7 +211,150 @@ struct NormBwdParams {
   int64_t ld_dy, ld_h, ld_dres, ld_dx;
 };
 
-// A block takes rows b, b + grid, ... and adds up dy * n of its columns in shared memory.
+// Rows through a ring of kStages rows in shared memory, filled by cp.async: every thread copies the vectors
+// that it reads itself, so that the ring needs no barrier and the loads of the rows to come run on
+// through the row's sum. A thread keeps the sums of dweight of its E columns in registers over all its
+// rows and stores them once, [blocks][H] fp32 for tdx_rmsnorm_dweight_kernel. kLanes as above.
+// Bound by HBM (8 bytes an element in bf16 with dres): 16381 x 8192 157 us with the sums' second kernel
+// (6.8 TB/s, a plain copy's rate 161), 100001 x 1024 120 us (123), 8000 x 16384 161 us (157), 262144 x 128
+// 45 us (40). Ring depth 2 / 3 / 4 at 16381 x 8192: 158 (32 columns a thread) / 157 / 158 us. Two blocks of
+// 512 threads per SM, at 64 registers, spill: 223 us.
+template <typename T, int E, int kStages, int kMaxThreads, int kBlocks, int kLanes>
+__global__ void __launch_bounds__(kMaxThreads, kBlocks) tdx_rmsnorm_bwd_rows_kernel(const __grid_constant__ NormBwdParams p) {
+  constexpr int N = kVec<T>;
+  constexpr int V = E / N;
+  extern __shared__ uint4 ring[];   // [stage][dy, h, dres][vector][thread]
+  __shared__ float sm[2][16];
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kGroups = kLanes ? kThreads / (kLanes ? kLanes : 1) : 1;   // rows that a block has in hand
+  const int width = kLanes ? kLanes : blockDim.x;
+  const int group = kLanes ? threadIdx.x / (kLanes ? kLanes : 1) : 0;
+  const int at = (threadIdx.x - group * width) * N;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups + group;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+  const T* dy = static_cast<const T*>(p.dy) + at;
+  const T* h = static_cast<const T*>(p.h) + at;
+  const T* dr = static_cast<const T*>(p.dres) + at;
+  const bool res = p.dres != nullptr;
+  uint4* mine = ring + threadIdx.x;
+  const uint32_t dst = smem_u32(mine);
+  griddep_wait();
+  auto fetch = [&](int64_t t, int s) {
+    if (t < p.T) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (at + i * width * N < p.H) {
+          const uint32_t d = dst + (s * 3 * V + i) * blockDim.x * 16;
+          cp_async16(d, dy + t * p.ld_dy + i * width * N);
+          cp_async16(d + V * blockDim.x * 16, h + t * p.ld_h + i * width * N);
+          if (res) cp_async16(d + 2 * V * blockDim.x * 16, dr + t * p.ld_dres + i * width * N);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) fetch(first + s * step, s);
+  // 32 columns a thread and 512 threads: the weight waits in shared memory, behind the ring (in registers
+  // it spills: 8000 x 16384 226 against 161 us)
+  constexpr bool kWeightApart = kMaxThreads * E > 8192 && kLanes == 0;
+  uint4* const apart = mine + kStages * 3 * V * blockDim.x;
+  uint4 qw[V];
+  float acc[V][N];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    qw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (at + i * width * N < p.H) qw[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.weight) + at + i * width * N);
+    if (kWeightApart) apart[i * blockDim.x] = qw[i];
+#pragma unroll
+    for (int k = 0; k < N; ++k) acc[i][k] = 0.0f;
+  }
+  int s = 0, flip = 0;
+  float next_rstd = first < p.T ? p.rstd[first] : 0.0f;
+  // all groups of a warp go round as often as its first: their shuffles are shared
+  for (int64_t t = first; t - (kLanes ? group % (32 / (kLanes ? kLanes : 32)) : 0) < p.T; t += step) {
+    const float rstd = next_rstd;
+    next_rstd = t + step < p.T ? p.rstd[t + step] : 0.0f;
+    cp_async_wait<kStages - 1>();
+    uint4 qd[V], qh[V], qr[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (at + i * width * N < p.H && t < p.T) {
+        const uint4* q = mine + (s * 3 * V + i) * blockDim.x;
+        qd[i] = q[0];
+        qh[i] = q[V * blockDim.x];
+        if (res) qr[i] = q[2 * V * blockDim.x];
+      } else {
+        qd[i] = qh[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float d[N], v[N], g[N];
+      unpack(qd[i], d, T{});
+      unpack(qh[i], v, T{});
+      unpack(kWeightApart ? apart[i * blockDim.x] : qw[i], g, T{});
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float n = v[k] * rstd;
+        dot = fmaf(d[k] * g[k], n, dot);
+        acc[i][k] = fmaf(d[k], n, acc[i][k]);
+      }
+    }
+    fetch(t + kStages * step, s);   // the stage is read
+    dot = lanes_sum<kLanes ? kLanes : 32>(dot);
+    if (!kLanes) {
+      if (lane == 0) sm[flip][warp] = dot;
+      __syncthreads();
+      dot = warp_sum(lane < width / 32 ? sm[flip][lane] : 0.0f);
+      flip ^= 1;
+    }
+    const float mean = dot / static_cast<float>(p.H);
+    T* dx = static_cast<T*>(p.dx) + t * p.ld_dx + at;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (at + i * width * N < p.H && t < p.T) {
+        float d[N], v[N], g[N];
+        unpack(qd[i], d, T{});
+        unpack(qh[i], v, T{});
+        unpack(kWeightApart ? apart[i * blockDim.x] : qw[i], g, T{});
+#pragma unroll
+        for (int k = 0; k < N; ++k) d[k] = rstd * (d[k] * g[k] - v[k] * rstd * mean);
+        if (res) {
+          unpack(qr[i], v, T{});
+#pragma unroll
+          for (int k = 0; k < N; ++k) d[k] += v[k];
+        }
+        store_vec(dx + i * width * N, d);
+      }
+    }
+    s = s + 1 == kStages ? 0 : s + 1;
+  }
+  cp_async_wait<0>();
+  float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.H;
+  if (kLanes) {
+    // the groups' sums, added in the order of the groups
+    float* all = reinterpret_cast<float*>(ring);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (at + i * width * N < p.H) store_vec(all + group * p.H + at + i * width * N, acc[i]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.H; c += kThreads) {
+      float a = 0.0f;
+      for (int i = 0; i < kGroups; ++i) a += all[i * p.H + c];
+      out[c] = a;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (at + i * width * N < p.H) store_vec(out + at + i * width * N, acc[i]);
+  }
+}
+
+// Rows too long for the ring: a block takes rows b, b + grid, ... and adds up dy * n of its columns in shared memory.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) tdx_rmsnorm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
   constexpr int N = kVec<T>;
@@ -171,33 +406,115 @@ __global__ void __launch_bounds__(kThreads) tdx_rmsnorm_bwd_kernel(const __grid_
     for (int i = 0; i < N; ++i) out[c + i] = dw[c + i];
 }
 
-// dweight[c] = the partial sums of column c in the order of the row groups
-__global__ void __launch_bounds__(kThreads) tdx_rmsnorm_dweight_kernel(const float* part, float* dweight, int parts, int H) {
+// dweight[c] = the sum of column c's partial sums (5 MB at most up to H = 16384, in L2): warp w adds the row groups w, w + 32, ... of 64 columns,
+// the warps' sums follow in order.
+__global__ void __launch_bounds__(1024) tdx_rmsnorm_dweight_kernel(const float* part, float* dweight, int parts, int H) {
+  __shared__ float2 sm[32][33];
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 64 + lane * 2;
+  float2 a = make_float2(0.0f, 0.0f);
   griddep_wait();
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= H) return;
-  float s = 0.0f;
-  for (int b = 0; b < parts; ++b) s += part[static_cast<int64_t>(b) * H + c];
-  dweight[c] = s;
+  if (c < H) {
+#pragma unroll 10
+    for (int b = warp; b < parts; b += 32) {
+      const float2 v = *reinterpret_cast<const float2*>(part + static_cast<int64_t>(b) * H + c);
+      a.x += v.x;
+      a.y += v.y;
+    }
+  }
+  sm[warp][lane] = a;
+  __syncthreads();
+  if (warp == 0 && c < H) {
+    for (int i = 1; i < 32; ++i) {
+      a.x += sm[i][lane].x;
+      a.y += sm[i][lane].y;
+    }
+    *reinterpret_cast<float2*>(dweight + c) = a;
+  }
+}
+
+// Largest dynamic shared memory of a kernel, raised once per device (calls may come from several threads)
+template <typename K>
+bool raise_smem(K kernel, int bytes, std::atomic<bool>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_relaxed)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  return true;
+}
+
+template <typename T, typename O, int E, int kLanes>
+tdx_status launch_norm_lanes(const NormParams& p, cudaStream_t st) {
+  const int rows = kThreads / kLanes;
+  return launch_rows(tdx_rmsnorm_rows_kernel<T, O, E, kLanes>,
+                     static_cast<unsigned>((static_cast<int64_t>(p.T) + rows - 1) / rows), kThreads, 0, st, p);
+}
+
+template <typename T, typename O>
+tdx_status launch_norm_t(const NormParams& p, cudaStream_t st) {
+  if (p.H <= 64) return launch_norm_lanes<T, O, 8, 8>(p, st);
+  if (p.H <= 128) return launch_norm_lanes<T, O, 8, 16>(p, st);
+  if (p.H <= 256) return launch_norm_lanes<T, O, 8, 32>(p, st);
+  if (p.H <= 512) return launch_norm_lanes<T, O, 16, 32>(p, st);
+  if (p.H <= 1024) return launch_norm_lanes<T, O, 32, 32>(p, st);
+  if (p.H <= 16384) {
+    // up to one row per SM, 16 elements a thread shorten the row; beyond, 32 carry more loads per block:
+    // 1 x 8192 2.0 / 2.2 us, 32768 x 7168 293 / 272 us
+    auto block = [&](int e) { return static_cast<unsigned>((p.H + 32 * e - 1) / (32 * e) * 32); };
+    if (p.T <= sm_count()) return launch_rows(tdx_rmsnorm_rows_kernel<T, O, 16, 0>, p.T, block(16), 0, st, p);
+    return launch_rows(tdx_rmsnorm_rows_kernel<T, O, 32, 0>, p.T, block(32), 0, st, p);
+  }
+  return launch_rows(tdx_rmsnorm_kernel<T, O>, p.T, kThreads, 0, st, p);
 }
 
 template <typename T>
 tdx_status launch_norm(tdx_dtype out, const NormParams& p, cudaStream_t st) {
   switch (out) {
-    case TDX_BF16: return launch_rows(tdx_rmsnorm_kernel<T, bf16>, p.T, kThreads, 0, st, p);
-    case TDX_FP32: return launch_rows(tdx_rmsnorm_kernel<T, float>, p.T, kThreads, 0, st, p);
-    default: return launch_rows(tdx_rmsnorm_kernel<T, e4m3>, p.T, kThreads, 0, st, p);
+    case TDX_BF16: return launch_norm_t<T, bf16>(p, st);
+    case TDX_FP32: return launch_norm_t<T, float>(p, st);
+    default: return launch_norm_t<T, e4m3>(p, st);
   }
 }
 
+// Blocks per SM of the gradient's kernel, as many as its registers and shared memory leave room for
+constexpr int bwd_blocks(int H) { return H <= 256 ? 4 : H <= 512 ? 2 : H <= 1024 ? 1 : H <= 2048 ? 4 : H <= 4096 ? 2 : 1; }
+// Most row groups whose partial sums of dweight are added at the end: what the workspace holds
+constexpr int bwd_most_parts(int H) { return H <= 16384 ? 152 * bwd_blocks(H) : kBwdParts; }
+
+template <typename T, int E, int kStages, int kMaxThreads, int kBlocks, int kLanes>
+tdx_status launch_bwd_rows(const NormBwdParams& p, int* parts, cudaStream_t st) {
+  static std::atomic<bool> done[64];
+  // the ring, and the weight where a thread has 32 columns of a long row
+  constexpr int kRows = kStages * 3 + (kMaxThreads * E > 8192 && kLanes == 0 ? 1 : 0);
+  constexpr int kMost = kRows * E * static_cast<int>(sizeof(T)) * kMaxThreads;
+  const auto kernel = tdx_rmsnorm_bwd_rows_kernel<T, E, kStages, kMaxThreads, kBlocks, kLanes>;
+  if (kMost > 48 * 1024 && !raise_smem(kernel, kMost, done)) return TDX_ERR_CUDA;
+  const int block = kLanes ? kThreads : (p.H + 32 * E - 1) / (32 * E) * 32;
+  const int rows = kLanes ? kThreads / (kLanes ? kLanes : 1) : 1;
+  const int64_t want = (static_cast<int64_t>(p.T) + rows - 1) / rows;
+  const int most = std::min(bwd_most_parts(p.H), bwd_blocks(p.H) * (sm_count() > 0 ? sm_count() : kRefSMs));
+  *parts = static_cast<int>(want < most ? want : most);
+  return launch_rows(kernel, *parts, block, static_cast<size_t>(kRows) * E * sizeof(T) * block, st, p);
+}
+
 template <typename T>
-tdx_status launch_norm_bwd(const NormBwdParams& p, int grid, cudaStream_t st) {
+tdx_status launch_norm_bwd(const NormBwdParams& p, int* parts, cudaStream_t st) {
+  if (p.H <= 64) return launch_bwd_rows<T, 8, 2, kThreads, 4, 8>(p, parts, st);
+  if (p.H <= 128) return launch_bwd_rows<T, 8, 2, kThreads, 4, 16>(p, parts, st);
+  if (p.H <= 256) return launch_bwd_rows<T, 8, 2, kThreads, 4, 32>(p, parts, st);
+  if (p.H <= 512) return launch_bwd_rows<T, 16, 2, kThreads, 2, 32>(p, parts, st);
+  if (p.H <= 1024) return launch_bwd_rows<T, 32, 2, kThreads, 1, 32>(p, parts, st);
+  if (p.H <= 8192) return launch_bwd_rows<T, 16, sizeof(T) == 2 ? 3 : 2, 512, 1, 0>(p, parts, st);
+  if constexpr (sizeof(T) == 2) {
+    if (p.H <= 16384) return launch_bwd_rows<T, 32, 2, 512, 1, 0>(p, parts, st);
+  }
+  static std::atomic<bool> done[64];
   const size_t smem = static_cast<size_t>(p.H) * sizeof(float);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(tdx_rmsnorm_bwd_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           32768 * static_cast<int>(sizeof(float))) != cudaSuccess)
-    return TDX_ERR_CUDA;
-  return launch_rows(tdx_rmsnorm_bwd_kernel<T>, grid, kThreads, smem, st, p);
+  if (!raise_smem(tdx_rmsnorm_bwd_kernel<T>, 32768 * static_cast<int>(sizeof(float)), done)) return TDX_ERR_CUDA;
+  *parts = std::min(p.T, bwd_most_parts(p.H));
+  return launch_rows(tdx_rmsnorm_bwd_kernel<T>, *parts, kThreads, smem, st, p);
 }
 
 tdx_norm_opts norm_defaults() {
@@ -213,8 +530,6 @@ tdx_status check_sizes(int T, int H, tdx_dtype dtype) {
   if (T < 0 || H <= 0 || !known(dtype)) return TDX_ERR_INVALID_ARG;
   return dtype == TDX_FP8_E4M3 ? TDX_ERR_UNSUPPORTED : TDX_OK;
 }
-
-int bwd_parts(int T) { return T < kBwdParts ? T : kBwdParts; }
 
 }  // namespace
 }  // namespace tdx
@@ -271,7 +586,7 @@ tdx_status tdx_rmsnorm_bwd_workspace_size(int T, int H, tdx_dtype dtype, size_t*
   const tdx_status s = check_sizes(T, H, dtype);
   if (s != TDX_OK) return s;
   if (H > 32768) return TDX_ERR_UNSUPPORTED;
-  *bytes = static_cast<size_t>(T > 0 ? bwd_parts(T) : 1) * H * sizeof(float);
+  *bytes = static_cast<size_t>(T < 1 ? 1 : std::min(T, bwd_most_parts(H))) * H * sizeof(float);
   return TDX_OK;
 }
 
@@ -297,7 +612,7 @@ tdx_status tdx_rmsnorm_bwd(const void* dy, const void* h, const void* weight, co
     return TDX_ERR_ALIGNMENT;
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need) return TDX_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int parts = bwd_parts(T);
+  int parts = 0;
   float* part = static_cast<float*>(workspace);
   if (T > 0) {
     p.dy = dy;
@@ -309,10 +624,10 @@ tdx_status tdx_rmsnorm_bwd(const void* dy, const void* h, const void* weight, co
     p.part = part;
     p.T = T;
     p.H = H;
-    s = dtype == TDX_BF16 ? launch_norm_bwd<bf16>(p, parts, st) : launch_norm_bwd<float>(p, parts, st);
+    s = dtype == TDX_BF16 ? launch_norm_bwd<bf16>(p, &parts, st) : launch_norm_bwd<float>(p, &parts, st);
     if (s != TDX_OK) return s;
   }
-  return launch_rows(tdx_rmsnorm_dweight_kernel, (H + kThreads - 1) / kThreads, kThreads, 0, st,
+  return launch_rows(tdx_rmsnorm_dweight_kernel, (H + 63) / 64, 1024, 0, st,
                      static_cast<const float*>(part), dweight, parts, H);
 }
 

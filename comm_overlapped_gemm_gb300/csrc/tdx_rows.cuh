@@ -77,16 +77,21 @@ __device__ __forceinline__ void store_vec(e4m3* p, const float (&v)[4]) {
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(bf16 v) { return __bfloat162float(v); }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Sum and maximum over groups of L consecutive lanes (a power of two); every lane of the warp takes part
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
 }
+__device__ __forceinline__ float warp_sum(float v) { return lanes_sum<32>(v); }
+__device__ __forceinline__ float warp_max(float v) { return lanes_max<32>(v); }
 
 // ------------------------------------------------------------------------------------ host side
 // Launch with programmatic dependent launch: the grid may be scheduled before the stream's previous
