@@ -1,4 +1,6 @@
 // Routing of tokens to experts and its gradient (tdx_moe_route, tdx_moe_route_bwd).
+#include <algorithm>
+
 #include "tdx_rows.cuh"
 
 namespace tdx {
@@ -21,20 +23,239 @@ struct RouteParams {
   int sigmoid, renorm;
   float scale;
   int64_t ld;
+  int vector;        // rows may be read in the lanes' 8 or 16 bytes
+  int group_lanes;   // lanes per group
 };
 
-// 1 / (1 + exp(-x)), each step rounded to fp32 (no contraction of exp's last product into the sum)
-__device__ __forceinline__ float sigmoid_rn(float x) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x))); }
+// 1 / (1 + exp(-x)), each step rounded to fp32 (no contraction of exp's last product into the sum); the
+// correctly rounded reciprocal is the correctly rounded quotient
+__device__ __forceinline__ float sigmoid_rn(float x) { return __frcp_rn(__fadd_rn(1.0f, expf(-x))); }
 
 // Order-preserving image of a float: larger key, larger integer; NaN comes last (1), 0 is left for
 // "taken or not in a chosen group". -0 counts as +0.
 __device__ __forceinline__ uint32_t ordered(float f) {
-  if (f != f) return 1u;
   const uint32_t u = __float_as_uint(__fadd_rn(f, 0.0f));
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t o = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  return f != f ? 1u : o;
+}
+__device__ __forceinline__ float from_ordered(uint32_t o) {
+  return o <= 1u ? NAN : __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-// One warp per token; the row's scores and keys in shared memory, E floats each.
+// The score of a group from its two largest keys
+__device__ __forceinline__ uint32_t group_key(const RouteParams& p, uint32_t k1, uint32_t k2, bool two, float m) {
+  if (p.group_top == 1) return k1;
+  float a = from_ordered(k1), b = two ? from_ordered(k2) : 0.0f;
+  if (!p.sigmoid && p.bias == nullptr) {
+    a = expf(__fadd_rn(a, -m));
+    if (two) b = expf(__fadd_rn(b, -m));
+  }
+  return ordered(__fadd_rn(a, b));
+}
+
+// Gate of the lane's chosen expert (lane j < k: the j-th) and the row's outputs. `v`: its score s where the
+// scores are sigmoids, else its logit; m, sum: the row's softmax, used where gates are not renormalised.
+__device__ __forceinline__ void finish_row(const RouteParams& p, int64_t t, int lane, int id, float v, float m, float sum,
+                                           bool nan, int* hist) {
+  const bool on = lane < p.k;
+  float s, den = 1.0f;
+  if (p.sigmoid) {
+    s = on ? v : 0.0f;
+    if (p.renorm) den = lanes_sum<16>(s);
+  } else {
+    // renormalised softmax is the softmax over the chosen logits, taken from their own maximum
+    if (!on) v = -INFINITY;
+    const float top = p.renorm ? lanes_max<16>(v) : m;
+    s = top == -INFINITY ? 0.0f : expf(v - top);
+    den = p.renorm ? lanes_sum<16>(s) : sum;
+  }
+  float g = s == 0.0f ? 0.0f : s / den * p.scale;
+  if (nan) g = NAN;
+  if (on) {
+    p.idx[t * p.k + lane] = id;
+    p.gates[t * p.k + lane] = g;
+    if (p.counts != nullptr) atomicAdd(hist + id, 1);
+  }
+}
+
+// Load the lane's V consecutive logits (columns lane * V on), -inf past the end; `vector`: in words of the
+// lane's bytes, 16 at most.
+template <typename T, int V>
+__device__ __forceinline__ void load_logits(const T* x, int lane, int E, bool vector, float (&v)[V]) {
+  constexpr int kBytes = V * static_cast<int>(sizeof(T));
+  const int c = lane * V;
+  if (vector && c < E) {
+    if constexpr (kBytes >= 16) {
+      constexpr int N = kVec<T>;
+#pragma unroll
+      for (int i = 0; i < V; i += N) {
+        float w[N];
+        load_vec(x + c + i, w);
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[i + k] = w[k];
+      }
+      return;
+    } else if constexpr (V > 1) {
+      constexpr int kWords = kBytes / 4;   // 1 or 2
+      uint32_t w[kWords];
+      if constexpr (kWords == 2) {
+        const uint2 q = *reinterpret_cast<const uint2*>(x + c);
+        w[0] = q.x;
+        w[1] = q.y;
+      } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(x + c);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
+        else v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = c + i < E ? to_float(x[c + i]) : -INFINITY;
+}
+
+// One warp per token, V consecutive experts per lane, everything in registers. A lane knows the two best
+// of its keys (and finds further ones by another look at its V keys, which it seldom has to), so that
+// each of the k rounds is a warp maximum, the lowest lane that holds it (the lowest index: lanes hold
+// ascending experts), and that lane's step to its next key. Groups are aligned runs of lanes.
+// Bound by issue slots: the ids have to be those of the definition, so that every sigmoid is an
+// expf and a correctly rounded reciprocal.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_kernel(const __grid_constant__ RouteParams p) {
+  extern __shared__ int hist[];   // [E], only where counts are wanted
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = p.E, c0 = lane * V;
+  griddep_wait();
+  if (p.counts != nullptr) {
+    for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
+    __syncthreads();
+  }
+  float bias[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) bias[i] = p.bias != nullptr && c0 + i < E ? p.bias[c0 + i] : 0.0f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  float x[V], next[V];
+  if (t < p.T) load_logits<T, V>(static_cast<const T*>(p.logits) + t * p.ld, lane, E, p.vector, next);
+  for (; t < p.T; t += step) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = next[i];
+    const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+    if (t + step < p.T) load_logits<T, V>(row + step * p.ld, lane, E, p.vector, next);
+    bool nan = false;
+    float m = -INFINITY, sum = 1.0f;
+    uint32_t key[V];
+    if (p.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float s = sigmoid_rn(x[i]);
+        if (p.bias != nullptr) s = __fadd_rn(s, bias[i]);
+        key[i] = ordered(s);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        m = fmaxf(m, x[i]);
+        nan |= x[i] != x[i];
+        key[i] = ordered(x[i]);
+      }
+      nan = __any_sync(kAll, nan);
+      m = warp_max(m);
+      if (!p.renorm || p.bias != nullptr) {
+        float e[V];
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          e[i] = expf(__fadd_rn(x[i], -m));
+          if (c0 + i < E) sum += e[i];
+        }
+        sum = warp_sum(sum);
+        if (p.bias != nullptr) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) key[i] = ordered(__fadd_rn(__fdiv_rn(e[i], sum), bias[i]));
+        }
+      }
+    }
+    // the lane's two best keys a >= b and their experts
+    uint32_t a = 0, b = 0;
+    int ai = 0, bi = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint32_t k = c0 + i < E ? key[i] : 0u;
+      const bool first = k > a, second = k > b;
+      bi = first ? ai : second ? c0 + i : bi;
+      b = max(b, min(a, k));
+      ai = first ? c0 + i : ai;
+      a = max(a, k);
+    }
+    if (p.n_group > 1) {
+      // a group's run of lanes shares its two best keys; a group is chosen if fewer than topk_group come
+      // before it, each lane of the run comparing a part of the groups
+      const int run = p.group_lanes;
+      uint32_t k1 = a, k2 = b;
+      for (int o = 1; o < run; o <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(kAll, k1, o), o2 = __shfl_xor_sync(kAll, k2, o);
+        k2 = max(min(k1, o1), max(k2, o2));
+        k1 = max(k1, o1);
+      }
+      const uint32_t mine = group_key(p, k1, k2, E > p.n_group, m);
+      const int g = lane / run;
+      int before = 0;
+      for (int o = 0; o < p.n_group; o += run) {
+        const int other = o + lane - g * run;
+        const uint32_t k = __shfl_sync(kAll, mine, other * run);
+        if (other < p.n_group && (k > mine || (k == mine && other < g))) ++before;
+      }
+      for (int o = 1; o < run; o <<= 1) before += __shfl_xor_sync(kAll, before, o);
+      if (g >= p.n_group || before >= p.topk_group) a = b = 0;
+    }
+    int id = 0;
+    uint32_t got = 0;   // lane j: the j-th expert and its key
+    for (int j = 0; j < p.k; ++j) {
+      const uint32_t top = __reduce_max_sync(kAll, a);
+      const int src = __ffs(__ballot_sync(kAll, a == top)) - 1;
+      const int e = __shfl_sync(kAll, ai, src);
+      if (lane == j) {
+        id = e;
+        got = top;
+      }
+      if (lane == src) {
+        a = b;
+        ai = bi;
+        b = 0;
+        if (V > 2 && a == 0) {
+          // both are taken: the best of those that come after the one just taken
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const uint32_t k = c0 + i < E ? key[i] : 0u;
+            if ((k < top || (k == top && c0 + i > e)) && k > a) {
+              a = k;
+              ai = c0 + i;
+            }
+          }
+        }
+      }
+    }
+    float v = from_ordered(got);
+    if (p.bias != nullptr && lane < p.k) {
+      v = to_float(row[id]);
+      if (p.sigmoid) v = sigmoid_rn(v);
+    }
+    finish_row(p, t, lane, id, v, m, sum, nan, hist);
+  }
+  if (p.counts != nullptr) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kThreads)
+      if (hist[e] > 0) atomicAdd(p.counts + e, hist[e]);
+  }
+}
+
+// Groups that are no aligned runs of lanes: one warp per token with the row's scores and keys in shared
+// memory, E floats each.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) tdx_moe_route_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ float sm[];
@@ -42,7 +263,13 @@ __global__ void __launch_bounds__(kThreads) tdx_moe_route_kernel(const __grid_co
   const int E = p.E;
   float* score = sm + warp * 2 * E;
   uint32_t* key = reinterpret_cast<uint32_t*>(score + E);
+  int* hist = reinterpret_cast<int*>(sm + kWarps * 2 * E);   // [E], only where counts are wanted
+  griddep_launch_dependents();
   griddep_wait();
+  if (p.counts != nullptr) {
+    for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
+    __syncthreads();
+  }
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.T;
        t += static_cast<int64_t>(gridDim.x) * kWarps) {
     const T* x = static_cast<const T*>(p.logits) + t * p.ld;
@@ -77,30 +304,15 @@ __global__ void __launch_bounds__(kThreads) tdx_moe_route_kernel(const __grid_co
     if (p.n_group > 1) {
       // lane g scores group g; a group is chosen if fewer than topk_group groups come before it
       const int per = E / p.n_group;
-      float gs = -INFINITY;
       uint32_t gk = 0;
       if (lane < p.n_group) {
         uint32_t k1 = 0, k2 = 0;
         for (int i = 0; i < per; ++i) {
           const uint32_t k = key[lane * per + i];
-          if (k > k1) {
-            k2 = k1;
-            k1 = k;
-          } else if (k > k2) {
-            k2 = k;
-          }
+          k2 = max(k2, min(k1, k));
+          k1 = max(k1, k);
         }
-        gk = k1;
-        if (p.group_top == 2) {
-          auto back = [](uint32_t k) { return k == 1u ? NAN : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); };
-          float a = back(k1), b = per > 1 ? back(k2) : 0.0f;
-          if (!p.sigmoid && p.bias == nullptr) {
-            a = expf(__fadd_rn(a, -m));
-            b = per > 1 ? expf(__fadd_rn(b, -m)) : 0.0f;
-          }
-          gs = __fadd_rn(a, b);
-          gk = ordered(gs);
-        }
+        gk = group_key(p, k1, k2, per > 1, m);
       }
       int before = 0;
       for (int g = 0; g < p.n_group; ++g) {
@@ -127,26 +339,13 @@ __global__ void __launch_bounds__(kThreads) tdx_moe_route_kernel(const __grid_co
       if (lane == 0) key[e] = 0;
       __syncwarp();
     }
-    const bool on = lane < p.k;
-    float s = 0.0f, den = 1.0f;
-    if (p.sigmoid) {
-      s = on ? score[mine] : 0.0f;
-      if (p.renorm) den = warp_sum(s);
-    } else {
-      // renormalised softmax is the softmax over the chosen logits, taken from their own maximum
-      const float v = on ? score[mine] : -INFINITY;
-      const float top = p.renorm ? warp_max(v) : m;
-      s = top == -INFINITY ? 0.0f : expf(v - top);
-      den = p.renorm ? warp_sum(s) : sum;
-    }
-    float g = s == 0.0f ? 0.0f : s / den * p.scale;
-    if (nan) g = NAN;
-    if (on) {
-      p.idx[t * p.k + lane] = mine;
-      p.gates[t * p.k + lane] = g;
-      if (p.counts != nullptr) atomicAdd(p.counts + mine, 1);
-    }
+    finish_row(p, t, lane, mine, lane < p.k ? score[mine] : 0.0f, m, sum, nan, hist);
     __syncwarp();
+  }
+  if (p.counts != nullptr) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kThreads)
+      if (hist[e] > 0) atomicAdd(p.counts + e, hist[e]);
   }
 }
 
@@ -245,10 +444,36 @@ tdx_status route_params(int T, int E, int topk, tdx_dtype dtype, const tdx_route
   return TDX_OK;
 }
 
-unsigned route_grid(int T) {
+unsigned route_grid(int T, int blocks_per_sm) {
   const int blocks = (T + kWarps - 1) / kWarps;
-  const int most = (sm_count() > 0 ? sm_count() : kRefSMs) * 8;
+  const int most = (sm_count() > 0 ? sm_count() : kRefSMs) * blocks_per_sm;
   return static_cast<unsigned>(blocks < most ? blocks : most);
+}
+
+template <typename T, int V>
+tdx_status launch_route_rows(RouteParams& p, cudaStream_t st) {
+  constexpr int kBytes = std::min(16, V * static_cast<int>(sizeof(T)));
+  p.vector = p.E % V == 0 && aligned(p.logits, kBytes) && (p.ld * static_cast<int64_t>(sizeof(T))) % kBytes == 0;
+  p.group_lanes = p.E / p.n_group / V;
+  return launch_rows(tdx_moe_route_rows_kernel<T, V>, route_grid(p.T, V <= 8 ? 4 : 2), kThreads,
+                     p.counts != nullptr ? p.E * sizeof(int) : 0, st, p);
+}
+
+template <typename T>
+tdx_status launch_route(RouteParams& p, cudaStream_t st) {
+  const int V = p.E <= 32 ? 1 : p.E <= 64 ? 2 : p.E <= 128 ? 4 : p.E <= 256 ? 8 : 16;
+  const int per = p.E / p.n_group;
+  if (p.n_group > 1 && (per % V != 0 || ((per / V) & (per / V - 1)) != 0)) {
+    const size_t smem = static_cast<size_t>(kWarps) * 2 * p.E * sizeof(float) + (p.counts != nullptr ? p.E * sizeof(int) : 0);
+    return launch_rows(tdx_moe_route_kernel<T>, route_grid(p.T, 8), kThreads, smem, st, p);
+  }
+  switch (V) {
+    case 1: return launch_route_rows<T, 1>(p, st);
+    case 2: return launch_route_rows<T, 2>(p, st);
+    case 4: return launch_route_rows<T, 4>(p, st);
+    case 8: return launch_route_rows<T, 8>(p, st);
+    default: return launch_route_rows<T, 16>(p, st);
+  }
 }
 
 }  // namespace
@@ -281,10 +506,8 @@ tdx_status tdx_moe_route(const void* logits, const float* bias, int32_t* topk_id
   p.idx = topk_idx;
   p.gates = gates;
   p.counts = counts;
-  const size_t smem = static_cast<size_t>(kWarps) * 2 * E * sizeof(float);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dtype == TDX_BF16 ? launch_rows(tdx_moe_route_kernel<bf16>, route_grid(T), kThreads, smem, st, p)
-                           : launch_rows(tdx_moe_route_kernel<float>, route_grid(T), kThreads, smem, st, p);
+  return dtype == TDX_BF16 ? launch_route<bf16>(p, st) : launch_route<float>(p, st);
 }
 
 tdx_status tdx_moe_route_bwd(const void* logits, const int32_t* topk_idx, const float* dgates, void* dlogits, int T,
@@ -303,8 +526,8 @@ tdx_status tdx_moe_route_bwd(const void* logits, const int32_t* topk_idx, const 
   p.dgates = dgates;
   p.dlogits = dlogits;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dtype == TDX_BF16 ? launch_rows(tdx_moe_route_bwd_kernel<bf16>, route_grid(T), kThreads, 0, st, p)
-                           : launch_rows(tdx_moe_route_bwd_kernel<float>, route_grid(T), kThreads, 0, st, p);
+  return dtype == TDX_BF16 ? launch_rows(tdx_moe_route_bwd_kernel<bf16>, route_grid(T, 8), kThreads, 0, st, p)
+                           : launch_rows(tdx_moe_route_bwd_kernel<float>, route_grid(T, 8), kThreads, 0, st, p);
 }
 
 }  // extern "C"
