@@ -24,7 +24,7 @@ struct RouteParams {
   float scale;
   int64_t ld;
   int vector;        // rows may be read in the lanes' 8 or 16 bytes
-  int group_lanes;   // lanes per group
+  int group_shift;   // log2 of the lanes per group
 };
 
 // 1 / (1 + exp(-x)), each step rounded to fp32 (no contraction of exp's last product into the sum); the
@@ -42,39 +42,55 @@ __device__ __forceinline__ float from_ordered(uint32_t o) {
   return o <= 1u ? NAN : __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-// The score of a group from its two largest keys
-__device__ __forceinline__ uint32_t group_key(const RouteParams& p, uint32_t k1, uint32_t k2, bool two, float m) {
-  if (p.group_top == 1) return k1;
-  float a = from_ordered(k1), b = two ? from_ordered(k2) : 0.0f;
+// The score of a group from its two largest keys (`two`: it has two; softmax without a bias adds exp(x - m))
+__device__ __forceinline__ uint32_t group_key(const RouteParams& p, float k1, float k2, bool two, float m) {
+  if (p.group_top == 1) return ordered(k1);
   if (!p.sigmoid && p.bias == nullptr) {
-    a = expf(__fadd_rn(a, -m));
-    if (two) b = expf(__fadd_rn(b, -m));
+    k1 = expf(__fadd_rn(k1, -m));
+    k2 = expf(__fadd_rn(k2, -m));
   }
-  return ordered(__fadd_rn(a, b));
+  return ordered(__fadd_rn(k1, two ? k2 : 0.0f));
 }
 
-// Gate of the lane's chosen expert (lane j < k: the j-th) and the row's outputs. `v`: its score s where the
-// scores are sigmoids, else its logit; m, sum: the row's softmax, used where gates are not renormalised.
-__device__ __forceinline__ void finish_row(const RouteParams& p, int64_t t, int lane, int id, float v, float m, float sum,
-                                           bool nan, int* hist) {
-  const bool on = lane < p.k;
-  float s, den = 1.0f;
-  if (p.sigmoid) {
-    s = on ? v : 0.0f;
-    if (p.renorm) den = lanes_sum<16>(s);
-  } else {
+// The outputs of a row held by L lanes, R chosen experts a lane: place sub + r * L of the choice in slot r.
+// v: the score s where scores are sigmoids, else the logit; m, sum: the row's softmax, used where gates are
+// not renormalised. The approximate exponential leaves a gate
+// within 2^-22 * (4 + |v - m|) of its value.
+template <int L, int R>
+__device__ __forceinline__ void finish_row(const RouteParams& p, int64_t t, int sub, bool write, const int (&id)[R],
+                                           float (&v)[R], float m, float sum, bool nan, int* hist) {
+  constexpr int kReach = L < 16 ? L : 16;   // lanes that can hold one of 16 places
+  float den = sum;
+  if (!p.sigmoid) {
     // renormalised softmax is the softmax over the chosen logits, taken from their own maximum
-    if (!on) v = -INFINITY;
-    const float top = p.renorm ? lanes_max<16>(v) : m;
-    s = top == -INFINITY ? 0.0f : expf(v - top);
-    den = p.renorm ? lanes_sum<16>(s) : sum;
+    float top = m;
+    if (p.renorm) {
+      top = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (sub + r * L < p.k) top = fmaxf(top, v[r]);
+      top = lanes_max<kReach>(top);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = top == -INFINITY ? 0.0f : __expf(v[r] - top);
   }
-  float g = s == 0.0f ? 0.0f : s / den * p.scale;
-  if (nan) g = NAN;
-  if (on) {
-    p.idx[t * p.k + lane] = id;
-    p.gates[t * p.k + lane] = g;
-    if (p.counts != nullptr) atomicAdd(hist + id, 1);
+  if (p.renorm) {
+    den = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (sub + r * L < p.k) den += v[r];
+    den = lanes_sum<kReach>(den);
+  } else if (p.sigmoid) {
+    den = 1.0f;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int j = sub + r * L;
+    if (write && j < p.k) {
+      p.idx[t * p.k + j] = id[r];
+      p.gates[t * p.k + j] = nan ? NAN : v[r] == 0.0f ? 0.0f : v[r] / den * p.scale;
+      if (p.counts != nullptr) atomicAdd(hist + id[r], 1);
+    }
   }
 }
 
@@ -117,236 +133,385 @@ __device__ __forceinline__ void load_logits(const T* x, int lane, int E, bool ve
   for (int i = 0; i < V; ++i) v[i] = c + i < E ? to_float(x[c + i]) : -INFINITY;
 }
 
-// One warp per token, V consecutive experts per lane, everything in registers. A lane knows the two best
-// of its keys (and finds further ones by another look at its V keys, which it seldom has to), so that
-// each of the k rounds is a warp maximum, the lowest lane that holds it (the lowest index: lanes hold
-// ascending experts), and that lane's step to its next key. Groups are aligned runs of lanes.
-// Bound by issue slots: the ids have to be those of the definition, so that every sigmoid is an
-// expf and a correctly rounded reciprocal.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_kernel(const __grid_constant__ RouteParams p) {
-  extern __shared__ int hist[];   // [E], only where counts are wanted
-  griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int E = p.E, c0 = lane * V;
-  griddep_wait();
-  if (p.counts != nullptr) {
-    for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
-    __syncthreads();
+// One row by one warp, from the definition's own steps: the row's scores and keys in shared memory, 2 E
+// floats. The rows that tdx_moe_route_rows_kernel cannot settle, and groups that are no aligned runs of
+// its lanes, come here.
+template <typename T>
+__device__ __noinline__ void route_row(const RouteParams& p, int64_t t, float* score, int* hist) {
+  const int lane = threadIdx.x & 31;
+  const int E = p.E;
+  uint32_t* key = reinterpret_cast<uint32_t*>(score + E);
+  const T* x = static_cast<const T*>(p.logits) + t * p.ld;
+  float m = -INFINITY, sum = 1.0f;
+  bool nan = false;
+  if (!p.sigmoid) {
+    for (int e = lane; e < E; e += 32) {
+      const float v = to_float(x[e]);
+      m = fmaxf(m, v);
+      nan |= v != v;
+    }
+    m = warp_max(m);
+    nan = __any_sync(kAll, nan);
+    sum = 0.0f;
+    for (int e = lane; e < E; e += 32) sum += expf(__fadd_rn(to_float(x[e]), -m));
+    sum = warp_sum(sum);
   }
-  float bias[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) bias[i] = p.bias != nullptr && c0 + i < E ? p.bias[c0 + i] : 0.0f;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  float x[V], next[V];
-  if (t < p.T) load_logits<T, V>(static_cast<const T*>(p.logits) + t * p.ld, lane, E, p.vector, next);
-  for (; t < p.T; t += step) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = next[i];
-    const T* row = static_cast<const T*>(p.logits) + t * p.ld;
-    if (t + step < p.T) load_logits<T, V>(row + step * p.ld, lane, E, p.vector, next);
-    bool nan = false;
-    float m = -INFINITY, sum = 1.0f;
-    uint32_t key[V];
+  for (int e = lane; e < E; e += 32) {
+    const float v = to_float(x[e]);
+    float s, k;
     if (p.sigmoid) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float s = sigmoid_rn(x[i]);
-        if (p.bias != nullptr) s = __fadd_rn(s, bias[i]);
-        key[i] = ordered(s);
-      }
+      s = sigmoid_rn(v);
+      k = p.bias ? __fadd_rn(s, p.bias[e]) : s;
     } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        m = fmaxf(m, x[i]);
-        nan |= x[i] != x[i];
-        key[i] = ordered(x[i]);
-      }
-      nan = __any_sync(kAll, nan);
-      m = warp_max(m);
-      if (!p.renorm || p.bias != nullptr) {
-        float e[V];
-        sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          e[i] = expf(__fadd_rn(x[i], -m));
-          if (c0 + i < E) sum += e[i];
-        }
-        sum = warp_sum(sum);
-        if (p.bias != nullptr) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) key[i] = ordered(__fadd_rn(__fdiv_rn(e[i], sum), bias[i]));
-        }
-      }
+      s = v;
+      k = p.bias ? __fadd_rn(__fdiv_rn(expf(__fadd_rn(v, -m)), sum), p.bias[e]) : v;
     }
-    // the lane's two best keys a >= b and their experts
-    uint32_t a = 0, b = 0;
-    int ai = 0, bi = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const uint32_t k = c0 + i < E ? key[i] : 0u;
-      const bool first = k > a, second = k > b;
-      bi = first ? ai : second ? c0 + i : bi;
-      b = max(b, min(a, k));
-      ai = first ? c0 + i : ai;
-      a = max(a, k);
-    }
-    if (p.n_group > 1) {
-      // a group's run of lanes shares its two best keys; a group is chosen if fewer than topk_group come
-      // before it, each lane of the run comparing a part of the groups
-      const int run = p.group_lanes;
-      uint32_t k1 = a, k2 = b;
-      for (int o = 1; o < run; o <<= 1) {
-        const uint32_t o1 = __shfl_xor_sync(kAll, k1, o), o2 = __shfl_xor_sync(kAll, k2, o);
-        k2 = max(min(k1, o1), max(k2, o2));
-        k1 = max(k1, o1);
-      }
-      const uint32_t mine = group_key(p, k1, k2, E > p.n_group, m);
-      const int g = lane / run;
-      int before = 0;
-      for (int o = 0; o < p.n_group; o += run) {
-        const int other = o + lane - g * run;
-        const uint32_t k = __shfl_sync(kAll, mine, other * run);
-        if (other < p.n_group && (k > mine || (k == mine && other < g))) ++before;
-      }
-      for (int o = 1; o < run; o <<= 1) before += __shfl_xor_sync(kAll, before, o);
-      if (g >= p.n_group || before >= p.topk_group) a = b = 0;
-    }
-    int id = 0;
-    uint32_t got = 0;   // lane j: the j-th expert and its key
-    for (int j = 0; j < p.k; ++j) {
-      const uint32_t top = __reduce_max_sync(kAll, a);
-      const int src = __ffs(__ballot_sync(kAll, a == top)) - 1;
-      const int e = __shfl_sync(kAll, ai, src);
-      if (lane == j) {
-        id = e;
-        got = top;
-      }
-      if (lane == src) {
-        a = b;
-        ai = bi;
-        b = 0;
-        if (V > 2 && a == 0) {
-          // both are taken: the best of those that come after the one just taken
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const uint32_t k = c0 + i < E ? key[i] : 0u;
-            if ((k < top || (k == top && c0 + i > e)) && k > a) {
-              a = k;
-              ai = c0 + i;
-            }
-          }
-        }
-      }
-    }
-    float v = from_ordered(got);
-    if (p.bias != nullptr && lane < p.k) {
-      v = to_float(row[id]);
-      if (p.sigmoid) v = sigmoid_rn(v);
-    }
-    finish_row(p, t, lane, id, v, m, sum, nan, hist);
+    score[e] = s;
+    key[e] = ordered(k);
   }
-  if (p.counts != nullptr) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kThreads)
-      if (hist[e] > 0) atomicAdd(p.counts + e, hist[e]);
+  __syncwarp();
+  if (p.n_group > 1) {
+    // lane g scores group g; a group is chosen if fewer than topk_group groups come before it
+    const int per = E / p.n_group;
+    uint32_t gk = 0;
+    if (lane < p.n_group) {
+      // NaN keys (1) come last: the two largest are NaN only where nothing else is there
+      uint32_t k1 = 0, k2 = 0;
+      for (int i = 0; i < per; ++i) {
+        const uint32_t k = key[lane * per + i];
+        k2 = max(k2, min(k1, k));
+        k1 = max(k1, k);
+      }
+      gk = group_key(p, from_ordered(k1), from_ordered(k2), per > 1, m);
+    }
+    int before = 0;
+    for (int g = 0; g < p.n_group; ++g) {
+      const uint32_t o = __shfl_sync(kAll, gk, g);
+      before += (o > gk || (o == gk && g < lane)) ? 1 : 0;
+    }
+    const unsigned keep = __ballot_sync(kAll, lane < p.n_group && before < p.topk_group);
+    for (int e = lane; e < E; e += 32)
+      if (!((keep >> (e / per)) & 1u)) key[e] = 0;
+    __syncwarp();
   }
+  int mine = 0;   // lane j: the j-th chosen expert
+  for (int j = 0; j < p.k; ++j) {
+    uint32_t best = 0;
+    int at = E;
+    for (int e = lane; e < E; e += 32)
+      if (key[e] > best) {
+        best = key[e];
+        at = e;
+      }
+    const uint32_t top = __reduce_max_sync(kAll, best);
+    const int e = static_cast<int>(__reduce_min_sync(kAll, best == top ? static_cast<uint32_t>(at) : kAll));
+    if (lane == j) mine = e;
+    if (lane == 0) key[e] = 0;
+    __syncwarp();
+  }
+  const int id[1] = {mine};
+  float v[1] = {lane < p.k ? score[mine] : 0.0f};
+  finish_row<32, 1>(p, t, lane, true, id, v, m, sum, nan, hist);
+  __syncwarp();
 }
 
-// Groups that are no aligned runs of lanes: one warp per token with the row's scores and keys in shared
-// memory, E floats each.
+// Shared memory of both kernels: 2 E floats per warp for route_row, then E counters where counts are wanted
+__device__ __forceinline__ int* clear_hist(const RouteParams& p, float* sm) {
+  int* hist = reinterpret_cast<int*>(sm + kWarps * 2 * p.E);
+  if (p.counts != nullptr) {
+    for (int e = threadIdx.x; e < p.E; e += kThreads) hist[e] = 0;
+    __syncthreads();
+  }
+  return hist;
+}
+__device__ __forceinline__ void add_hist(const RouteParams& p, const int* hist) {
+  if (p.counts == nullptr) return;
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kThreads)
+    if (hist[e] > 0) atomicAdd(p.counts + e, hist[e]);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) tdx_moe_route_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ float sm[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int E = p.E;
-  float* score = sm + warp * 2 * E;
-  uint32_t* key = reinterpret_cast<uint32_t*>(score + E);
-  int* hist = reinterpret_cast<int*>(sm + kWarps * 2 * E);   // [E], only where counts are wanted
+  const int warp = threadIdx.x >> 5;
   griddep_launch_dependents();
   griddep_wait();
-  if (p.counts != nullptr) {
-    for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
-    __syncthreads();
-  }
+  int* hist = clear_hist(p, sm);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.T;
-       t += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const T* x = static_cast<const T*>(p.logits) + t * p.ld;
+       t += static_cast<int64_t>(gridDim.x) * kWarps)
+    route_row<T>(p, t, sm + warp * 2 * p.E, hist);
+  add_hist(p, hist);
+}
+
+// Exchange so that a >= b
+__device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {
+  const uint32_t lo = min(a, b);
+  a = max(a, b);
+  b = lo;
+}
+// Sorting networks, descending: 5 exchanges for four words, 19 for eight; of sixteen the best eight, from two
+// sorted halves
+__device__ __forceinline__ void sort_words(uint32_t (&w)[4]) {
+  order(w[0], w[1]), order(w[2], w[3]), order(w[0], w[2]), order(w[1], w[3]), order(w[1], w[2]);
+}
+__device__ __forceinline__ void sort_words(uint32_t (&w)[8]) {
+  order(w[0], w[1]), order(w[2], w[3]), order(w[4], w[5]), order(w[6], w[7]);
+  order(w[0], w[2]), order(w[1], w[3]), order(w[4], w[6]), order(w[5], w[7]);
+  order(w[1], w[2]), order(w[5], w[6]), order(w[0], w[4]), order(w[3], w[7]);
+  order(w[1], w[5]), order(w[2], w[6]), order(w[1], w[4]), order(w[3], w[6]);
+  order(w[2], w[4]), order(w[3], w[5]), order(w[3], w[4]);
+}
+__device__ __forceinline__ void best_words(const uint32_t (&w)[4], uint32_t (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] = w[i];
+  sort_words(s);
+}
+__device__ __forceinline__ void best_words(const uint32_t (&w)[8], uint32_t (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = w[i];
+  sort_words(s);
+}
+__device__ __forceinline__ void best_words(const uint32_t (&w)[16], uint32_t (&s)[8]) {
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    s[i] = w[i];
+    h[i] = w[8 + i];
+  }
+  sort_words(s);
+  sort_words(h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = max(s[i], h[7 - i]);
+  order(s[0], s[4]), order(s[1], s[5]), order(s[2], s[6]), order(s[3], s[7]);
+  order(s[0], s[2]), order(s[1], s[3]), order(s[4], s[6]), order(s[5], s[7]);
+  order(s[0], s[1]), order(s[2], s[3]), order(s[4], s[5]), order(s[6], s[7]);
+}
+
+// L lanes per token, 32 / L tokens per warp, V consecutive experts per lane in registers; K >= topk.
+//
+// The choice is K + 1 maxima over the token's lanes of 32-bit words that hold a key's leading 32 - B bits
+// and below them the expert, B bits, counted backwards: all words differ, equal keys come in the order of
+// their experts, and a maximum names its expert, so that a round is a maximum and one lane's step to
+// the next word of its sorted list (the best eight of sixteen: a lane that runs out of them sends the row to
+// route_row). What the words leave open are keys that agree in their leading bits: inside the choice the
+// exact keys put them in order; at its end (the last expert taken and the first left out) the row goes
+// to route_row, as do rows with a NaN. bf16 logits that are compared as such fit into the leading bits.
+// Entries past E hold -inf: they come after everything that may be chosen.
+//
+// Bound by issue slots, not by HBM: ids have to be those of the definition, so that every sigmoid is
+// an expf and a correctly rounded reciprocal.
+template <typename T, int L, int V, int K>
+__global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_kernel(const __grid_constant__ RouteParams p) {
+  constexpr int kTokens = 32 / L;
+  constexpr int kLog = (V == 4 ? 2 : V == 8 ? 3 : 4) + (L == 8 ? 3 : L == 16 ? 4 : 5);
+  constexpr uint32_t kLow = (1u << kLog) - 1u;
+  constexpr int S = V < 8 ? V : 8;                // words of the sorted list
+  constexpr int R = K > L ? K / L : 1;            // places of the choice per lane
+  extern __shared__ float sm[];
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane % L, first = lane - sub;   // lane within the token's, and the token's first lane
+  const int E = p.E, c0 = sub * V;
+  const int run = 1 << p.group_shift, group = sub >> p.group_shift;
+  griddep_wait();
+  int* hist = clear_hist(p, sm);
+  const bool biased = p.bias != nullptr;
+  float bias[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) bias[i] = c0 + i >= E ? -INFINITY : biased ? p.bias[c0 + i] : 0.0f;
+  const bool exact_words = sizeof(T) == 2 && !p.sigmoid && !biased;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kTokens;
+  int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTokens + lane / L;
+  float next[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) next[i] = -INFINITY;
+  if (t < p.T) load_logits<T, V>(static_cast<const T*>(p.logits) + t * p.ld, sub, E, p.vector, next);
+  for (; t - lane / L < p.T; t += step) {
+    const bool live = t < p.T;
+    const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+    float f[V];   // logits, then keys
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = next[i];
+    if (t + step < p.T) load_logits<T, V>(row + step * p.ld, sub, E, p.vector, next);
     float m = -INFINITY, sum = 1.0f;
-    bool nan = false;
-    if (!p.sigmoid) {
-      for (int e = lane; e < E; e += 32) {
-        const float v = to_float(x[e]);
-        m = fmaxf(m, v);
-        nan |= v != v;
+    if (p.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = sigmoid_rn(f[i]);
+      if (biased) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = __fadd_rn(f[i], bias[i]);
       }
-      m = warp_max(m);
-      nan = __any_sync(kAll, nan);
-      sum = 0.0f;
-      for (int e = lane; e < E; e += 32) sum += expf(to_float(x[e]) - m);
-      sum = warp_sum(sum);
-    }
-    for (int e = lane; e < E; e += 32) {
-      const float v = to_float(x[e]);
-      float s, k;
-      if (p.sigmoid) {
-        s = sigmoid_rn(v);
-        k = p.bias ? __fadd_rn(s, p.bias[e]) : s;
-      } else {
-        s = v;
-        k = p.bias ? __fadd_rn(__fdiv_rn(expf(__fadd_rn(v, -m)), sum), p.bias[e]) : v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) m = fmaxf(m, f[i]);
+      m = lanes_max<L>(m);
+      if (biased) {
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          f[i] = expf(__fadd_rn(f[i], -m));
+          sum += f[i];
+        }
+        sum = lanes_sum<L>(sum);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = __fadd_rn(__fdiv_rn(f[i], sum), bias[i]);
+      } else if (!p.renorm) {
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum += __expf(f[i] - m);
+        sum = lanes_sum<L>(sum);
       }
-      score[e] = s;
-      key[e] = ordered(k);
     }
-    __syncwarp();
+    // a NaN among the keys (or +inf and -inf) shows in their sum
+    float any = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) any += f[i];
+    const unsigned odd = __ballot_sync(kAll, any != any);
+    bool slow = L == 32 ? odd != 0 : ((odd >> first) & ((1u << (L & 31)) - 1u)) != 0;
+    bool kept = true;
     if (p.n_group > 1) {
-      // lane g scores group g; a group is chosen if fewer than topk_group groups come before it
-      const int per = E / p.n_group;
-      uint32_t gk = 0;
-      if (lane < p.n_group) {
-        uint32_t k1 = 0, k2 = 0;
-        for (int i = 0; i < per; ++i) {
-          const uint32_t k = key[lane * per + i];
-          k2 = max(k2, min(k1, k));
-          k1 = max(k1, k);
-        }
-        gk = group_key(p, k1, k2, per > 1, m);
+      // a group's run of lanes shares its two best keys; a group is chosen if fewer than topk_group come
+      // before it, each lane of the run comparing a part of the groups
+      float k1 = -INFINITY, k2 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        k2 = fmaxf(k2, fminf(k1, f[i]));
+        k1 = fmaxf(k1, f[i]);
       }
+      for (int o = 1; o < run; o <<= 1) {
+        const float o1 = __shfl_xor_sync(kAll, k1, o), o2 = __shfl_xor_sync(kAll, k2, o);
+        k2 = fmaxf(fminf(k1, o1), fmaxf(k2, o2));
+        k1 = fmaxf(k1, o1);
+      }
+      const uint32_t mine = group_key(p, k1, k2, E > p.n_group, m);
       int before = 0;
-      for (int g = 0; g < p.n_group; ++g) {
-        const uint32_t o = __shfl_sync(kAll, gk, g);
-        before += (o > gk || (o == gk && g < lane)) ? 1 : 0;
+      for (int o = sub & (run - 1); o - (sub & (run - 1)) < p.n_group; o += run) {
+        const uint32_t k = __shfl_sync(kAll, mine, first + (o << p.group_shift));
+        if (o < p.n_group && (k > mine || (k == mine && o < group))) ++before;
       }
-      const unsigned keep = __ballot_sync(kAll, lane < p.n_group && before < p.topk_group);
-      for (int e = lane; e < E; e += 32)
-        if (!((keep >> (e / per)) & 1u)) key[e] = 0;
-      __syncwarp();
+      for (int o = 1; o < run; o <<= 1) before += __shfl_xor_sync(kAll, before, o);
+      kept = group < p.n_group && before < p.topk_group;
     }
-    int mine = 0;   // lane j: the j-th chosen expert
-    for (int j = 0; j < p.k; ++j) {
-      uint32_t best = 0;
-      int at = E;
-      for (int e = lane; e < E; e += 32)
-        if (key[e] > best) {
-          best = key[e];
-          at = e;
+    uint32_t best[S];
+    {
+      uint32_t w[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t u = __float_as_uint(__fadd_rn(f[i], 0.0f));   // -0 to +0
+        const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+        w[i] = (k & ~kLow) | (kLow - static_cast<uint32_t>(c0 + i));
+      }
+      best_words(w, best);
+    }
+    if (!kept) {
+#pragma unroll
+      for (int i = 0; i < S; ++i) best[i] = 0;
+    }
+    uint32_t got[R], left = 0;   // the words of the lane's places, and the first word left out
+#pragma unroll
+    for (int r = 0; r < R; ++r) got[r] = 0;
+    bool dry = false;
+#pragma unroll
+    for (int j = 0; j <= K; ++j) {
+      uint32_t top = best[0];
+      if constexpr (L == 32) {
+        top = __reduce_max_sync(kAll, top);
+      } else {
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+      }
+      if (j < K && sub == j % L) got[j < K ? j / L : 0] = top;
+      if (j == p.k) left = top;
+      if (best[0] == top) {
+#pragma unroll
+        for (int i = 0; i + 1 < S; ++i) best[i] = best[i + 1];
+        best[S - 1] = 0;
+        if (V > S) dry |= best[0] == 0 && top != 0;
+      }
+    }
+    if (V > S) slow |= __any_sync(kAll, dry);
+    // the exact keys, and what the gates are made of (the scores, or the logits)
+    int id[R];
+    float v[R];
+    uint32_t exact[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      id[r] = static_cast<int>(kLow - (got[r] & kLow));
+      v[r] = 0.0f;
+      exact[r] = 0;
+      if (live && !slow && sub + r * L < p.k) {
+        v[r] = to_float(row[id[r]]);
+        float k = v[r];
+        if (p.sigmoid) k = v[r] = sigmoid_rn(v[r]);
+        else if (biased) k = __fdiv_rn(expf(__fadd_rn(v[r], -m)), sum);
+        if (biased) k = __fadd_rn(k, p.bias[id[r]]);
+        exact[r] = ordered(k);
+      }
+    }
+    if (!exact_words) {
+      bool open = false;   // places whose next one agrees in the leading bits
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int j = sub + r * L;
+        uint32_t after = __shfl_sync(kAll, got[r], first + (sub + 1) % L);
+        if (R > 1 && r + 1 < R) {
+          const uint32_t over = __shfl_sync(kAll, got[r + 1 < R ? r + 1 : 0], first);
+          if (sub == L - 1) after = over;
         }
-      const uint32_t top = __reduce_max_sync(kAll, best);
-      const int e = static_cast<int>(__reduce_min_sync(kAll, best == top ? static_cast<uint32_t>(at) : kAll));
-      if (lane == j) mine = e;
-      if (lane == 0) key[e] = 0;
-      __syncwarp();
+        if (j == p.k - 1) {
+          after = left;
+          slow |= left != 0 && (got[r] ^ left) <= kLow;
+        }
+        open |= j < p.k && after != 0 && (got[r] ^ after) <= kLow;
+      }
+      const unsigned ends = __ballot_sync(kAll, slow);
+      slow = L == 32 ? ends != 0 : ((ends >> first) & ((1u << (L & 31)) - 1u)) != 0;
+      if (__any_sync(kAll, open)) {
+        // where each place's expert lies by its exact key, and who belongs into it
+        int place[R], to[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) place[r] = to[r] = 0;
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+          for (int j = 0; j < L && j + q * L < p.k; ++j) {
+            const uint32_t o = __shfl_sync(kAll, exact[q], first + j);
+            const int oid = __shfl_sync(kAll, id[q], first + j);
+#pragma unroll
+            for (int r = 0; r < R; ++r) place[r] += o > exact[r] || (o == exact[r] && oid < id[r]) ? 1 : 0;
+          }
+        int nid[R];
+        float nv[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          nid[r] = id[r];
+          nv[r] = v[r];
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+          for (int j = 0; j < L && j + q * L < p.k; ++j) {
+            const int at = __shfl_sync(kAll, place[q], first + j);
+            const int oid = __shfl_sync(kAll, id[q], first + j);
+            const float ov = __shfl_sync(kAll, v[q], first + j);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              if (at == sub + r * L) {
+                nid[r] = oid;
+                nv[r] = ov;
+              }
+          }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          id[r] = nid[r];
+          v[r] = nv[r];
+        }
+      }
     }
-    finish_row(p, t, lane, mine, lane < p.k ? score[mine] : 0.0f, m, sum, nan, hist);
-    __syncwarp();
+    finish_row<L, R>(p, t, sub, live && !slow, id, v, m, sum, false, hist);
+    for (unsigned rest = __ballot_sync(kAll, live && slow && sub == 0); rest != 0; rest &= rest - 1)
+      route_row<T>(p, __shfl_sync(kAll, t, __ffs(rest) - 1), sm + warp * 2 * E, hist);
   }
-  if (p.counts != nullptr) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kThreads)
-      if (hist[e] > 0) atomicAdd(p.counts + e, hist[e]);
-  }
+  add_hist(p, hist);
 }
 
 // One warp per token; lane j holds the j-th id and its coefficient.
@@ -444,36 +609,42 @@ tdx_status route_params(int T, int E, int topk, tdx_dtype dtype, const tdx_route
   return TDX_OK;
 }
 
-unsigned route_grid(int T, int blocks_per_sm) {
-  const int blocks = (T + kWarps - 1) / kWarps;
-  const int most = (sm_count() > 0 ? sm_count() : kRefSMs) * blocks_per_sm;
+// Blocks for T tokens, `each` of them per warp
+unsigned route_grid(int64_t T, int each, int blocks_per_sm) {
+  const int64_t blocks = (T + kWarps * each - 1) / (kWarps * each);
+  const int64_t most = static_cast<int64_t>(sm_count() > 0 ? sm_count() : kRefSMs) * blocks_per_sm;
   return static_cast<unsigned>(blocks < most ? blocks : most);
 }
 
-template <typename T, int V>
-tdx_status launch_route_rows(RouteParams& p, cudaStream_t st) {
+size_t route_smem(const RouteParams& p) {
+  return static_cast<size_t>(kWarps) * 2 * p.E * sizeof(float) + (p.counts != nullptr ? p.E * sizeof(int) : 0);
+}
+
+template <typename T, int L, int V, int K>
+tdx_status launch_route_k(RouteParams& p, cudaStream_t st) {
   constexpr int kBytes = std::min(16, V * static_cast<int>(sizeof(T)));
   p.vector = p.E % V == 0 && aligned(p.logits, kBytes) && (p.ld * static_cast<int64_t>(sizeof(T))) % kBytes == 0;
-  p.group_lanes = p.E / p.n_group / V;
-  return launch_rows(tdx_moe_route_rows_kernel<T, V>, route_grid(p.T, V <= 8 ? 4 : 2), kThreads,
-                     p.counts != nullptr ? p.E * sizeof(int) : 0, st, p);
+  for (int lanes = p.E / p.n_group / V; lanes > 1; lanes >>= 1) ++p.group_shift;
+  return launch_rows(tdx_moe_route_rows_kernel<T, L, V, K>, route_grid(p.T, 32 / L, V <= 8 ? 4 : 2),
+                     kThreads, route_smem(p), st, p);
+}
+
+template <typename T, int L, int V>
+tdx_status launch_route_v(RouteParams& p, cudaStream_t st) {
+  if (p.k <= 4) return launch_route_k<T, L, V, 4>(p, st);
+  return p.k <= 8 ? launch_route_k<T, L, V, 8>(p, st) : launch_route_k<T, L, V, 16>(p, st);
 }
 
 template <typename T>
 tdx_status launch_route(RouteParams& p, cudaStream_t st) {
-  const int V = p.E <= 32 ? 1 : p.E <= 64 ? 2 : p.E <= 128 ? 4 : p.E <= 256 ? 8 : 16;
+  const int V = p.E <= 32 ? 4 : p.E <= 256 ? 8 : 16;
   const int per = p.E / p.n_group;
-  if (p.n_group > 1 && (per % V != 0 || ((per / V) & (per / V - 1)) != 0)) {
-    const size_t smem = static_cast<size_t>(kWarps) * 2 * p.E * sizeof(float) + (p.counts != nullptr ? p.E * sizeof(int) : 0);
-    return launch_rows(tdx_moe_route_kernel<T>, route_grid(p.T, 8), kThreads, smem, st, p);
-  }
-  switch (V) {
-    case 1: return launch_route_rows<T, 1>(p, st);
-    case 2: return launch_route_rows<T, 2>(p, st);
-    case 4: return launch_route_rows<T, 4>(p, st);
-    case 8: return launch_route_rows<T, 8>(p, st);
-    default: return launch_route_rows<T, 16>(p, st);
-  }
+  if (p.n_group > 1 && (per % V != 0 || ((per / V) & (per / V - 1)) != 0))
+    return launch_rows(tdx_moe_route_kernel<T>, route_grid(p.T, 1, 8), kThreads, route_smem(p), st, p);
+  if (p.E <= 32) return launch_route_v<T, 8, 4>(p, st);
+  if (p.E <= 64) return launch_route_v<T, 8, 8>(p, st);
+  if (p.E <= 128) return launch_route_v<T, 16, 8>(p, st);
+  return p.E <= 256 ? launch_route_v<T, 32, 8>(p, st) : launch_route_v<T, 32, 16>(p, st);
 }
 
 }  // namespace
@@ -526,8 +697,8 @@ tdx_status tdx_moe_route_bwd(const void* logits, const int32_t* topk_idx, const 
   p.dgates = dgates;
   p.dlogits = dlogits;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dtype == TDX_BF16 ? launch_rows(tdx_moe_route_bwd_kernel<bf16>, route_grid(T, 8), kThreads, 0, st, p)
-                           : launch_rows(tdx_moe_route_bwd_kernel<float>, route_grid(T, 8), kThreads, 0, st, p);
+  return dtype == TDX_BF16 ? launch_rows(tdx_moe_route_bwd_kernel<bf16>, route_grid(T, 1, 8), kThreads, 0, st, p)
+                           : launch_rows(tdx_moe_route_bwd_kernel<float>, route_grid(T, 1, 8), kThreads, 0, st, p);
 }
 
 }  // extern "C"
