@@ -54,8 +54,8 @@ __device__ __forceinline__ uint32_t group_key(const RouteParams& p, float k1, fl
 
 // The outputs of a row held by L lanes, R chosen experts a lane: place sub + r * L of the choice in slot r.
 // v: the score s where scores are sigmoids, else the logit; m, sum: the row's softmax, used where gates are
-// not renormalised. The approximate exponential leaves a gate
-// within 2^-22 * (4 + |v - m|) of its value.
+// not renormalised. The approximate exponential and quotient leave a gate within 2^-22 * (4 + |v - m|) of its
+// value.
 template <int L, int R>
 __device__ __forceinline__ void finish_row(const RouteParams& p, int64_t t, int sub, bool write, const int (&id)[R],
                                            float (&v)[R], float m, float sum, bool nan, int* hist) {
@@ -88,7 +88,9 @@ __device__ __forceinline__ void finish_row(const RouteParams& p, int64_t t, int 
     const int j = sub + r * L;
     if (write && j < p.k) {
       p.idx[t * p.k + j] = id[r];
-      p.gates[t * p.k + j] = nan ? NAN : v[r] == 0.0f ? 0.0f : v[r] / den * p.scale;
+      // the approximate quotient, where the sum is no subnormal
+      const float q = den < 1e-37f ? v[r] / den : __fdividef(v[r], den);
+      p.gates[t * p.k + j] = nan ? NAN : v[r] == 0.0f ? 0.0f : q * p.scale;
       if (p.counts != nullptr) atomicAdd(hist + id[r], 1);
     }
   }
@@ -288,15 +290,24 @@ __device__ __forceinline__ void best_words(const uint32_t (&w)[16], uint32_t (&s
   order(s[0], s[1]), order(s[2], s[3]), order(s[4], s[5]), order(s[6], s[7]);
 }
 
+// Largest of L lanes' words
+template <int L>
+__device__ __forceinline__ uint32_t lanes_top(uint32_t w) {
+  if constexpr (L == 32) return __reduce_max_sync(kAll, w);
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) w = max(w, __shfl_xor_sync(kAll, w, o));
+  return w;
+}
+
 // L lanes per token, 32 / L tokens per warp, V consecutive experts per lane in registers; K >= topk.
 //
 // The choice is K + 1 maxima over the token's lanes of 32-bit words that hold a key's leading 32 - B bits
 // and below them the expert, B bits, counted backwards: all words differ, equal keys come in the order of
 // their experts, and a maximum names its expert, so that a round is a maximum and one lane's step to
 // the next word of its sorted list (the best eight of sixteen: a lane that runs out of them sends the row to
-// route_row). What the words leave open are keys that agree in their leading bits: inside the choice the
-// exact keys put them in order; at its end (the last expert taken and the first left out) the row goes
-// to route_row, as do rows with a NaN. bf16 logits that are compared as such fit into the leading bits.
+// route_row). What the words leave open are keys that agree in their leading bits: where neighbours do, the
+// exact keys of the choice and of the first word left out put them in order. Rows where the first two
+// left out agree with the last one taken go to route_row, as do rows with a NaN. bf16 logits that are compared as such fit into the leading bits.
 // Entries past E hold -inf: they come after everything that may be chosen.
 //
 // Bound by issue slots, not by HBM: ids have to be those of the definition, so that every sigmoid is
@@ -408,21 +419,14 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
 #pragma unroll
       for (int i = 0; i < S; ++i) best[i] = 0;
     }
-    uint32_t got[R], left = 0;   // the words of the lane's places, and the first word left out
+    uint32_t got[R], top = 0;   // the words of the lane's places
 #pragma unroll
     for (int r = 0; r < R; ++r) got[r] = 0;
     bool dry = false;
 #pragma unroll
     for (int j = 0; j <= K; ++j) {
-      uint32_t top = best[0];
-      if constexpr (L == 32) {
-        top = __reduce_max_sync(kAll, top);
-      } else {
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
-      }
+      top = lanes_top<L>(best[0]);
       if (j < K && sub == j % L) got[j < K ? j / L : 0] = top;
-      if (j == p.k) left = top;
       if (best[0] == top) {
 #pragma unroll
         for (int i = 0; i + 1 < S; ++i) best[i] = best[i + 1];
@@ -431,23 +435,29 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
       }
     }
     if (V > S) slow |= __any_sync(kAll, dry);
-    // the exact keys, and what the gates are made of (the scores, or the logits)
+    // the word of place j, K at most
+    auto word = [&](int j) {
+      uint32_t w = __shfl_sync(kAll, got[0], first + j % L);
+      if (R > 1) {
+        const uint32_t w1 = __shfl_sync(kAll, got[R - 1], first + j % L);
+        if (j >= L) w = w1;
+      }
+      return j == K ? top : w;
+    };
+    const uint32_t left = word(p.k);   // the first word left out
+    // what the gates are made of: the scores, or the logits
+    auto gate_score = [&](int e) {
+      const float x = to_float(row[e]);
+      if (!p.sigmoid) return x;
+      return x < -80.0f ? sigmoid_rn(x) : __fdividef(1.0f, 1.0f + __expf(-x));
+    };
     int id[R];
     float v[R];
-    uint32_t exact[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       id[r] = static_cast<int>(kLow - (got[r] & kLow));
       v[r] = 0.0f;
-      exact[r] = 0;
-      if (live && !slow && sub + r * L < p.k) {
-        v[r] = to_float(row[id[r]]);
-        float k = v[r];
-        if (p.sigmoid) k = v[r] = sigmoid_rn(v[r]);
-        else if (biased) k = __fdiv_rn(expf(__fadd_rn(v[r], -m)), sum);
-        if (biased) k = __fadd_rn(k, p.bias[id[r]]);
-        exact[r] = ordered(k);
-      }
+      if (live && !slow && sub + r * L < p.k) v[r] = gate_score(id[r]);
     }
     if (!exact_words) {
       bool open = false;   // places whose next one agrees in the leading bits
@@ -456,22 +466,43 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
         const int j = sub + r * L;
         uint32_t after = __shfl_sync(kAll, got[r], first + (sub + 1) % L);
         if (R > 1 && r + 1 < R) {
-          const uint32_t over = __shfl_sync(kAll, got[r + 1 < R ? r + 1 : 0], first);
+          const uint32_t over = __shfl_sync(kAll, got[R - 1], first);
           if (sub == L - 1) after = over;
         }
-        if (j == p.k - 1) {
-          after = left;
-          slow |= left != 0 && (got[r] ^ left) <= kLow;
-        }
+        if (j == p.k - 1) after = left;
         open |= j < p.k && after != 0 && (got[r] ^ after) <= kLow;
       }
-      const unsigned ends = __ballot_sync(kAll, slow);
-      slow = L == 32 ? ends != 0 : ((ends >> first) & ((1u << (L & 31)) - 1u)) != 0;
       if (__any_sync(kAll, open)) {
-        // where each place's expert lies by its exact key, and who belongs into it
-        int place[R], to[R];
+        // Put the places and the first word left out in order by their exact keys. Should the second
+        // word left out agree with it and with the last place, there may be more of them: route_row.
+        const uint32_t next_top = lanes_top<L>(best[0]);
+        const uint32_t second = p.k == K ? next_top : word(p.k + 1);
+        const uint32_t end = word(p.k - 1);
+        slow |= second != 0 && (end ^ left) <= kLow && (left ^ second) <= kLow;
+        auto exact_key = [&](int e) {
+          const float x = to_float(row[e]);
+          float k = x;
+          if (p.sigmoid) k = sigmoid_rn(x);
+          else if (biased) k = __fdiv_rn(expf(__fadd_rn(x, -m)), sum);
+          return ordered(biased ? __fadd_rn(k, p.bias[e]) : k);
+        };
+        const bool settle = live && !slow;
+        uint32_t exact[R], exact_left = 0;
+        const int id_left = static_cast<int>(kLow - (left & kLow));
+        float v_left = 0.0f;
+        if (settle && left != 0 && id_left < E) {
+          exact_left = exact_key(id_left);
+          v_left = gate_score(id_left);
+        }
+        int place[R], nid[R], place_left = 0;
+        float nv[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) place[r] = to[r] = 0;
+        for (int r = 0; r < R; ++r) {
+          exact[r] = settle && sub + r * L < p.k ? exact_key(id[r]) : 0u;
+          place[r] = exact_left > exact[r] || (exact_left == exact[r] && id_left < id[r]) ? 1 : 0;
+          nid[r] = id[r];
+          nv[r] = v[r];
+        }
 #pragma unroll
         for (int q = 0; q < R; ++q)
           for (int j = 0; j < L && j + q * L < p.k; ++j) {
@@ -479,14 +510,8 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
             const int oid = __shfl_sync(kAll, id[q], first + j);
 #pragma unroll
             for (int r = 0; r < R; ++r) place[r] += o > exact[r] || (o == exact[r] && oid < id[r]) ? 1 : 0;
+            place_left += o > exact_left || (o == exact_left && oid < id_left) ? 1 : 0;
           }
-        int nid[R];
-        float nv[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          nid[r] = id[r];
-          nv[r] = v[r];
-        }
 #pragma unroll
         for (int q = 0; q < R; ++q)
           for (int j = 0; j < L && j + q * L < p.k; ++j) {
@@ -502,8 +527,9 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
           }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          id[r] = nid[r];
-          v[r] = nv[r];
+          const bool take = place_left == sub + r * L;
+          id[r] = take ? id_left : nid[r];
+          v[r] = take ? v_left : nv[r];
         }
       }
     }
