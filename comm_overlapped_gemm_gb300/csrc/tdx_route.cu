@@ -25,6 +25,8 @@ struct RouteParams {
   int64_t ld;
   int vector;        // rows may be read in the lanes' 8 or 16 bytes
   int group_shift;   // log2 of the lanes per group
+  int per;           // experts per group
+  int warp_floats;   // shared memory of a warp
 };
 
 // 1 / (1 + exp(-x)), each step rounded to fp32 (no contraction of exp's last product into the sum); the
@@ -96,9 +98,10 @@ __device__ __forceinline__ void finish_row(const RouteParams& p, int64_t t, int 
   }
 }
 
-// Load the lane's V consecutive logits (columns lane * V on), -inf past the end; `vector`: in words of the
-// lane's bytes, 16 at most.
-template <typename T, int V>
+// Load V logits of a row held by L lanes, -inf past the end. `vector`: the lane's V consecutive ones (columns
+// lane * V on) in words of 16 bytes at most; else columns lane, lane + L, ..., so that odd row lengths
+// and addresses are read in whole lines too.
+template <typename T, int L, int V>
 __device__ __forceinline__ void load_logits(const T* x, int lane, int E, bool vector, float (&v)[V]) {
   constexpr int kBytes = V * static_cast<int>(sizeof(T));
   const int c = lane * V;
@@ -132,12 +135,12 @@ __device__ __forceinline__ void load_logits(const T* x, int lane, int E, bool ve
     }
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = c + i < E ? to_float(x[c + i]) : -INFINITY;
+  for (int i = 0; i < V; ++i) v[i] = !vector && lane + i * L < E ? to_float(x[lane + i * L]) : -INFINITY;
 }
 
 // One row by one warp, from the definition's own steps: the row's scores and keys in shared memory, 2 E
-// floats. The rows that tdx_moe_route_rows_kernel cannot settle, and groups that are no aligned runs of
-// its lanes, come here.
+// floats. The rows that tdx_moe_route_rows_kernel cannot settle, and groups that its lanes cannot hold (five of
+// 100 experts), come here.
 template <typename T>
 __device__ __noinline__ void route_row(const RouteParams& p, int64_t t, float* score, int* hist) {
   const int lane = threadIdx.x & 31;
@@ -217,9 +220,10 @@ __device__ __noinline__ void route_row(const RouteParams& p, int64_t t, float* s
   __syncwarp();
 }
 
-// Shared memory of both kernels: 2 E floats per warp for route_row, then E counters where counts are wanted
+// Shared memory of both kernels: p.warp_floats per warp (2 E for route_row, 32 V for the other's rows where
+// they are not read in vectors), then E counters where counts are wanted
 __device__ __forceinline__ int* clear_hist(const RouteParams& p, float* sm) {
-  int* hist = reinterpret_cast<int*>(sm + kWarps * 2 * p.E);
+  int* hist = reinterpret_cast<int*>(sm + kWarps * p.warp_floats);
   if (p.counts != nullptr) {
     for (int e = threadIdx.x; e < p.E; e += kThreads) hist[e] = 0;
     __syncthreads();
@@ -242,8 +246,21 @@ __global__ void __launch_bounds__(kThreads) tdx_moe_route_kernel(const __grid_co
   int* hist = clear_hist(p, sm);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.T;
        t += static_cast<int64_t>(gridDim.x) * kWarps)
-    route_row<T>(p, t, sm + warp * 2 * p.E, hist);
+    route_row<T>(p, t, sm + warp * p.warp_floats, hist);
   add_hist(p, hist);
+}
+
+// V consecutive values of a 16-byte aligned place in shared memory
+template <int V>
+__device__ __forceinline__ void read_lane(const float* from, float (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(from + i);
+    v[i] = q.x;
+    v[i + 1] = q.y;
+    v[i + 2] = q.z;
+    v[i + 3] = q.w;
+  }
 }
 
 // Exchange so that a >= b
@@ -308,7 +325,8 @@ __device__ __forceinline__ uint32_t lanes_top(uint32_t w) {
 // route_row). What the words leave open are keys that agree in their leading bits: where neighbours do, the
 // exact keys of the choice and of the first word left out put them in order. Rows where the first two
 // left out agree with the last one taken go to route_row, as do rows with a NaN. bf16 logits that are compared as such fit into the leading bits.
-// Entries past E hold -inf: they come after everything that may be chosen.
+// A group is a run of 2^n lanes (all of them where there are no groups); entries past its end hold -inf and
+// the word 0, which says that there is nothing.
 //
 // Bound by issue slots, not by HBM: ids have to be those of the definition, so that every sigmoid is
 // an expf and a correctly rounded reciprocal.
@@ -323,28 +341,42 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane % L, first = lane - sub;   // lane within the token's, and the token's first lane
-  const int E = p.E, c0 = sub * V;
-  const int run = 1 << p.group_shift, group = sub >> p.group_shift;
+  const int E = p.E, per = p.per;
+  const int run = 1 << p.group_shift, group = sub >> p.group_shift;   // lanes per group, and the lane's
+  const int within = (sub & (run - 1)) * V;                             // its first expert, counted in the group
+  const int c0 = group * per + within;
+  const bool holds = group < p.n_group && within < per;
   griddep_wait();
   int* hist = clear_hist(p, sm);
+  float* const stage = sm + warp * p.warp_floats;
   const bool biased = p.bias != nullptr;
   float bias[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) bias[i] = c0 + i >= E ? -INFINITY : biased ? p.bias[c0 + i] : 0.0f;
+  for (int i = 0; i < V; ++i) bias[i] = !holds || within + i >= per ? -INFINITY : biased ? p.bias[c0 + i] : 0.0f;
   const bool exact_words = sizeof(T) == 2 && !p.sigmoid && !biased;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kTokens;
   int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTokens + lane / L;
   float next[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) next[i] = -INFINITY;
-  if (t < p.T) load_logits<T, V>(static_cast<const T*>(p.logits) + t * p.ld, sub, E, p.vector, next);
+  if (t < p.T) load_logits<T, L, V>(static_cast<const T*>(p.logits) + t * p.ld, sub, E, p.vector, next);
   for (; t - lane / L < p.T; t += step) {
     const bool live = t < p.T;
     const T* row = static_cast<const T*>(p.logits) + t * p.ld;
     float f[V];   // logits, then keys
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = next[i];
-    if (t + step < p.T) load_logits<T, V>(row + step * p.ld, sub, E, p.vector, next);
+    if (!p.vector) {
+      // from every L-th column to consecutive ones
+      float* const token = stage + first * V;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < V; ++i) token[sub + i * L] = f[i];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = holds && within + i < per ? token[c0 + i] : -INFINITY;
+    }
+    if (t + step < p.T) load_logits<T, L, V>(row + step * p.ld, sub, E, p.vector, next);
     float m = -INFINITY, sum = 1.0f;
     if (p.sigmoid) {
 #pragma unroll
@@ -380,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
     for (int i = 0; i < V; ++i) any += f[i];
     const unsigned odd = __ballot_sync(kAll, any != any);
     bool slow = L == 32 ? odd != 0 : ((odd >> first) & ((1u << (L & 31)) - 1u)) != 0;
-    bool kept = true;
+    bool kept = holds;
     if (p.n_group > 1) {
       // a group's run of lanes shares its two best keys; a group is chosen if fewer than topk_group come
       // before it, each lane of the run comparing a part of the groups
@@ -395,14 +427,14 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
         k2 = fmaxf(fminf(k1, o1), fmaxf(k2, o2));
         k1 = fmaxf(k1, o1);
       }
-      const uint32_t mine = group_key(p, k1, k2, E > p.n_group, m);
+      const uint32_t mine = group_key(p, k1, k2, per > 1, m);
       int before = 0;
       for (int o = sub & (run - 1); o - (sub & (run - 1)) < p.n_group; o += run) {
         const uint32_t k = __shfl_sync(kAll, mine, first + (o << p.group_shift));
         if (o < p.n_group && (k > mine || (k == mine && o < group))) ++before;
       }
       for (int o = 1; o < run; o <<= 1) before += __shfl_xor_sync(kAll, before, o);
-      kept = group < p.n_group && before < p.topk_group;
+      kept &= before < p.topk_group;
     }
     uint32_t best[S];
     {
@@ -412,6 +444,11 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
         const uint32_t u = __float_as_uint(__fadd_rn(f[i], 0.0f));   // -0 to +0
         const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
         w[i] = (k & ~kLow) | (kLow - static_cast<uint32_t>(c0 + i));
+      }
+      if (!p.vector) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (within + i >= per) w[i] = 0;
       }
       best_words(w, best);
     }
@@ -490,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
         uint32_t exact[R], exact_left = 0;
         const int id_left = static_cast<int>(kLow - (left & kLow));
         float v_left = 0.0f;
-        if (settle && left != 0 && id_left < E) {
+        if (settle && left != 0) {
           exact_left = exact_key(id_left);
           v_left = gate_score(id_left);
         }
@@ -535,67 +572,193 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
     }
     finish_row<L, R>(p, t, sub, live && !slow, id, v, m, sum, false, hist);
     for (unsigned rest = __ballot_sync(kAll, live && slow && sub == 0); rest != 0; rest &= rest - 1)
-      route_row<T>(p, __shfl_sync(kAll, t, __ffs(rest) - 1), sm + warp * 2 * E, hist);
+      route_row<T>(p, __shfl_sync(kAll, t, __ffs(rest) - 1), stage, hist);
   }
   add_hist(p, hist);
 }
 
-// One warp per token; lane j holds the j-th id and its coefficient.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) tdx_moe_route_bwd_kernel(const __grid_constant__ RouteParams p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  griddep_wait();
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.T;
-       t += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const T* x = static_cast<const T*>(p.logits) + t * p.ld;
-    T* dx = static_cast<T*>(p.dlogits) + t * p.ld;
-    int id = lane < p.k ? p.idx[t * p.k + lane] : -1;
-    if (id >= p.E) id = -1;
-    const bool on = id >= 0;
-    const float v = on ? to_float(x[id]) : -INFINITY;
-    const float dg = on ? p.dgates[t * p.k + lane] * p.scale : 0.0f;
-    float m = -INFINITY, inv = 0.0f;   // dense softmax: p_e = exp(x_e - m) * inv
-    float d = 0.0f;                    // what the chosen expert receives
-    float dot = 0.0f;
-    const bool dense = !p.sigmoid && !p.renorm;
-    if (p.sigmoid) {
-      const float s = on ? 1.0f / (1.0f + expf(-v)) : 0.0f;
-      const float q = on ? 1.0f / (1.0f + expf(v)) : 0.0f;
-      float c = dg;
-      if (p.renorm) {
-        const float S = warp_sum(s);
-        c = S > 0.0f ? (dg - warp_sum(dg * s) / S) / S : 0.0f;
+// Store V values of a row of E where load_logits finds them
+template <typename T, int L, int V>
+__device__ __forceinline__ void store_logits(T* x, int lane, int E, bool vector, const float (&v)[V]) {
+  constexpr int kBytes = V * static_cast<int>(sizeof(T));
+  const int c = lane * V;
+  if (vector) {
+    if (c >= E) return;
+    if constexpr (kBytes >= 16) {
+      constexpr int N = kVec<T>;
+#pragma unroll
+      for (int i = 0; i < V; i += N) {
+        float w[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) w[k] = v[i + k];
+        store_vec(x + c + i, w);
       }
-      d = c * s * q;
-    } else if (p.renorm) {
-      m = warp_max(v);
-      const float e = on && m > -INFINITY ? expf(v - m) : 0.0f;
-      const float S = warp_sum(e);
-      const float g = S > 0.0f ? e / S : 0.0f;
-      d = g * (dg - warp_sum(dg * g));
     } else {
-      for (int e = lane; e < p.E; e += 32) m = fmaxf(m, to_float(x[e]));
-      m = warp_max(m);
+      static_assert(V == 4 && sizeof(T) == 2);
+      store_vec(x + c, v);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (lane + i * L < E) x[lane + i * L] = static_cast<T>(v[i]);
+}
+
+// L lanes per token, V consecutive experts per lane as forwards; slot r of a lane is the choice's place
+// sub + r * L. What a chosen expert's logit receives is scattered into a row of shared memory and read
+// back by the lanes that hold the row, so that dlogits are written in whole lines and softmax over the
+// whole row needs no look at the chosen logits. Choices of the same expert add up in the order of their places.
+// Bound by HBM and the launch: 4 E (softmax over the row: 8 E) bytes and 8 topk bytes a token.
+template <typename T, int L, int V>
+__global__ void __launch_bounds__(kThreads) tdx_moe_route_bwd_kernel(const __grid_constant__ RouteParams p) {
+  constexpr int kTokens = 32 / L;
+  constexpr int R = kMoeMaxTopk > L ? kMoeMaxTopk / L : 1;
+  __shared__ __align__(16) float rows[kWarps * 32 * V];
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane % L, first = lane - sub;
+  float* const row = rows + (warp * 32 + first) * V;
+  const int E = p.E;
+  const bool dense = !p.sigmoid && !p.renorm;
+  griddep_wait();
+  for (int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kTokens + lane / L; t - lane / L < p.T;
+       t += static_cast<int64_t>(gridDim.x) * kWarps * kTokens) {
+    const bool live = t < p.T;
+    const T* x = static_cast<const T*>(p.logits) + t * p.ld;
+    float e[V];   // softmax over the row: logits, then exponentials
+#pragma unroll
+    for (int i = 0; i < V; ++i) e[i] = -INFINITY;
+    if (dense && live) load_logits<T, L, V>(x, sub, E, p.vector, e);
+    int id[R];
+    float d[R], v[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int j = sub + r * L;
+      id[r] = -1;
+      d[r] = 0.0f;
+      v[r] = -INFINITY;
+      if (live && j < p.k) {
+        id[r] = p.idx[t * p.k + j];
+        if (id[r] < 0 || id[r] >= E) id[r] = -1;
+      }
+      if (id[r] >= 0) {
+        d[r] = p.dgates[t * p.k + j] * p.scale;
+        if (!dense) v[r] = to_float(x[id[r]]);
+      }
+    }
+    // d: what the chosen score receives, then (but for softmax over the row) what its logit does
+    float m = -INFINITY, inv = 0.0f;
+    if (p.sigmoid) {
+      float s[R], S = 0.0f, dot = 0.0f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        s[r] = id[r] >= 0 ? sigmoid_rn(v[r]) : 0.0f;
+        S += s[r];
+        dot += d[r] * s[r];
+      }
+      if (p.renorm) {
+        S = lanes_sum<L>(S);
+        dot = lanes_sum<L>(dot);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (p.renorm) d[r] = S > 0.0f ? (d[r] - dot / S) / S : S != S ? S : 0.0f;
+        d[r] = id[r] >= 0 ? d[r] * s[r] * sigmoid_rn(-v[r]) : 0.0f;
+      }
+    } else if (p.renorm) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) m = fmaxf(m, v[r]);
+      m = lanes_max<L>(m);
+      float S = 0.0f, dot = 0.0f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        v[r] = id[r] >= 0 && !(m == -INFINITY && v[r] == m) ? expf(v[r] - m) : 0.0f;
+        S += v[r];
+      }
+      S = lanes_sum<L>(S);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        v[r] = S == 0.0f ? 0.0f : v[r] / S;
+        dot += d[r] * v[r];
+      }
+      dot = lanes_sum<L>(dot);
+#pragma unroll
+      for (int r = 0; r < R; ++r) d[r] = v[r] * (d[r] - dot);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) m = fmaxf(m, e[i]);
+      m = lanes_max<L>(m);
       float S = 0.0f;
-      for (int e = lane; e < p.E; e += 32) S += expf(to_float(x[e]) - m);
-      S = warp_sum(S);
-      inv = m > -INFINITY ? 1.0f / S : 0.0f;
-      d = dg;
-      dot = warp_sum(on && inv > 0.0f ? dg * expf(v - m) * inv : 0.0f);
-    }
-    for (int base = 0; base < p.E; base += 32) {
-      const int e = base + lane;
-      float a = 0.0f;
-      for (int j = 0; j < p.k; ++j) {
-        const int ij = __shfl_sync(kAll, id, j);
-        const float dj = __shfl_sync(kAll, d, j);
-        if (ij == e) a += dj;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        e[i] = m == -INFINITY && e[i] == m ? 0.0f : __expf(e[i] - m);
+        S += e[i];
       }
-      if (e < p.E) {
-        if (dense) a = inv > 0.0f ? expf(to_float(x[e]) - m) * inv * (a - dot) : 0.0f;
-        dx[e] = static_cast<T>(a);
+      S = lanes_sum<L>(S);
+      inv = S == 0.0f ? 0.0f : 1.0f / S;
+    }
+#pragma unroll
+    for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(row + sub * V + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    __syncwarp();
+    // places that name one expert: the tag left there is another place's
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (id[r] >= 0) row[id[r]] = __int_as_float(sub + r * L);
+    __syncwarp();
+    bool twice = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) twice |= id[r] >= 0 && __float_as_int(row[id[r]]) != sub + r * L;
+    if (__any_sync(kAll, twice)) {
+      float add[R];
+      bool lead[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        add[r] = d[r];
+        lead[r] = true;
+      }
+#pragma unroll
+      for (int q = 0; q < R; ++q)
+        for (int j = 0; j < L; ++j) {
+          const int oid = __shfl_sync(kAll, id[q], first + j);
+          const float od = __shfl_sync(kAll, d[q], first + j);
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            if (oid == id[r] && oid >= 0) {
+              if (j + q * L < sub + r * L) lead[r] = false;
+              if (j + q * L > sub + r * L) add[r] += od;
+            }
+        }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        d[r] = add[r];
+        if (!lead[r]) id[r] = -1;
       }
     }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (id[r] >= 0) row[id[r]] = d[r];
+    __syncwarp();
+    float a[V];
+    if (p.vector) {
+      read_lane(row + sub * V, a);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) a[i] = row[sub + i * L];
+    }
+    if (dense) {
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        e[i] *= inv;
+        dot = fmaf(a[i], e[i], dot);
+      }
+      dot = lanes_sum<L>(dot);
+#pragma unroll
+      for (int i = 0; i < V; ++i) a[i] = e[i] * (a[i] - dot);
+    }
+    if (live) store_logits<T, L, V>(static_cast<T*>(p.dlogits) + t * p.ld, sub, E, p.vector, a);
+    __syncwarp();   // before the row is cleared
   }
 }
 
@@ -642,17 +805,27 @@ unsigned route_grid(int64_t T, int each, int blocks_per_sm) {
   return static_cast<unsigned>(blocks < most ? blocks : most);
 }
 
-size_t route_smem(const RouteParams& p) {
-  return static_cast<size_t>(kWarps) * 2 * p.E * sizeof(float) + (p.counts != nullptr ? p.E * sizeof(int) : 0);
+// log2 of the lanes that a group takes at V experts a lane
+int group_lanes_log(const RouteParams& p, int V) {
+  int log = 0;
+  while ((V << log) < p.per) ++log;
+  return log;
+}
+
+// Shared memory of a launch with at least `floats` per warp
+size_t route_smem(RouteParams* p, int floats) {
+  p->warp_floats = (std::max(2 * p->E, floats) + 3) & ~3;
+  return static_cast<size_t>(kWarps) * p->warp_floats * sizeof(float) + (p->counts != nullptr ? p->E * sizeof(int) : 0);
 }
 
 template <typename T, int L, int V, int K>
 tdx_status launch_route_k(RouteParams& p, cudaStream_t st) {
   constexpr int kBytes = std::min(16, V * static_cast<int>(sizeof(T)));
-  p.vector = p.E % V == 0 && aligned(p.logits, kBytes) && (p.ld * static_cast<int64_t>(sizeof(T))) % kBytes == 0;
-  for (int lanes = p.E / p.n_group / V; lanes > 1; lanes >>= 1) ++p.group_shift;
-  return launch_rows(tdx_moe_route_rows_kernel<T, L, V, K>, route_grid(p.T, 32 / L, V <= 8 ? 4 : 2),
-                     kThreads, route_smem(p), st, p);
+  p.vector = p.per % V == 0 && aligned(p.logits, kBytes) && (p.ld * static_cast<int64_t>(sizeof(T))) % kBytes == 0;
+  p.group_shift = group_lanes_log(p, V);
+  if (p.n_group == 1) p.group_shift = L == 8 ? 3 : L == 16 ? 4 : 5;
+  const size_t smem = route_smem(&p, p.vector ? 0 : 32 * V);
+  return launch_rows(tdx_moe_route_rows_kernel<T, L, V, K>, route_grid(p.T, 32 / L, V <= 8 ? 4 : 2), kThreads, smem, st, p);
 }
 
 template <typename T, int L, int V>
@@ -661,16 +834,39 @@ tdx_status launch_route_v(RouteParams& p, cudaStream_t st) {
   return p.k <= 8 ? launch_route_k<T, L, V, 8>(p, st) : launch_route_k<T, L, V, 16>(p, st);
 }
 
+// Whether L lanes hold the row, V experts each and a power of two of lanes per group
+bool route_fits(const RouteParams& p, int L, int V) {
+  return p.n_group == 1 ? p.E <= L * V : p.n_group << group_lanes_log(p, V) <= L;
+}
+
+// The smallest layout that holds the row. A warp for one token is not the best where a part of it can hold
+// one: the maxima, sums and addresses are the same instructions for one token as for four.
 template <typename T>
 tdx_status launch_route(RouteParams& p, cudaStream_t st) {
-  const int V = p.E <= 32 ? 4 : p.E <= 256 ? 8 : 16;
-  const int per = p.E / p.n_group;
-  if (p.n_group > 1 && (per % V != 0 || ((per / V) & (per / V - 1)) != 0))
-    return launch_rows(tdx_moe_route_kernel<T>, route_grid(p.T, 1, 8), kThreads, route_smem(p), st, p);
-  if (p.E <= 32) return launch_route_v<T, 8, 4>(p, st);
-  if (p.E <= 64) return launch_route_v<T, 8, 8>(p, st);
-  if (p.E <= 128) return launch_route_v<T, 16, 8>(p, st);
-  return p.E <= 256 ? launch_route_v<T, 32, 8>(p, st) : launch_route_v<T, 32, 16>(p, st);
+  p.per = p.E / p.n_group;
+  if (route_fits(p, 8, 4)) return launch_route_v<T, 8, 4>(p, st);
+  if (route_fits(p, 8, 8)) return launch_route_v<T, 8, 8>(p, st);
+  if (route_fits(p, 16, 8)) return launch_route_v<T, 16, 8>(p, st);
+  if (route_fits(p, 32, 8)) return launch_route_v<T, 32, 8>(p, st);
+  if (route_fits(p, 32, 16)) return launch_route_v<T, 32, 16>(p, st);
+  const size_t smem = route_smem(&p, 0);
+  return launch_rows(tdx_moe_route_kernel<T>, route_grid(p.T, 1, 8), kThreads, smem, st, p);
+}
+
+template <typename T, int L, int V>
+tdx_status launch_route_bwd_v(RouteParams& p, cudaStream_t st) {
+  constexpr int kBytes = std::min(16, V * static_cast<int>(sizeof(T)));
+  p.vector = p.E % V == 0 && aligned(p.logits, kBytes) && aligned(p.dlogits, kBytes) &&
+             (p.ld * static_cast<int64_t>(sizeof(T))) % kBytes == 0;
+  return launch_rows(tdx_moe_route_bwd_kernel<T, L, V>, route_grid(p.T, 32 / L, 8), kThreads, 0, st, p);
+}
+
+template <typename T>
+tdx_status launch_route_bwd(RouteParams& p, cudaStream_t st) {
+  if (p.E <= 32) return launch_route_bwd_v<T, 8, 4>(p, st);
+  if (p.E <= 64) return launch_route_bwd_v<T, 8, 8>(p, st);
+  if (p.E <= 128) return launch_route_bwd_v<T, 16, 8>(p, st);
+  return p.E <= 256 ? launch_route_bwd_v<T, 32, 8>(p, st) : launch_route_bwd_v<T, 32, 16>(p, st);
 }
 
 }  // namespace
@@ -723,8 +919,7 @@ tdx_status tdx_moe_route_bwd(const void* logits, const int32_t* topk_idx, const 
   p.dgates = dgates;
   p.dlogits = dlogits;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dtype == TDX_BF16 ? launch_rows(tdx_moe_route_bwd_kernel<bf16>, route_grid(T, 1, 8), kThreads, 0, st, p)
-                           : launch_rows(tdx_moe_route_bwd_kernel<float>, route_grid(T, 1, 8), kThreads, 0, st, p);
+  return dtype == TDX_BF16 ? launch_route_bwd<bf16>(p, st) : launch_route_bwd<float>(p, st);
 }
 
 }  // extern "C"
