@@ -23,7 +23,7 @@ struct RouteParams {
   int sigmoid, renorm;
   float scale;
   int64_t ld;
-  int vector;        // rows may be read in the lanes' 8 or 16 bytes
+  int vector;        // the lanes' experts may be read in words of 8 or 16 bytes
   int group_shift;   // log2 of the lanes per group
   int per;           // experts per group
   int warp_floats;   // shared memory of a warp
@@ -310,9 +310,12 @@ __device__ __forceinline__ void best_words(const uint32_t (&w)[16], uint32_t (&s
 // Largest of L lanes' words
 template <int L>
 __device__ __forceinline__ uint32_t lanes_top(uint32_t w) {
-  if constexpr (L == 32) return __reduce_max_sync(kAll, w);
+  if constexpr (L == 32) {
+    w = __reduce_max_sync(kAll, w);
+  } else {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) w = max(w, __shfl_xor_sync(kAll, w, o));
+    for (int o = L / 2; o > 0; o >>= 1) w = max(w, __shfl_xor_sync(kAll, w, o));
+  }
   return w;
 }
 
@@ -330,7 +333,7 @@ __device__ __forceinline__ uint32_t lanes_top(uint32_t w) {
 //
 // Bound by issue slots, not by HBM: ids have to be those of the definition, so that every sigmoid is
 // an expf and a correctly rounded reciprocal.
-template <typename T, int L, int V, int K>
+template <typename T, int L, int V, int K, bool kVector>
 __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_kernel(const __grid_constant__ RouteParams p) {
   constexpr int kTokens = 32 / L;
   constexpr int kLog = (V == 4 ? 2 : V == 8 ? 3 : 4) + (L == 8 ? 3 : L == 16 ? 4 : 5);
@@ -359,24 +362,28 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
   float next[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) next[i] = -INFINITY;
-  if (t < p.T) load_logits<T, L, V>(static_cast<const T*>(p.logits) + t * p.ld, sub, E, p.vector, next);
+  if (t < p.T) load_logits<T, L, V>(static_cast<const T*>(p.logits) + t * p.ld, sub, E, kVector, next);
   for (; t - lane / L < p.T; t += step) {
     const bool live = t < p.T;
     const T* row = static_cast<const T*>(p.logits) + t * p.ld;
     float f[V];   // logits, then keys
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = next[i];
-    if (!p.vector) {
+    if constexpr (!kVector) {
       // from every L-th column to consecutive ones
       float* const token = stage + first * V;
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < V; ++i) token[sub + i * L] = f[i];
       __syncwarp();
+      if (p.n_group == 1) {
+        read_lane(token + sub * V, f);
+      } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = holds && within + i < per ? token[c0 + i] : -INFINITY;
+        for (int i = 0; i < V; ++i) f[i] = holds && within + i < per ? token[c0 + i] : -INFINITY;
+      }
     }
-    if (t + step < p.T) load_logits<T, L, V>(row + step * p.ld, sub, E, p.vector, next);
+    if (t + step < p.T) load_logits<T, L, V>(row + step * p.ld, sub, E, kVector, next);
     float m = -INFINITY, sum = 1.0f;
     if (p.sigmoid) {
 #pragma unroll
@@ -445,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
         const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
         w[i] = (k & ~kLow) | (kLow - static_cast<uint32_t>(c0 + i));
       }
-      if (!p.vector) {
+      if constexpr (!kVector) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
           if (within + i >= per) w[i] = 0;
@@ -825,7 +832,9 @@ tdx_status launch_route_k(RouteParams& p, cudaStream_t st) {
   p.group_shift = group_lanes_log(p, V);
   if (p.n_group == 1) p.group_shift = L == 8 ? 3 : L == 16 ? 4 : 5;
   const size_t smem = route_smem(&p, p.vector ? 0 : 32 * V);
-  return launch_rows(tdx_moe_route_rows_kernel<T, L, V, K>, route_grid(p.T, 32 / L, V <= 8 ? 4 : 2), kThreads, smem, st, p);
+  const unsigned grid = route_grid(p.T, 32 / L, V <= 8 ? 4 : 2);
+  return p.vector ? launch_rows(tdx_moe_route_rows_kernel<T, L, V, K, true>, grid, kThreads, smem, st, p)
+                  : launch_rows(tdx_moe_route_rows_kernel<T, L, V, K, false>, grid, kThreads, smem, st, p);
 }
 
 template <typename T, int L, int V>
