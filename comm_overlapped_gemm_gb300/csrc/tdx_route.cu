@@ -331,8 +331,12 @@ __device__ __forceinline__ uint32_t lanes_top(uint32_t w) {
 // A group is a run of 2^n lanes (all of them where there are no groups); entries past its end hold -inf and
 // the word 0, which says that there is nothing.
 //
-// Bound by issue slots, not by HBM: ids have to be those of the definition, so that every sigmoid is
-// an expf and a correctly rounded reciprocal.
+// Bound by issue slots, not by HBM: 32768 tokens, softmax, 8 of 64 experts 7.6 us (146 warp instructions a
+// token; HBM 1.6 us), sigmoid with bias, 8 of 256 in 4 of 8 groups 28.8 us (737, of them 177 for scores: ids
+// have to be those of the definition, so that every sigmoid is an expf and a correctly rounded
+// reciprocal; 151 for the groups, 150 for the maxima, 42 for the sorted lists; HBM 5.3 us), 2.85 of 4
+// instructions a cycle. With 16 lanes of 16 experts for 256: 32.3 us, at half the blocks; three / five blocks
+// per SM 30.2 / 32.2 us; the maxima in a loop 33.0 us.
 template <typename T, int L, int V, int K, bool kVector>
 __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_kernel(const __grid_constant__ RouteParams p) {
   constexpr int kTokens = 32 / L;
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
           if (sub == L - 1) after = over;
         }
         if (j == p.k - 1) after = left;
-        open |= j < p.k && after != 0 && (got[r] ^ after) <= kLow;
+        open |= live && j < p.k && after != 0 && (got[r] ^ after) <= kLow;
       }
       if (__any_sync(kAll, open)) {
         // Put the places and the first word left out in order by their exact keys. Should the second
@@ -615,7 +619,9 @@ __device__ __forceinline__ void store_logits(T* x, int lane, int E, bool vector,
 // sub + r * L. What a chosen expert's logit receives is scattered into a row of shared memory and read
 // back by the lanes that hold the row, so that dlogits are written in whole lines and softmax over the
 // whole row needs no look at the chosen logits. Choices of the same expert add up in the order of their places.
-// Bound by HBM and the launch: 4 E (softmax over the row: 8 E) bytes and 8 topk bytes a token.
+// 4 E (softmax over the row: 8 E) bytes and 8 topk bytes a token: 32768 tokens, softmax over 64 experts 4.9 us
+// (HBM 2.8), 500 experts 34 us (20; in lanes of consecutive experts, read one by one, 89), renormalised
+// sigmoid over 256 17 us (5.5), there bound by the warp's steps for one token.
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(kThreads) tdx_moe_route_bwd_kernel(const __grid_constant__ RouteParams p) {
   constexpr int kTokens = 32 / L;
@@ -848,11 +854,14 @@ bool route_fits(const RouteParams& p, int L, int V) {
   return p.n_group == 1 ? p.E <= L * V : p.n_group << group_lanes_log(p, V) <= L;
 }
 
-// The smallest layout that holds the row. A warp for one token is not the best where a part of it can hold
-// one: the maxima, sums and addresses are the same instructions for one token as for four.
+// The smallest layout that holds the row: the maxima, sums and addresses are the same instructions for four
+// tokens of a warp as for one (32768 tokens, 64 experts 7.6 us, a warp per token 13.4). Up to a warp per
+// scheduler a whole warp's maximum in one instruction is sooner there than shuffles: 1 token 2.0 / 2.4 us, 600 tokens
+// 2.4 / 2.5, but 1024 3.4 / 2.5.
 template <typename T>
 tdx_status launch_route(RouteParams& p, cudaStream_t st) {
   p.per = p.E / p.n_group;
+  if (p.T <= 4 * sm_count() && route_fits(p, 32, 8)) return launch_route_v<T, 32, 8>(p, st);
   if (route_fits(p, 8, 4)) return launch_route_v<T, 8, 4>(p, st);
   if (route_fits(p, 8, 8)) return launch_route_v<T, 8, 8>(p, st);
   if (route_fits(p, 16, 8)) return launch_route_v<T, 16, 8>(p, st);
