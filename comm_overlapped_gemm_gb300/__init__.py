@@ -151,7 +151,7 @@ def _ptr(x) -> int:
         return 0
     if isinstance(x, int):
         return x
-    return int(x.data_ptr())
+    return x.data_ptr()
 
 
 def _nbytes(x) -> int:
