@@ -218,7 +218,7 @@ tdx_status tdx_swiglu(const void* y, void* out, const float* row_scale, const in
   ActParams p;
   const tdx_status s = act_params(R, I, dtype, o.out_dtype, o, &p);
   if (s != TDX_OK) return s;
-  if (y == nullptr || out == nullptr || !positive_finite(o.out_scale) || o.topk < 0) return TDX_ERR_INVALID_ARG;
+  if (y == nullptr || out == nullptr || !usable_scale(o.out_scale) || o.topk < 0) return TDX_ERR_INVALID_ARG;
   if ((o.topk > 0) != (dest != nullptr) || (o.topk > 0 && (R % o.topk != 0 || row_scale == nullptr)))
     return TDX_ERR_INVALID_ARG;
   if (!aligned(y, 16) || !aligned(out, 16) || !aligned(row_scale, 4) || !aligned(dest, 4)) return TDX_ERR_ALIGNMENT;

@@ -50,6 +50,20 @@ __device__ float block_reduce(float v, float* sm) {
   return r;
 }
 
+// The e4m3 scale of a row, max|y| / 448 (1 where that is 0 or no number), from m = max|h * weight|, and the factors
+// that take h * weight to codes: y / scale = h * weight * 448 / m, the numbers of rows near the smallest
+// float first multiplied by a power of two, so that 448 / m stays finite.
+__device__ __forceinline__ float row_scale(float m, float rstd, float* inv, float* up) {
+  const float s = m * rstd / 448.0f;
+  if (!(s > 0.0f)) {
+    *inv = rstd;
+    return 1.0f;
+  }
+  if (m < 1e-30f) *up = 0x1p100f;
+  *inv = 448.0f / (m * *up);
+  return s;
+}
+
 // A row held in registers, E of its elements per thread in 16-byte vectors: one read of x and residual,
 // one reduction for the sum of squares and (where the row's scale is wanted) max|h * weight|, whose
 // product with rstd is max|y|, one write of h and y.
@@ -122,11 +136,9 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E) tdx_rmsnorm_row
     if (scaled) m = warp_max(a.y);
   }
   const float rstd = 1.0f / sqrtf(ss / static_cast<float>(p.H) + p.eps);
-  float inv = rstd * p.inv_scale;
+  float inv = rstd * p.inv_scale, up = 1.0f;
   if (scaled) {
-    m *= rstd;
-    const float s = m > 0.0f ? m / 448.0f : 1.0f;
-    inv = rstd / s;
+    const float s = row_scale(m, rstd, &inv, &up);
     if (at == 0 && H > 0) p.row_scale[t] = s;
   }
   if (at == 0 && H > 0 && p.rstd != nullptr) p.rstd[t] = rstd;
@@ -134,7 +146,7 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E) tdx_rmsnorm_row
   for (int i = 0; i < V; ++i) {
     if (at + i * width * N < H) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) v[i][k] *= inv;
+      for (int k = 0; k < N; ++k) v[i][k] = v[i][k] * up * inv;
       store_vec(y + i * width * N, v[i]);
     }
   }
@@ -172,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) tdx_rmsnorm_kernel(const __grid_cons
   }
   ss = block_reduce<false>(ss, sm);
   const float rstd = 1.0f / sqrtf(ss / static_cast<float>(p.H) + p.eps);
-  float inv = p.inv_scale;
+  float inv = rstd * p.inv_scale, up = 1.0f;
   if (p.row_scale != nullptr) {
     float m = 0.0f;
     for (int c = threadIdx.x * N; c < p.H; c += kThreads * N) {
@@ -180,11 +192,10 @@ __global__ void __launch_bounds__(kThreads) tdx_rmsnorm_kernel(const __grid_cons
       load_h(c, v);
       load_vec(w + c, g);
 #pragma unroll
-      for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i] * rstd * g[i]));
+      for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i] * g[i]));
     }
     m = block_reduce<true>(m, sm);
-    const float s = m > 0.0f ? m / 448.0f : 1.0f;
-    inv = 1.0f / s;
+    const float s = row_scale(m, rstd, &inv, &up);
     if (threadIdx.x == 0) p.row_scale[t] = s;
   }
   if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[t] = rstd;
@@ -194,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) tdx_rmsnorm_kernel(const __grid_cons
     load_vec(w + c, g);
     if (h != nullptr) store_vec(h + c, v);
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = v[i] * rstd * g[i] * inv;
+    for (int i = 0; i < N; ++i) v[i] = v[i] * g[i] * up * inv;
     store_vec(y + c, v);
   }
 }
@@ -528,7 +539,7 @@ tdx_norm_opts norm_defaults() {
 
 tdx_status check_sizes(int T, int H, tdx_dtype dtype) {
   if (T < 0 || H <= 0 || !known(dtype)) return TDX_ERR_INVALID_ARG;
-  return dtype == TDX_FP8_E4M3 ? TDX_ERR_UNSUPPORTED : TDX_OK;
+  return dtype == TDX_FP8_E4M3 || H > (1 << 28) ? TDX_ERR_UNSUPPORTED : TDX_OK;
 }
 
 }  // namespace
@@ -551,7 +562,7 @@ tdx_status tdx_rmsnorm(const void* x, const void* residual, const void* weight, 
   if (s != TDX_OK) return s;
   if (x == nullptr || weight == nullptr || y == nullptr || (h_out != nullptr && residual == nullptr))
     return TDX_ERR_INVALID_ARG;
-  if (!known(o.out_dtype) || !(o.eps >= 0.0f) || !std::isfinite(o.eps) || !positive_finite(o.out_scale))
+  if (!known(o.out_dtype) || !(o.eps >= 0.0f) || !std::isfinite(o.eps) || !usable_scale(o.out_scale))
     return TDX_ERR_INVALID_ARG;
   if (row_scale != nullptr && o.out_dtype != TDX_FP8_E4M3) return TDX_ERR_INVALID_ARG;
   NormParams p;

@@ -114,7 +114,8 @@ tdx_status launch_rows(void (*kernel)(KArgs...), unsigned grid, unsigned block, 
 }
 
 inline bool aligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-inline bool positive_finite(float v) { return v > 0.0f && std::isfinite(v); }
+// A scale that the kernels may divide by: it and its reciprocal are positive and finite
+inline bool usable_scale(float v) { return v > 0.0f && std::isfinite(v) && std::isfinite(1.0f / v); }
 inline size_t bytes_of(tdx_dtype d) { return d == TDX_BF16 ? 2 : d == TDX_FP8_E4M3 ? 1 : 4; }
 inline bool known(tdx_dtype d) { return d == TDX_BF16 || d == TDX_FP8_E4M3 || d == TDX_FP32; }
 

@@ -342,14 +342,15 @@ tdx_status tdx_moe_combine_plan_info(int W, int T, int F, int H, int E, int topk
  *  weight     device, H of `dtype`.
  *  y          device, T x H of opts->out_dtype (TDX_BF16, TDX_FP32 or TDX_FP8_E4M3).
  *  row_scale  device, T fp32 (4-byte aligned), e4m3 output only: row t is stored as
- *             y[t] / row_scale[t] with row_scale[t] = max|y[t]| / 448 (1 if that is 0). NULL: e4m3
+ *             y[t] / row_scale[t] with row_scale[t] = max|y[t]| / 448 (1 if that is 0 or NaN). NULL: e4m3
  *             output is y / opts->out_scale, one scale per tensor as the e4m3 products take it.
  *  rstd       optional, T fp32 (4-byte aligned), for tdx_rmsnorm_bwd.
- * A row holding a NaN or an infinity gives the NaNs the formula gives; others are not touched. */
+ * A row holding a NaN or an infinity gives the NaNs the formula gives; others are not touched.
+ * H <= 2^28 (TDX_ERR_UNSUPPORTED beyond). */
 typedef struct tdx_norm_opts {
   tdx_dtype out_dtype;       /* default TDX_BF16 */
   float eps;                 /* default 1e-6; finite, >= 0 */
-  float out_scale;           /* default 1; finite, > 0 */
+  float out_scale;           /* default 1; positive and finite, as its reciprocal */
   int64_t ld_x, ld_residual, ld_h, ld_y;   /* row strides (tdx_rmsnorm_bwd: ld_x of dy, ld_residual
                                 of dres, ld_h of h, ld_y of dx) */
 } tdx_norm_opts;
@@ -426,7 +427,7 @@ tdx_status tdx_moe_route_bwd(const void* logits, const int32_t* topk_idx, const 
  *  dest       given exactly when opts->topk > 0. Both 4-byte aligned. */
 typedef struct tdx_act_opts {
   tdx_dtype out_dtype;       /* default TDX_BF16 */
-  float out_scale;           /* default 1; finite, > 0 */
+  float out_scale;           /* default 1; positive and finite, as its reciprocal */
   int topk;                  /* slots per token for row_scale and dest; default 0; divides R */
   int64_t ld_y, ld_out;      /* row strides (backwards: of y and dy, and of dout) */
 } tdx_act_opts;

@@ -125,6 +125,23 @@ def test_rmsnorm_rows_that_hold_nothing_or_too_much(H):
     assert bool((q[0].float()[big].abs() == 448.0).all())
 
 
+@pytest.mark.parametrize("H", [128, 2048, 33024])
+def test_rmsnorm_row_scales_of_tiny_rows(H):
+    """Rows near the smallest float have a scale near it and ordinary codes."""
+    rng = np.random.default_rng(H)
+    x, xv = dev(rng.standard_normal((5, H)) * np.array([1e-20, 1e-33, 3e-37, 1e-38, 1.0])[:, None], "fp32")
+    w, wv = dev(1 + 0.2 * rng.standard_normal(H), "fp32")
+    _, q, scale, _ = run_norm(x, None, w, "fp32", "e4m3", True, eps=1.0)
+    _, _, wy = RO.rmsnorm(xv, None, wv, 1.0)
+    ws = RO.e4m3_row_scale(wy)
+    calc = F * (H / 32 + 64)
+    near(host(scale)[:4], ws[:4], 2 * calc * ws[:4] + 2.0 ** -149, "scale")
+    # a scale that is itself subnormal has fewer bits: its relative rounding goes into the codes' bound
+    coarse = (2.0 ** -149 / ws)[:, None]
+    want = wy / ws[:, None]
+    near(host(q), want, (U["e4m3"] + 3 * calc + coarse) * np.abs(want) * (1 + 2.0 ** -6) + SMALLEST["e4m3"], "codes")
+
+
 def test_rmsnorm_in_place_on_another_stream_and_repeatable():
     g = torch.Generator().manual_seed(5)
     x, r = (torch.randn(33, 2048, generator=g).bfloat16().cuda() for _ in range(2))

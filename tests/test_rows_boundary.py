@@ -66,8 +66,9 @@ def test_rmsnorm_refusals(tdx):
     assert norm(tdx, dtype=tdx.TDX_FP8_E4M3) == uns
     for eps in (-1e-6, math.nan, math.inf):
         assert norm(tdx, eps=eps) == inv
-    for s in (0.0, -1.0, math.nan, math.inf):
+    for s in (0.0, -1.0, math.nan, math.inf, 1e-40):
         assert norm(tdx, out_dtype=1, out_scale=s) == inv
+    assert norm(tdx, H=(1 << 28) + 8) == uns
     assert norm(tdx, rs=FAKE) == inv                   # row scales without an e4m3 output
     assert norm(tdx, H=60) == ali                      # 120-byte rows
     assert norm(tdx, H=24, out_dtype=1) == ali         # 24-byte e4m3 rows
