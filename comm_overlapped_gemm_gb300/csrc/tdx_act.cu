@@ -1,14 +1,14 @@
 // Gated SiLU between two products and its gradient (tdx_swiglu, tdx_swiglu_bwd).
+#include <algorithm>
+
 #include "tdx_rows.cuh"
 
 namespace tdx {
 namespace {
 
-constexpr int kThreads = 256;
-// Vectors per thread of a large call. 1 / 2 / 4 / 8: forwards 262144 x 2048 472 / 454 / 468 / 482 us and
-// 8192 x 2048 (scaled by token) 19.6 / 19.5 / 22.0 / 31.9 us, backwards 65533 x 3584 333 / 329 / 330 /
-// 393 us (bf16).
-constexpr int kWide = 2;
+constexpr int kThreads = 128;
+constexpr int kWide = 2;          // vectors per thread of a large call
+constexpr int kDestBlocks = 24;   // blocks per SM that go round where rows are found through dest
 
 struct ActParams {
   const void* y;
@@ -16,94 +16,118 @@ struct ActParams {
   const void* dout;
   const float* row_scale;
   const int32_t* dest;
-  int R, I, topk;
-  int cols;        // 16-byte vectors of a row that a block takes
-  int rows;        // rows that a block takes
-  int col_blocks;  // blocks along a row
-  int magic;       // ceil(2^20 / cols): l / cols = l * magic >> 20 for l and cols up to 1024
+  int R, I;
+  int per;          // 16-byte vectors of a row of I
+  int64_t all;      // vectors of the call, R * per
+  uint64_t magic;   // ceil(2^64 / per), 0 for per = 1
+  uint64_t magic_k; // the same for topk
   int64_t ld_y, ld_out;
   float inv_scale;
 };
 
 // a * sigmoid(a) with the approximate exponential and quotient: together within 2^-22 * (2 + |a|) of
-// it, far inside the output's rounding (bf16, e4m3) or of the order of fp32's own (8 roundings at
-// |a| = 1). exp(-a) = inf gives -0, as the exact quotient does. The exact expf and quotient took the
-// kernel from memory-bound to issue-bound (262144 x 2048 bf16: 669 us).
+// it, far inside the output's rounding (bf16, e4m3) or of the order of fp32's own. exp(-a) = inf gives -0,
+// as the exact quotient does. With the exact expf and quotient the kernel is bound by issue slots
+// (262144 x 2048 bf16, one vector per thread: 669 us).
 __device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
 
-// The block's l-th vector: its row of the call (dest not applied) and its first column
+// i / d as the high half of i * ceil(2^64 / d): exact as long as i * (the product of d and that - 2^64) < 2^64,
+// that is i < 2^37 for d up to 2^27
+__host__ uint64_t magic_of(int d) { return d == 1 ? 0 : ~UINT64_C(0) / d + 1; }
+__device__ __forceinline__ int64_t divide(int64_t i, uint64_t magic) {
+  return magic != 0 ? static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(i), magic)) : i;
+}
+// The call's i-th vector: its row (dest not applied) and first column
 template <int N>
-__device__ __forceinline__ bool place(const ActParams& p, int l, int rb, int cb, int64_t* r, int* c) {
-  const int lr = (l * p.magic) >> 20;
-  *r = static_cast<int64_t>(rb) * p.rows + lr;
-  *c = (cb * p.cols + l - lr * p.cols) * N;
-  return lr < p.rows && *r < p.R && *c < p.I;
+__device__ __forceinline__ int64_t place(const ActParams& p, int64_t i, int* c) {
+  const int64_t r = divide(i, p.magic);
+  *c = static_cast<int>(i - r * p.per) * N;
+  return r;
 }
 
-// Bound by HBM: 6 bytes an element in bf16, 7.1 TB/s at 262144 x 2048 (454 us, a plain copy's rate 482);
-// 8192 x 2048 takes 19.5 us of 15.1, the launch's ramp and tail the rest. Each thread issues all loads of its
-// V vectors before it computes, so that a block has 2 V x 4 KiB in flight; a block takes whole rows where
-// they are short and a stretch of one row where they are long, which leaves a multiplication and a shift to
-// find a vector's row.
-template <typename T, typename O, int V>
+// Bound by HBM: 6 bytes an element in bf16, 7.2 TB/s at 262144 x 2048 (450 us, a plain copy's rate 482); 8192 x
+// 2048 takes 16.3 us of 15.1. The call's vectors are dealt out in the order of their addresses, V x kThreads to
+// a block, whatever the row's length; a thread issues all loads of its V vectors before it computes.
+// V = 1 / 2 / 4 / 8 with 256 threads: 472 / 454 / 468 / 482 us; 128 / 256 / 512 threads with V = 2: 448 / 454 / 459.
+// kDest: rows are found through dest, which puts a second memory latency in front of a block's loads. So
+// blocks go round and look up their next rows and scales while the loads of the present ones are under way:
+// 8192 x 2048 18.4 us, 262144 x 2048 506 us; a block per piece 19.6 and 545, 8 (all resident) / 10 / 16 blocks
+// per SM that go round 522 / 622 / 509.
+template <typename T, typename O, int V, bool kDest>
 __global__ void __launch_bounds__(kThreads) tdx_swiglu_kernel(const __grid_constant__ ActParams p) {
   constexpr int N = kVec<T>;
   griddep_launch_dependents();
-  const int rb = blockIdx.x / p.col_blocks, cb = blockIdx.x - rb * p.col_blocks;
-  uint4 qg[V], qu[V];
-  int64_t row[V];
-  int col[V];
-  bool on[V];
-  float s[V];
-  griddep_wait();
+  int64_t row[V], next_row[V];   // -1: nothing to do
+  int col[V], next_col[V];
+  float s[V], next_s[V];
+  int64_t i = static_cast<int64_t>(blockIdx.x) * (V * kThreads) + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (V * kThreads);
+  auto find = [&](int64_t from) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    int64_t r;
-    on[v] = place<N>(p, v * kThreads + threadIdx.x, rb, cb, &r, &col[v]);
-    row[v] = r;
-    s[v] = 1.0f;
-    if (on[v] && p.row_scale != nullptr) {
-      if (p.dest != nullptr) {
-        row[v] = p.dest[r];
-        on[v] = row[v] >= 0 && row[v] < p.R;
-        r /= p.topk;
+    for (int v = 0; v < V; ++v) {
+      const int64_t at = from + v * kThreads;
+      next_row[v] = -1;
+      next_s[v] = 1.0f;
+      if (at < p.all) {
+        const int64_t r = place<N>(p, at, &next_col[v]);
+        next_row[v] = r;
+        if (kDest) {
+          next_row[v] = p.dest[r];
+          if (next_row[v] >= p.R) next_row[v] = -1;
+          next_s[v] = p.row_scale[divide(r, p.magic_k)];
+        } else if (p.row_scale != nullptr) {
+          next_s[v] = p.row_scale[r];
+        }
       }
-      s[v] = p.row_scale[r];
     }
-    if (on[v]) {
-      const T* y = static_cast<const T*>(p.y) + row[v] * p.ld_y + col[v];
-      qg[v] = __ldcs(reinterpret_cast<const uint4*>(y));
-      qu[v] = __ldcs(reinterpret_cast<const uint4*>(y + p.I));
+  };
+  griddep_wait();
+  find(i);
+  do {
+    uint4 qg[V], qu[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      row[v] = next_row[v];
+      col[v] = next_col[v];
+      s[v] = next_s[v];
+      if (row[v] >= 0) {
+        const T* y = static_cast<const T*>(p.y) + row[v] * p.ld_y + col[v];
+        qg[v] = __ldcs(reinterpret_cast<const uint4*>(y));
+        qu[v] = __ldcs(reinterpret_cast<const uint4*>(y + p.I));
+      }
     }
-  }
+    i += step;
+    if (kDest) find(i);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    if (!on[v]) continue;
-    float g[N], u[N];
-    unpack(qg[v], g, T{});
-    unpack(qu[v], u, T{});
-    const float su = s[v] * p.inv_scale;
+    for (int v = 0; v < V; ++v) {
+      if (row[v] < 0) continue;
+      float g[N], u[N];
+      unpack(qg[v], g, T{});
+      unpack(qu[v], u, T{});
+      const float su = s[v] * p.inv_scale;
 #pragma unroll
-    for (int k = 0; k < N; ++k) g[k] = silu(g[k] * s[v]) * (u[k] * su);
-    store_vec(static_cast<O*>(p.out) + row[v] * p.ld_out + col[v], g);
-  }
+      for (int k = 0; k < N; ++k) g[k] = silu(g[k] * s[v]) * (u[k] * su);
+      store_vec(static_cast<O*>(p.out) + row[v] * p.ld_out + col[v], g);
+    }
+  } while (kDest && i - threadIdx.x < p.all);
 }
 
-// As above: 10 bytes an element in bf16, 7.1 TB/s at 65533 x 3584 (329 us). dy may be y: a thread writes only what it has read.
+// As above: 10 bytes an element in bf16, 7.1 TB/s at 65533 x 3584 (330 us, a plain copy's rate 352). dy may be
+// y: a thread writes only what it has read.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) tdx_swiglu_bwd_kernel(const __grid_constant__ ActParams p) {
   constexpr int N = kVec<T>;
   griddep_launch_dependents();
-  const int rb = blockIdx.x / p.col_blocks, cb = blockIdx.x - rb * p.col_blocks;
   uint4 qg[V], qu[V], qd[V];
   int64_t row[V];
   int col[V];
-  bool on[V];
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * (V * kThreads) + threadIdx.x;
   griddep_wait();
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    on[v] = place<N>(p, v * kThreads + threadIdx.x, rb, cb, &row[v], &col[v]);
-    if (on[v]) {
+    row[v] = -1;
+    if (i + v * kThreads < p.all) {
+      row[v] = place<N>(p, i + v * kThreads, &col[v]);
       const T* y = static_cast<const T*>(p.y) + row[v] * p.ld_y + col[v];
       qg[v] = __ldcs(reinterpret_cast<const uint4*>(y));
       qu[v] = __ldcs(reinterpret_cast<const uint4*>(y + p.I));
@@ -112,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) tdx_swiglu_bwd_kernel(const __grid_c
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    if (!on[v]) continue;
+    if (row[v] < 0) continue;
     float g[N], u[N], d[N];
     unpack(qg[v], g, T{});
     unpack(qu[v], u, T{});
@@ -130,31 +154,30 @@ __global__ void __launch_bounds__(kThreads) tdx_swiglu_bwd_kernel(const __grid_c
   }
 }
 
-// Split the call into blocks of about V * kThreads vectors; returns the grid.
-unsigned act_split(ActParams* p, int n, int V) {
-  const int per = p->I / n, most = V * kThreads;
-  p->cols = per < most ? per : most;
-  p->rows = most / p->cols;
-  p->col_blocks = (per + p->cols - 1) / p->cols;
-  p->magic = ((1 << 20) + p->cols - 1) / p->cols;
-  return static_cast<unsigned>((static_cast<int64_t>(p->R) + p->rows - 1) / p->rows * p->col_blocks);
+int act_sms() { return sm_count() > 0 ? sm_count() : kRefSMs; }
+
+// Splits the call into vectors of n elements; whether it is large: enough of them to fill the device four
+// times over with kWide per thread (a small call spreads over more SMs with one).
+bool act_split(ActParams* p, int n) {
+  p->per = p->I / n;
+  p->all = static_cast<int64_t>(p->R) * p->per;
+  p->magic = magic_of(p->per);
+  return p->all >= static_cast<int64_t>(act_sms()) * 2048;
 }
 
-// kWide vectors per thread once that fills the device four times over, else one, so that small calls spread
-// over more SMs
-bool act_large(const ActParams& p, int n) {
-  const int sms = sm_count() > 0 ? sm_count() : kRefSMs;
-  return static_cast<int64_t>(p.R) * (p.I / n) >= static_cast<int64_t>(sms) * 8 * kThreads;
+unsigned act_grid(const ActParams& p, int V) { return static_cast<unsigned>((p.all + V * kThreads - 1) / (V * kThreads)); }
+
+template <typename T, typename O, int V>
+tdx_status launch_act_v(const ActParams& p, cudaStream_t st) {
+  const unsigned grid = act_grid(p, V);
+  if (p.dest == nullptr) return launch_rows(tdx_swiglu_kernel<T, O, V, false>, grid, kThreads, 0, st, p);
+  return launch_rows(tdx_swiglu_kernel<T, O, V, true>, std::min(grid, static_cast<unsigned>(act_sms() * kDestBlocks)), kThreads, 0, st,
+                     p);
 }
 
 template <typename T, typename O>
 tdx_status launch_act_t(ActParams& p, cudaStream_t st) {
-  if (act_large(p, kVec<T>)) {
-    const unsigned grid = act_split(&p, kVec<T>, kWide);
-    return launch_rows(tdx_swiglu_kernel<T, O, kWide>, grid, kThreads, 0, st, p);
-  }
-  const unsigned grid = act_split(&p, kVec<T>, 1);
-  return launch_rows(tdx_swiglu_kernel<T, O, 1>, grid, kThreads, 0, st, p);
+  return act_split(&p, kVec<T>) ? launch_act_v<T, O, kWide>(p, st) : launch_act_v<T, O, 1>(p, st);
 }
 
 template <typename T>
@@ -168,12 +191,8 @@ tdx_status launch_act(tdx_dtype out, ActParams& p, cudaStream_t st) {
 
 template <typename T>
 tdx_status launch_act_bwd(ActParams& p, cudaStream_t st) {
-  if (act_large(p, kVec<T>)) {
-    const unsigned grid = act_split(&p, kVec<T>, kWide);
-    return launch_rows(tdx_swiglu_bwd_kernel<T, kWide>, grid, kThreads, 0, st, p);
-  }
-  const unsigned grid = act_split(&p, kVec<T>, 1);
-  return launch_rows(tdx_swiglu_bwd_kernel<T, 1>, grid, kThreads, 0, st, p);
+  if (act_split(&p, kVec<T>)) return launch_rows(tdx_swiglu_bwd_kernel<T, kWide>, act_grid(p, kWide), kThreads, 0, st, p);
+  return launch_rows(tdx_swiglu_bwd_kernel<T, 1>, act_grid(p, 1), kThreads, 0, st, p);
 }
 
 tdx_act_opts act_defaults() {
@@ -227,7 +246,7 @@ tdx_status tdx_swiglu(const void* y, void* out, const float* row_scale, const in
   p.out = out;
   p.row_scale = row_scale;
   p.dest = dest;
-  p.topk = o.topk;
+  if (o.topk > 0) p.magic_k = magic_of(o.topk);
   if (o.out_dtype == TDX_FP8_E4M3) p.inv_scale = 1.0f / o.out_scale;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return dtype == TDX_BF16 ? launch_act<bf16>(o.out_dtype, p, st) : launch_act<float>(o.out_dtype, p, st);

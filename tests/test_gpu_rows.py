@@ -340,6 +340,60 @@ def test_route_masked_and_non_finite_logits(score, E, k, n_group):
             assert np.isnan(gates[5]).all()
 
 
+@pytest.mark.parametrize("E,k,n_group,topk_group,group_top,score", [(64, 8, 1, 1, 1, "softmax"), (256, 8, 8, 4, 2, "sigmoid"),
+                                                                  (500, 16, 4, 2, 2, "sigmoid"), (30, 2, 3, 2, 1, "softmax")])
+def test_route_of_more_tokens_than_the_warps_take_at_once(E, k, n_group, topk_group, group_top, score):
+    T = 40003 if E <= 64 else 20011
+    rng = np.random.default_rng(E)
+    x, xv = dev(1.5 * rng.standard_normal((T, E)), "fp32")
+    b, bv = dev(0.05 * rng.standard_normal(E), "fp32") if score == "sigmoid" else (None, None)
+    counts = torch.zeros(E, dtype=torch.int32, device="cuda")
+    ids, gates = run_route(x, k, "fp32", b, counts, score=score_code(score), n_group=n_group, topk_group=topk_group,
+                           group_top=group_top)
+    want, wg, margin = RO.route(xv, k, score, bv, n_group, topk_group, group_top)
+    clear = margin > 32 * F
+    assert clear.mean() >= 0.9
+    assert np.array_equal(ids[clear], want[clear])
+    near(gates[clear], wg[clear], F * (E / 16 + 64 + np.abs(xv).max() * 2) * wg[clear], "gates")
+    assert np.array_equal(counts.cpu().numpy(), np.bincount(ids.ravel(), minlength=E))
+    dg, dgv = dev(rng.standard_normal((T, k)), "fp32")
+    out = torch.full((T, E), PAD, device="cuda")
+    tdx.check(tdx.tdx_moe_route_bwd(x, torch.from_numpy(ids.astype(np.int32)).cuda(), dg, out, T, E, k, 2,
+                                    tdx.make_route_opts(score=score_code(score), renorm=0)))
+    wd = RO.route_bwd(xv, ids, dgv, score, False, 1.0)
+    mag = 2 * RO.scores(xv, score) * np.abs(dgv).sum(1, keepdims=True)
+    near(host(out), wd, U["fp32"] * np.abs(wd) + F * (E / 16 + 64 + 4 * np.abs(xv).max()) * mag, "dlogits")
+
+
+@pytest.mark.parametrize("E,n_group", [(64, 1), (256, 8), (512, 16), (100, 1), (24, 1)])
+@pytest.mark.parametrize("score,bias", [("softmax", False), ("sigmoid", False), ("sigmoid", True)])
+def test_route_keys_that_differ_in_their_last_bits(E, n_group, score, bias):
+    """Keys a few steps of fp32 apart, which the leading bits do not tell from one another: the order is
+    that of the definition's fp32 keys, computed here with the device's own exp and quotient."""
+    T, k = 700, 8
+    g = torch.Generator().manual_seed(E)
+    base = torch.randn(T, 1, generator=g)
+    x = (base + 2.0 ** -22 * torch.randint(-6, 7, (T, E), generator=g)).cuda()
+    x[::3] += (torch.rand(x[::3].shape, generator=g) < 0.5).cuda() * 1.0       # two clusters of keys
+    b = (2.0 ** -20 * torch.randint(-2, 3, (E,), generator=g)).cuda() if bias else None
+    ids, _ = run_route(x, k, "fp32", b, score=score_code(score), n_group=n_group, topk_group=max(1, n_group // 2),
+                       group_top=1)
+    key = x + 0.0
+    if score == "sigmoid":
+        key = 1.0 / (1.0 + torch.exp(-x))
+        if bias:
+            key = key + b
+    key = key.cpu().numpy().astype(np.float64)
+    if n_group > 1:
+        per = E // n_group
+        best = key.reshape(T, n_group, per).max(2)
+        keep = np.argsort(-best, axis=1, kind="stable")[:, :n_group // 2]
+        on = np.zeros((T, n_group), bool)
+        np.put_along_axis(on, keep, True, 1)
+        key = np.where(np.repeat(on, per, 1), key, -np.inf)
+    assert np.array_equal(ids, np.argsort(-key, axis=1, kind="stable")[:, :k])
+
+
 def test_route_counts_are_added_and_streams_hold():
     x = torch.randn(1000, 48, generator=torch.Generator().manual_seed(2)).cuda()
     counts = torch.arange(48, dtype=torch.int32, device="cuda")
@@ -460,6 +514,33 @@ def test_swiglu(R, I, dtype, out, scaled, pad):
     near(host(o), want, (U[out] + F * (24 + 4 * g)) * np.abs(want) * (1 + 2.0 ** -6) + SMALLEST[out], "out")
     if pad:
         assert bool((ob[:, I:].float() == torch.tensor(PAD).to(ob.dtype).float().item()).all())
+
+
+@pytest.mark.parametrize("topk", [0, 3])
+def test_swiglu_of_more_rows_than_the_blocks_take_at_once(topk):
+    R, I = 4101, 2080
+    rng = np.random.default_rng(topk)
+    y, yv = dev(2 * rng.standard_normal((R, 2 * I)), "bf16")
+    rs = dest = c = None
+    if topk:
+        rs, rv = dev(0.5 + rng.random(R // topk), "fp32")
+        perm = rng.permutation(R)
+        dest = torch.from_numpy(perm.astype(np.int32)).cuda()
+        c = np.empty(R)
+        c[perm] = np.repeat(rv, topk)
+    out = torch.full((R, I), PAD, dtype=torch.bfloat16, device="cuda")
+    tdx.check(tdx.tdx_swiglu(y, out, rs, dest, R, I, 0, tdx.make_act_opts(topk=topk)))
+    want = RO.swiglu(yv, c)
+    g = np.abs(yv[:, :I] * (1 if c is None else c[:, None]))
+    near(host(out), want, (U["bf16"] + F * (24 + 4 * g)) * np.abs(want) * (1 + 2.0 ** -6), "out")
+    if not topk:
+        do, dov = dev(0.1 * rng.standard_normal((R, I)), "bf16")
+        dy = torch.full_like(y, PAD)
+        tdx.check(tdx.tdx_swiglu_bwd(y, do, dy, R, I, 0))
+        want = RO.swiglu_bwd(yv, dov)
+        s, u = RO.scores(yv[:, :I], "sigmoid"), np.abs(yv[:, I:])
+        mag = np.concatenate([np.abs(dov) * u * s * (1 + g), np.abs(want[:, I:])], 1)
+        near(host(dy), want, U["bf16"] * np.abs(want) + F * (24 + 4 * np.concatenate([g, g], 1)) * mag * (1 + 2.0 ** -6))
 
 
 def test_swiglu_extremes_and_rows_that_dest_skips():
