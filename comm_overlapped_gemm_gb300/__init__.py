@@ -163,22 +163,25 @@ def _ptr_array(xs):
     return arr
 
 
-_torch = None   # the torch module, once a call needed its current stream
+_raw_stream = _device = None   # torch's calls for them, once CUDA is up
 
 
 def _stream(stream) -> int:
-    global _torch
     if stream is None:
-        if _torch is None:
-            import torch
-            _torch = torch
-        if not _torch.cuda.is_initialized():
-            return int(_torch.cuda.current_stream().cuda_stream) if _torch.cuda.is_available() else 0
-        # the handle without the Stream object around it: 0.3 us against 3.9 us a call
-        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+        # the handle without the Stream object around it: 0.2 us against 3.9 us a call
+        return _raw_stream(_device()) if _raw_stream is not None else _first_stream()
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
+
+
+def _first_stream() -> int:
+    global _raw_stream, _device
+    import torch
+    if not torch.cuda.is_initialized():
+        return int(torch.cuda.current_stream().cuda_stream) if torch.cuda.is_available() else 0
+    _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    return _stream(None)
 
 
 def make_opts(**kw) -> tdx_opts:
