@@ -16,7 +16,7 @@ using namespace tdx;
 
 namespace {
 
-constexpr uint32_t kVersion = (1u << 16) | 1u;   // 1.1: AllReduce, bf16 partials, MoE dispatch and combine
+constexpr uint32_t kVersion = (1u << 16) | 2u;   // 1.2: norm, routing, gated SiLU
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

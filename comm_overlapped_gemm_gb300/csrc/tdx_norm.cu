@@ -69,13 +69,16 @@ __device__ __forceinline__ float row_scale(float m, float rstd, float* inv, floa
 // product with rstd is max|y|, one write of h and y.
 // kLanes 8, 16, 32: that many lanes of a warp per row (short rows; the reduction is shuffles alone); 0: a
 // block per row, whose reduction takes one barrier.
-// Bound by HBM: 32768 x 7168 bf16 with the residual 272 us (6.9 TB/s, a plain copy's rate 281), 1000000 x
-// 128 152 us (6.9 TB/s); with a warp per row of 128, half of its lanes idle, 200 us. 1024 x 7168 to
-// e4m3 with row scales takes 11.4 us of 7.7 (the launch's ramp and tail). Rows through a ring of cp.async
-// stages in shared memory, as the gradient takes them, came out slower here (311 us): the many
-// independent blocks keep more loads in flight than one block per SM does between two sums.
+// Bound by HBM: 32768 x 7168 bf16 with the residual 271 us (6.9 TB/s, a plain copy's rate 281), 1000000 x
+// 128 152 us (6.9 TB/s; with a warp per row of 128, half of its lanes idle, 200 us). 1024 x 7168 to e4m3 with
+// row scales takes 11.2 us of 7.7: the launch's ramp and tail (a plain addition over as many bytes takes 9.0).
+// Rows through a ring of cp.async stages in shared memory, as the gradient takes them, came out slower
+// here (311 us): the many independent blocks keep more loads in flight than one block per SM does
+// between two sums.
+// Registers: 64 a thread for 32 bf16 elements, so that four blocks of 224 threads share an SM instead of three
+// (1024 x 7168 to e4m3 11.2 / 11.7 us; five, at 48 registers, spill: 13.8).
 template <typename T, typename O, int E, int kLanes>
-__global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E) tdx_rmsnorm_rows_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && sizeof(T) == 2 && E == 32 ? 2 : 1) tdx_rmsnorm_rows_kernel(const __grid_constant__ NormParams p) {
   constexpr int N = kVec<T>;
   constexpr int V = E / N;
   __shared__ float2 sm[32];
@@ -472,7 +475,7 @@ tdx_status launch_norm_t(const NormParams& p, cudaStream_t st) {
   if (p.H <= 1024) return launch_norm_lanes<T, O, 32, 32>(p, st);
   if (p.H <= 16384) {
     // up to one row per SM, 16 elements a thread shorten the row; beyond, 32 carry more loads per block:
-    // 1 x 8192 2.0 / 2.2 us, 32768 x 7168 293 / 272 us
+    // 1 x 8192 2.0 / 2.2 us, 32768 x 7168 293 / 271 us
     auto block = [&](int e) { return static_cast<unsigned>((p.H + 32 * e - 1) / (32 * e) * 32); };
     if (p.T <= sm_count()) return launch_rows(tdx_rmsnorm_rows_kernel<T, O, 16, 0>, p.T, block(16), 0, st, p);
     return launch_rows(tdx_rmsnorm_rows_kernel<T, O, 32, 0>, p.T, block(32), 0, st, p);
