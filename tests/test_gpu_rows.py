@@ -266,7 +266,8 @@ ROUTE_SIZES = [  # T, E, k, n_group, topk_group, group_top
     (1, 64, 8, 1, 1, 1), (700, 64, 8, 1, 1, 1), (33, 256, 8, 8, 4, 2), (1, 1, 1, 1, 1, 1), (50, 2, 2, 1, 1, 1),
     (65, 7, 3, 1, 1, 1), (300, 60, 4, 1, 1, 1), (100, 100, 6, 4, 2, 1), (64, 512, 16, 16, 4, 2), (40, 384, 12, 32, 5, 2),
     (9, 16, 16, 1, 1, 1), (31, 33, 5, 3, 2, 2), (20, 8, 2, 8, 3, 2), (2500, 128, 8, 1, 1, 1), (300, 160, 6, 8, 3, 1),
-    (70, 32, 16, 2, 1, 2), (11, 500, 7, 1, 1, 1)]
+    (70, 32, 16, 2, 1, 2), (11, 500, 7, 1, 1, 1), (300, 48, 4, 2, 1, 1), (900, 96, 6, 4, 2, 2), (64, 240, 8, 2, 1, 2),
+    (700, 240, 8, 10, 4, 2), (40, 480, 8, 2, 1, 2), (33, 500, 5, 5, 2, 2), (700, 120, 4, 5, 3, 1)]
 
 
 @pytest.mark.parametrize("T,E,k,n_group,topk_group,group_top", ROUTE_SIZES)
