@@ -395,6 +395,27 @@ def test_route_keys_that_differ_in_their_last_bits(E, n_group, score, bias):
     assert np.array_equal(ids, np.argsort(-key, axis=1, kind="stable")[:, :k])
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,n_group,topk_group", [(64, 8, 1, 1), (40, 4, 1, 1), (256, 8, 8, 4), (48, 6, 2, 1), (500, 16, 5, 3)])
+def test_route_bias_of_infinity(score, E, k, n_group, topk_group):
+    """A bias of -inf leaves an expert out while others are there, one of +inf puts it in front; neither
+    is seen in the gates."""
+    T = 300
+    rng = np.random.default_rng(E)
+    x, xv = dev(rng.standard_normal((T, E)), "fp32")
+    for value, some_of in (([-np.inf], 3), ([np.inf], 1), ([np.inf, -np.inf], 2)):
+        b = 0.05 * rng.standard_normal(E)
+        at = rng.choice(E, size=some_of * len(value), replace=False)
+        b[at] = np.repeat(value, some_of)
+        b, bv = dev(b, "fp32")
+        ids, gates = run_route(x, k, "fp32", b, score=score_code(score), n_group=n_group, topk_group=topk_group)
+        want, wg, margin = RO.route(xv, k, score, bv, n_group, topk_group)
+        clear = margin > 32 * F
+        assert clear.mean() >= 0.9 and np.array_equal(ids[clear], want[clear])
+        assert np.isfinite(gates).all()
+        near(gates[clear], wg[clear], F * (E / 16 + 64 + np.abs(xv).max() * 2) * wg[clear], "gates")
+
+
 def test_route_counts_are_added_and_streams_hold():
     x = torch.randn(1000, 48, generator=torch.Generator().manual_seed(2)).cuda()
     counts = torch.arange(48, dtype=torch.int32, device="cuda")
