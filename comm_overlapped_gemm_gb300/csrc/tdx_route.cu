@@ -360,14 +360,15 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
 #pragma unroll
   for (int i = 0; i < V; ++i) bias[i] = !holds || within + i >= per ? -INFINITY : biased ? p.bias[c0 + i] : 0.0f;
   const bool exact_words = sizeof(T) == 2 && !p.sigmoid && !biased;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * warps * kTokens;
-  int64_t t = (static_cast<int64_t>(blockIdx.x) * warps + warp) * kTokens + lane / L;
+  // T and a step are below 2^31 each: token numbers fit 32 bits
+  const uint32_t T_all = static_cast<uint32_t>(p.T), step = gridDim.x * warps * kTokens;
+  uint32_t t = (blockIdx.x * warps + warp) * kTokens + lane / L;
   float next[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) next[i] = -INFINITY;
-  if (t < p.T) load_logits<T, L, V>(static_cast<const T*>(p.logits) + t * p.ld, sub, c0, holds, E, kVector, next);
-  for (; t - lane / L < p.T; t += step) {
-    const bool live = t < p.T;
+  if (t < T_all) load_logits<T, L, V>(static_cast<const T*>(p.logits) + t * p.ld, sub, c0, holds, E, kVector, next);
+  for (; t - lane / L < T_all; t += step) {
+    const bool live = t < T_all;
     const T* row = static_cast<const T*>(p.logits) + t * p.ld;
     float f[V];   // logits, then keys
 #pragma unroll
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
         for (int i = 0; i < V; ++i) f[i] = holds && within + i < per ? token[c0 + i] : -INFINITY;
       }
     }
-    if (t + step < p.T) load_logits<T, L, V>(row + step * p.ld, sub, c0, holds, E, kVector, next);
+    if (t + step < T_all) load_logits<T, L, V>(row + step * p.ld, sub, c0, holds, E, kVector, next);
     float m = -INFINITY, sum = 1.0f;
     if (p.sigmoid) {
 #pragma unroll
