@@ -356,9 +356,15 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
   int* hist = clear_hist(p, sm);
   float* const stage = sm + warp * p.warp_floats;
   const bool biased = p.bias != nullptr;
-  float bias[V];
+  // the biases in the lanes' order, -inf past the end of a group
+  __shared__ __align__(16) float bias_of[L * V];
+  if (biased) {
+    if (threadIdx.x < L) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) bias[i] = !holds || within + i >= per ? -INFINITY : biased ? p.bias[c0 + i] : 0.0f;
+      for (int i = 0; i < V; ++i) bias_of[sub * V + i] = holds && within + i < per ? p.bias[c0 + i] : -INFINITY;
+    }
+    __syncthreads();
+  }
   const bool exact_words = sizeof(T) == 2 && !p.sigmoid && !biased;
   // T and a step are below 2^31 each: token numbers fit 32 bits
   const uint32_t T_all = static_cast<uint32_t>(p.T), step = gridDim.x * warps * kTokens;
@@ -393,6 +399,8 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
 #pragma unroll
       for (int i = 0; i < V; ++i) f[i] = sigmoid_rn(f[i]);
       if (biased) {
+        float bias[V];
+        read_lane(bias_of + sub * V, bias);
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = __fadd_rn(f[i], bias[i]);
       }
@@ -408,6 +416,8 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_k
           sum += f[i];
         }
         sum = lanes_sum<L>(sum);
+        float bias[V];
+        read_lane(bias_of + sub * V, bias);
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = __fadd_rn(__fdiv_rn(f[i], sum), bias[i]);
       } else if (!p.renorm) {
