@@ -326,18 +326,20 @@ __device__ __forceinline__ uint32_t lanes_top(uint32_t w) {
 // the next word of its sorted list (the best eight of sixteen: a lane that runs out of them sends the row to
 // route_row). What the words leave open are keys that agree in their leading bits: where neighbours do, the
 // exact keys of the choice and of the first word left out put them in order. Rows where the first two
-// left out agree with the last one taken go to route_row, as do rows with a NaN. bf16 logits that are compared as such fit into the leading bits.
+// left out agree with the last one taken go to route_row, as do rows with a NaN. bf16 logits that are
+// compared as such fit into the leading bits.
 // A group is a run of 2^n lanes (all of them where there are no groups); entries past its end hold -inf and
 // the word 0, which says that there is nothing.
 //
-// Bound by issue slots, not by HBM: 32768 tokens, softmax, 8 of 64 experts 7.6 us (146 warp instructions a
-// token; HBM 1.6 us), sigmoid with bias, 8 of 256 in 4 of 8 groups 28.8 us (737, of them 177 for scores: ids
+// Bound by issue slots, not by HBM: 32768 tokens, softmax, 8 of 64 experts 7.5 us (149 warp instructions a
+// token; HBM 1.6 us), sigmoid with bias, 8 of 256 in 4 of 8 groups 27.4 us (701, some 177 of them for scores: ids
 // have to be those of the definition, so that every sigmoid is an expf and a correctly rounded
-// reciprocal; 151 for the groups, 150 for the maxima, 42 for the sorted lists; HBM 5.3 us), 2.85 of 4
-// instructions a cycle. With 16 lanes of 16 experts for 256: 32.3 us, at half the blocks; three / five blocks
-// per SM 30.2 / 32.2 us; the maxima in a loop 33.0 us.
+// reciprocal; 150 for the groups, 150 for the maxima, 42 for the sorted lists; HBM 5.3 us), 2.85 of 4
+// instructions a cycle. Registers decide how much of that is reached: 64-bit token numbers 29.6 us, biases in
+// registers 27.8; with 16 lanes of 16 experts for 256 32.3, at half the blocks; three / five blocks per SM 30.2 /
+// 32.2; the maxima in a loop 33.0. 512 experts, sigmoid with bias, topk 16: 50.9 us at three blocks, 54.5 at two.
 template <typename T, int L, int V, int K, bool kVector>
-__global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 2) tdx_moe_route_rows_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 3) tdx_moe_route_rows_kernel(const __grid_constant__ RouteParams p) {
   constexpr int kTokens = 32 / L;
   constexpr int kLog = (V == 4 ? 2 : V == 8 ? 3 : 4) + (L == 8 ? 3 : L == 16 ? 4 : 5);
   constexpr uint32_t kLow = (1u << kLog) - 1u;
@@ -852,7 +854,7 @@ tdx_status launch_route_k(RouteParams& p, cudaStream_t st) {
   p.vector = p.per % V == 0 && aligned(p.logits, kBytes) && (p.ld * static_cast<int64_t>(sizeof(T))) % kBytes == 0;
   p.group_shift = group_lanes_log(p, V);
   if (p.n_group == 1) p.group_shift = L == 8 ? 3 : L == 16 ? 4 : 5;
-  const RouteShape at = route_shape(p.T, 32 / L, V <= 8 ? 4 : 2);
+  const RouteShape at = route_shape(p.T, 32 / L, V <= 8 ? 4 : 3);
   const size_t smem = route_smem(&p, at.block, p.vector ? 0 : 32 * V);
   return p.vector ? launch_rows(tdx_moe_route_rows_kernel<T, L, V, K, true>, at.grid, at.block, smem, st, p)
                   : launch_rows(tdx_moe_route_rows_kernel<T, L, V, K, false>, at.grid, at.block, smem, st, p);
@@ -870,9 +872,9 @@ bool route_fits(const RouteParams& p, int L, int V) {
 }
 
 // The smallest layout that holds the row: the maxima, sums and addresses are the same instructions for four
-// tokens of a warp as for one (32768 tokens, 64 experts 7.6 us, a warp per token 13.4). Up to a warp per
-// scheduler a whole warp's maximum in one instruction is sooner there than shuffles: 1 token 2.0 / 2.4 us, 600 tokens
-// 2.4 / 2.5, but 1024 3.4 / 2.5.
+// tokens of a warp as for one (32768 tokens, 64 experts 7.5 us, a warp per token 13.4). Up to a warp per
+// scheduler a whole warp's maximum in one instruction is sooner there than shuffles: 1 token 2.0 / 2.4 us, 600
+// tokens 2.4 / 2.5, but 1024 3.4 / 2.5.
 template <typename T>
 tdx_status launch_route(RouteParams& p, cudaStream_t st) {
   p.per = p.E / p.n_group;
