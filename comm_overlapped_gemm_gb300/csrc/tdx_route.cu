@@ -632,10 +632,12 @@ __device__ __forceinline__ void store_logits(T* x, int lane, int E, bool vector,
 // back by the lanes that hold the row, so that dlogits are written in whole lines and softmax over the
 // whole row needs no look at the chosen logits. Choices of the same expert add up in the order of their places.
 // 4 E (softmax over the row: 8 E) bytes and 8 topk bytes a token: 32768 tokens, softmax over 64 experts 4.9 us
-// (HBM 2.8), 500 experts 34 us (20; in lanes of consecutive experts, read one by one, 89), renormalised
-// sigmoid over 256 17 us (5.5), there bound by the warp's steps for one token.
+// (HBM 2.8), 128 experts 9.0 us (5.3), 500 experts 30 us (20; in lanes of consecutive experts, read one by one,
+// 89), renormalised sigmoid over 256 13.0 us (5.5), there bound by the latency of a warp's steps for its one
+// token: eight blocks per SM 13.0 us, four 16.7 (for 8 lanes a token more than the compiler's choice is slower:
+// 6.3 against 4.9).
 template <typename T, int L, int V>
-__global__ void __launch_bounds__(kThreads) tdx_moe_route_bwd_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(kThreads, L == 32 ? (V <= 8 ? 8 : 4) : L == 16 ? 6 : 1) tdx_moe_route_bwd_kernel(const __grid_constant__ RouteParams p) {
   constexpr int kTokens = 32 / L;
   constexpr int R = kMoeMaxTopk > L ? kMoeMaxTopk / L : 1;
   __shared__ __align__(16) float rows[kWarps * 32 * V];
@@ -646,9 +648,10 @@ __global__ void __launch_bounds__(kThreads) tdx_moe_route_bwd_kernel(const __gri
   const int E = p.E;
   const bool dense = !p.sigmoid && !p.renorm;
   griddep_wait();
-  for (int64_t t = (static_cast<int64_t>(blockIdx.x) * warps + warp) * kTokens + lane / L; t - lane / L < p.T;
-       t += static_cast<int64_t>(gridDim.x) * warps * kTokens) {
-    const bool live = t < p.T;
+  const uint32_t T_all = static_cast<uint32_t>(p.T), step = gridDim.x * warps * kTokens;   // each below 2^31
+  for (uint32_t t = (blockIdx.x * warps + warp) * kTokens + lane / L; t - lane / L < T_all; t += step) {
+    const bool live = t < T_all;
+    const int64_t at = static_cast<int64_t>(t) * p.k;
     const T* x = static_cast<const T*>(p.logits) + t * p.ld;
     float e[V];   // softmax over the row: logits, then exponentials
 #pragma unroll
@@ -663,11 +666,11 @@ __global__ void __launch_bounds__(kThreads) tdx_moe_route_bwd_kernel(const __gri
       d[r] = 0.0f;
       v[r] = -INFINITY;
       if (live && j < p.k) {
-        id[r] = p.idx[t * p.k + j];
+        id[r] = p.idx[at + j];
         if (id[r] < 0 || id[r] >= E) id[r] = -1;
       }
       if (id[r] >= 0) {
-        d[r] = p.dgates[t * p.k + j] * p.scale;
+        d[r] = p.dgates[at + j] * p.scale;
         if (!dense) v[r] = to_float(x[id[r]]);
       }
     }
