@@ -98,11 +98,12 @@ __device__ __forceinline__ void finish_row(const RouteParams& p, int64_t t, int 
   }
 }
 
-// Load V logits of a row held by L lanes, -inf past the end. `vector`: the lane's V consecutive ones (columns c
+// Load V logits of a row held by L lanes, `pad` past the end. `vector`: the lane's V consecutive ones (columns c
 // on, if it holds any) in words of 16 bytes at most; else columns lane, lane + L, ..., so that odd row
 // lengths and addresses are read in whole lines too.
 template <typename T, int L, int V>
-__device__ __forceinline__ void load_logits(const T* x, int lane, int c, bool holds, int E, bool vector, float (&v)[V]) {
+__device__ __forceinline__ void load_logits(const T* x, int lane, int c, bool holds, int E, bool vector, float pad,
+                                            float (&v)[V]) {
   constexpr int kBytes = V * static_cast<int>(sizeof(T));
   if (vector && holds) {
     if constexpr (kBytes >= 16) {
@@ -134,7 +135,7 @@ __device__ __forceinline__ void load_logits(const T* x, int lane, int c, bool ho
     }
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = !vector && lane + i * L < E ? to_float(x[lane + i * L]) : -INFINITY;
+  for (int i = 0; i < V; ++i) v[i] = !vector && lane + i * L < E ? to_float(x[lane + i * L]) : pad;
 }
 
 // One row by one warp, from the definition's own steps: the row's scores and keys in shared memory, 2 E
@@ -358,12 +359,15 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 3) tdx_moe_route_rows_k
   int* hist = clear_hist(p, sm);
   float* const stage = sm + warp * p.warp_floats;
   const bool biased = p.bias != nullptr;
-  // the biases in the lanes' order, -inf past the end of a group
+  // the biases in the lanes' order, -inf past the end of a group. Logits there are 0 where scores are sigmoids:
+  // the reciprocal of 1 + exp(inf) takes a slow path in the whole warp (384 experts, sigmoid: 41 against 56 us)
   __shared__ __align__(16) float bias_of[L * V];
-  if (biased) {
+  const float pad = p.sigmoid ? 0.0f : -INFINITY;
+  if (biased || p.sigmoid) {
     if (threadIdx.x < L) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) bias_of[sub * V + i] = holds && within + i < per ? p.bias[c0 + i] : -INFINITY;
+      for (int i = 0; i < V; ++i)
+        bias_of[sub * V + i] = !holds || within + i >= per ? -INFINITY : biased ? p.bias[c0 + i] : 0.0f;
     }
     __syncthreads();
   }
@@ -373,8 +377,8 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 3) tdx_moe_route_rows_k
   uint32_t t = (blockIdx.x * warps + warp) * kTokens + lane / L;
   float next[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) next[i] = -INFINITY;
-  if (t < T_all) load_logits<T, L, V>(static_cast<const T*>(p.logits) + t * p.ld, sub, c0, holds, E, kVector, next);
+  for (int i = 0; i < V; ++i) next[i] = pad;
+  if (t < T_all) load_logits<T, L, V>(static_cast<const T*>(p.logits) + t * p.ld, sub, c0, holds, E, kVector, pad, next);
   for (; t - lane / L < T_all; t += step) {
     const bool live = t < T_all;
     const T* row = static_cast<const T*>(p.logits) + t * p.ld;
@@ -392,20 +396,18 @@ __global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 3) tdx_moe_route_rows_k
         read_lane(token + sub * V, f);
       } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = holds && within + i < per ? token[c0 + i] : -INFINITY;
+        for (int i = 0; i < V; ++i) f[i] = holds && within + i < per ? token[c0 + i] : pad;
       }
     }
-    if (t + step < T_all) load_logits<T, L, V>(row + step * p.ld, sub, c0, holds, E, kVector, next);
+    if (t + step < T_all) load_logits<T, L, V>(row + step * p.ld, sub, c0, holds, E, kVector, pad, next);
     float m = -INFINITY, sum = 1.0f;
     if (p.sigmoid) {
 #pragma unroll
       for (int i = 0; i < V; ++i) f[i] = sigmoid_rn(f[i]);
-      if (biased) {
-        float bias[V];
-        read_lane(bias_of + sub * V, bias);
+      float bias[V];
+      read_lane(bias_of + sub * V, bias);
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = __fadd_rn(f[i], bias[i]);
-      }
+      for (int i = 0; i < V; ++i) f[i] = __fadd_rn(f[i], bias[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) m = fmaxf(m, f[i]);
@@ -656,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, L == 32 ? (V <= 8 ? 8 : 4) : L == 16
     float e[V];   // softmax over the row: logits, then exponentials
 #pragma unroll
     for (int i = 0; i < V; ++i) e[i] = -INFINITY;
-    if (dense && live) load_logits<T, L, V>(x, sub, sub * V, sub * V < E, E, p.vector, e);
+    if (dense && live) load_logits<T, L, V>(x, sub, sub * V, sub * V < E, E, p.vector, -INFINITY, e);
     int id[R];
     float d[R], v[R];
 #pragma unroll
