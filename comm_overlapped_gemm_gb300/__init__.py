@@ -149,9 +149,10 @@ _lib = _load()
 def _ptr(x) -> int:
     if x is None:
         return 0
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return x   # a device pointer already
 
 
 def _nbytes(x) -> int:
