@@ -80,7 +80,9 @@ __device__ __forceinline__ float row_scale(float m, float rstd, float* inv, floa
 // between two sums.
 // Registers: 64 a thread for 32 bf16 elements, so that four blocks of 224 threads share an SM instead of three
 // (1024 x 7168 to e4m3 11.2 / 11.7 us; five, at 48 registers, spill: 13.8).
-template <typename T, typename O, int E, int kLanes>
+// kSum: there may be a residual. Without one the row waits for its sum as it was read, not in fp32: 6960 x 7184
+// bf16 86% of a copy's rate, in fp32 78%.
+template <typename T, typename O, int E, int kLanes, bool kSum>
 __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && sizeof(T) == 2 && E == 32 ? 2 : 1) tdx_rmsnorm_rows_kernel(const __grid_constant__ NormParams p) {
   constexpr int N = kVec<T>;
   constexpr int V = E / N;
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && size
   for (int i = 0; i < V; ++i) {
     if (at + i * width * N < H) {
       qx[i] = __ldcs(reinterpret_cast<const uint4*>(x + i * width * N));
-      if (p.residual != nullptr) qr[i] = __ldcs(reinterpret_cast<const uint4*>(r + i * width * N));
+      if (kSum && p.residual != nullptr) qr[i] = __ldcs(reinterpret_cast<const uint4*>(r + i * width * N));
       qw[i] = *reinterpret_cast<const uint4*>(w + i * width * N);
     }
   }
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && size
   for (int i = 0; i < V; ++i) {
     if (at + i * width * N < H) {
       unpack(qx[i], v[i], T{});
-      if (p.residual != nullptr) {
+      if (kSum && p.residual != nullptr) {
         float a[N];
         unpack(qr[i], a, T{});
 #pragma unroll
@@ -151,6 +153,15 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && size
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if (at + i * width * N < H) {
+      if (!kSum) {
+        // the products again (the compiler is kept from holding on to them)
+        asm volatile("" : "+r"(qx[i].x), "+r"(qx[i].y), "+r"(qx[i].z), "+r"(qx[i].w));
+        float g[N];
+        unpack(qx[i], v[i], T{});
+        unpack(qw[i], g, T{});
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[i][k] *= g[k];
+      }
 #pragma unroll
       for (int k = 0; k < N; ++k) v[i][k] = v[i][k] * up * inv;
       store_vec(y + i * width * N, v[i]);
@@ -465,8 +476,14 @@ bool raise_smem(K kernel, int bytes, std::atomic<bool>* done) {
 template <typename T, typename O, int E, int kLanes>
 tdx_status launch_norm_lanes(const NormParams& p, cudaStream_t st) {
   const int rows = kThreads / kLanes;
-  return launch_rows(tdx_rmsnorm_rows_kernel<T, O, E, kLanes>,
+  return launch_rows(tdx_rmsnorm_rows_kernel<T, O, E, kLanes, true>,
                      static_cast<unsigned>((static_cast<int64_t>(p.T) + rows - 1) / rows), kThreads, 0, st, p);
+}
+
+template <typename T, typename O, int E, bool kSum>
+tdx_status launch_norm_block(const NormParams& p, cudaStream_t st) {
+  const unsigned block = static_cast<unsigned>((p.H + 32 * E - 1) / (32 * E) * 32);
+  return launch_rows(tdx_rmsnorm_rows_kernel<T, O, E, 0, kSum>, p.T, block, 0, st, p);
 }
 
 template <typename T, typename O>
@@ -477,11 +494,12 @@ tdx_status launch_norm_t(const NormParams& p, cudaStream_t st) {
   if (p.H <= 512) return launch_norm_lanes<T, O, 16, 32>(p, st);
   if (p.H <= 1024) return launch_norm_lanes<T, O, 32, 32>(p, st);
   if (p.H <= 16384) {
-    // up to one row per SM, 16 elements a thread shorten the row; beyond, 32 carry more loads per block:
-    // 1 x 8192 2.0 / 2.2 us, 32768 x 7168 293 / 271 us
-    auto block = [&](int e) { return static_cast<unsigned>((p.H + 32 * e - 1) / (32 * e) * 32); };
-    if (p.T <= sm_count()) return launch_rows(tdx_rmsnorm_rows_kernel<T, O, 16, 0>, p.T, block(16), 0, st, p);
-    return launch_rows(tdx_rmsnorm_rows_kernel<T, O, 32, 0>, p.T, block(32), 0, st, p);
+    // 32 elements a thread carry more loads per block of bf16 rows (32768 x 7168 with the residual 271 us, with 16
+    // 293); fp32 rows take 16 (48076 x 1040 without a residual 80% of a copy's rate, with 32 60%), as do up to one
+    // row per SM (1 x 8192 bf16 2.0 us, with 32 2.2)
+    const bool wide = sizeof(T) == 2 && p.T > sm_count();
+    if (p.residual != nullptr) return wide ? launch_norm_block<T, O, 32, true>(p, st) : launch_norm_block<T, O, 16, true>(p, st);
+    return wide ? launch_norm_block<T, O, 32, false>(p, st) : launch_norm_block<T, O, 16, false>(p, st);
   }
   return launch_rows(tdx_rmsnorm_kernel<T, O>, p.T, kLong, 0, st, p);
 }
