@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && size
   T* h = static_cast<T*>(p.h) + t * p.ld_h + at;
   O* y = static_cast<O*>(p.y) + t * p.ld_y + at;
   uint4 qx[V], qr[V], qw[V];
-  float v[V][N];
+  f32x2 v[V][N / 2];
   griddep_wait();
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -112,28 +112,34 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && size
     }
   }
   const bool scaled = p.row_scale != nullptr;
-  float ss = 0.0f, m = 0.0f;
+  f32x2 ss2 = pair(0.0f, 0.0f);
+  float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if (at + i * width * N < H) {
       unpack(qx[i], v[i], T{});
       if (kSum && p.residual != nullptr) {
-        float a[N];
+        f32x2 a[N / 2];
         unpack(qr[i], a, T{});
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[i][k] += a[k];
+        for (int k = 0; k < N / 2; ++k) v[i][k] = add2(v[i][k], a[k]);
         if (p.h != nullptr) store_vec(h + i * width * N, v[i]);
       }
-      float g[N];
-      unpack(qw[i], g, T{});
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        ss = fmaf(v[i][k], v[i][k], ss);
-        v[i][k] *= g[k];
-        m = fmaxf(m, fabsf(v[i][k]));
+      for (int k = 0; k < N / 2; ++k) ss2 = fma2(v[i][k], v[i][k], ss2);
+      if (kSum || scaled) {
+        f32x2 g[N / 2];
+        unpack(qw[i], g, T{});
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) v[i][k] = mul2(v[i][k], g[k]);
+      }
+      if (scaled) {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) m = fmaxf(m, fmaxf(fabsf(first(v[i][k])), fabsf(second(v[i][k]))));
       }
     }
   }
+  float ss = first(ss2) + second(ss2);
   ss = lanes_sum<kLanes ? kLanes : 32>(ss);
   if (scaled) m = lanes_max<kLanes ? kLanes : 32>(m);
   if (!kLanes) {
@@ -156,14 +162,18 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && size
       if (!kSum) {
         // the products again (the compiler is kept from holding on to them)
         asm volatile("" : "+r"(qx[i].x), "+r"(qx[i].y), "+r"(qx[i].z), "+r"(qx[i].w));
-        float g[N];
+        f32x2 g[N / 2];
         unpack(qx[i], v[i], T{});
         unpack(qw[i], g, T{});
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[i][k] *= g[k];
+        for (int k = 0; k < N / 2; ++k) v[i][k] = mul2(v[i][k], g[k]);
+      }
+      if (up != 1.0f) {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) v[i][k] = mul2(v[i][k], pair(up, up));
       }
 #pragma unroll
-      for (int k = 0; k < N; ++k) v[i][k] = v[i][k] * up * inv;
+      for (int k = 0; k < N / 2; ++k) v[i][k] = mul2(v[i][k], pair(inv, inv));
       store_vec(y + i * width * N, v[i]);
     }
   }

@@ -40,6 +40,38 @@ __device__ __forceinline__ void unpack(const uint4& q, float (&v)[4], float) {
   v[2] = __uint_as_float(q.z);
   v[3] = __uint_as_float(q.w);
 }
+// Two fp32 values in a register pair: one instruction for both (each rounded as the scalar one rounds)
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float first(f32x2 a) { return __uint_as_float(static_cast<uint32_t>(a)); }
+__device__ __forceinline__ float second(f32x2 a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+template <int N, typename T>
+__device__ __forceinline__ void unpack(const uint4& q, f32x2 (&v)[N], T) {
+  float f[2 * N];
+  unpack(q, f, T{});
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = pair(f[2 * i], f[2 * i + 1]);
+}
+
 template <typename T>
 __device__ __forceinline__ void load_vec(const T* p, float (&v)[kVec<T>]) {
   unpack(*reinterpret_cast<const uint4*>(p), v, T{});
@@ -76,6 +108,17 @@ __device__ __forceinline__ void store_vec(e4m3* p, const float (&v)[4]) {
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(bf16 v) { return __bfloat162float(v); }
+
+template <int N, typename O>
+__device__ __forceinline__ void store_vec(O* p, const f32x2 (&v)[N]) {
+  float f[2 * N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    f[2 * i] = first(v[i]);
+    f[2 * i + 1] = second(v[i]);
+  }
+  store_vec(p, f);
+}
 
 // Sum and maximum over groups of L consecutive lanes (a power of two); every lane of the warp takes part
 template <int L>
