@@ -37,7 +37,7 @@ struct NormParams {
   float* rstd;
   int T, H;
   int64_t ld_x, ld_r, ld_h, ld_y;
-  float eps, inv_scale;
+  float eps, inv_scale, inv_h;   // inv_h = 1 / H
 };
 
 // Sum (or maximum) over the block; every thread gets it.
@@ -54,16 +54,18 @@ __device__ float block_reduce(float v, float* sm) {
 }
 
 // The e4m3 scale of a row, max|y| / 448 (1 where that is 0 or no number), from m = max|h * weight|, and the factors
-// that take h * weight to codes: y / scale = h * weight * 448 / m, the numbers of rows near the smallest
-// float first multiplied by a power of two, so that 448 / m stays finite.
+// that take h * weight to codes: y / scale = h * weight * 448 / m, the numbers of rows near the ends of fp32's
+// range first multiplied by a power of two, so that 448 / m stays finite and is no subnormal. Every thread
+// computes this: the approximate quotient and rsqrtf (2 ulp each) keep it short.
 __device__ __forceinline__ float row_scale(float m, float rstd, float* inv, float* up) {
-  const float s = m * rstd / 448.0f;
+  const float s = m * rstd * (1.0f / 448.0f);
   if (!(s > 0.0f)) {
     *inv = rstd;
     return 1.0f;
   }
   if (m < 1e-30f) *up = 0x1p100f;
-  *inv = 448.0f / (m * *up);
+  if (m > 1e30f) *up = 0x1p-100f;
+  *inv = __fdividef(448.0f, m * *up);
   return s;
 }
 
@@ -72,16 +74,17 @@ __device__ __forceinline__ float row_scale(float m, float rstd, float* inv, floa
 // product with rstd is max|y|, one write of h and y.
 // kLanes 8, 16, 32: that many lanes of a warp per row (short rows; the reduction is shuffles alone); 0: a
 // block per row, whose reduction takes one barrier.
-// Bound by HBM: 32768 x 7168 bf16 with the residual 271 us (6.9 TB/s, a plain copy's rate 281), 1000000 x
+// Bound by HBM: 32768 x 7168 bf16 with the residual 268 us (7.0 TB/s, a plain copy's rate 281), 1000000 x
 // 128 152 us (6.9 TB/s; with a warp per row of 128, half of its lanes idle, 200 us). 1024 x 7168 to e4m3 with
-// row scales takes 11.2 us of 7.7: the launch's ramp and tail (a plain addition over as many bytes takes 9.0).
+// row scales takes 10.6 us of 7.7: the launch's ramp and tail (a plain addition over as many bytes takes 9.0).
 // Rows through a ring of cp.async stages in shared memory, as the gradient takes them, came out slower
 // here (311 us): the many independent blocks keep more loads in flight than one block per SM does
 // between two sums.
 // Registers: 64 a thread for 32 bf16 elements, so that four blocks of 224 threads share an SM instead of three
-// (1024 x 7168 to e4m3 11.2 / 11.7 us; five, at 48 registers, spill: 13.8).
+// (1024 x 7168 to e4m3 11.2 / 11.7 us at the time; five, at 48 registers, spill: 13.8).
 // kSum: there may be a residual. Without one the row waits for its sum as it was read, not in fp32: 6960 x 7184
-// bf16 86% of a copy's rate, in fp32 78%.
+// bf16 91% of a copy's rate (in fp32, before the sums were taken two at a time and rsqrtf, 78%; now bound by issue
+// slots, as is the e4m3 output there, 67%).
 template <typename T, typename O, int E, int kLanes, bool kSum>
 __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && sizeof(T) == 2 && E == 32 ? 2 : 1) tdx_rmsnorm_rows_kernel(const __grid_constant__ NormParams p) {
   constexpr int N = kVec<T>;
@@ -149,7 +152,7 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && size
     ss = warp_sum(a.x);
     if (scaled) m = warp_max(a.y);
   }
-  const float rstd = 1.0f / sqrtf(ss / static_cast<float>(p.H) + p.eps);
+  const float rstd = rsqrtf(fmaf(ss, p.inv_h, p.eps));
   float inv = rstd * p.inv_scale, up = 1.0f;
   if (scaled) {
     const float s = row_scale(m, rstd, &inv, &up);
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(kLong) tdx_rmsnorm_kernel(const __grid_constan
     for (int i = 0; i < N; ++i) ss = fmaf(v[i], v[i], ss);
   }
   ss = block_reduce<false, kLong>(ss, sm);
-  const float rstd = 1.0f / sqrtf(ss / static_cast<float>(p.H) + p.eps);
+  const float rstd = rsqrtf(fmaf(ss, p.inv_h, p.eps));
   float inv = rstd * p.inv_scale, up = 1.0f;
   if (p.row_scale != nullptr) {
     float m = 0.0f;
@@ -504,7 +507,7 @@ tdx_status launch_norm_t(const NormParams& p, cudaStream_t st) {
   if (p.H <= 512) return launch_norm_lanes<T, O, 16, 32>(p, st);
   if (p.H <= 1024) return launch_norm_lanes<T, O, 32, 32>(p, st);
   if (p.H <= 16384) {
-    // 32 elements a thread carry more loads per block of bf16 rows (32768 x 7168 with the residual 271 us, with 16
+    // 32 elements a thread carry more loads per block of bf16 rows (32768 x 7168 with the residual 268 us, with 16
     // 293); fp32 rows take 16 (48076 x 1040 without a residual 80% of a copy's rate, with 32 60%), as do up to one
     // row per SM (1 x 8192 bf16 2.0 us, with 32 2.2)
     const bool wide = sizeof(T) == 2 && p.T > sm_count();
@@ -624,6 +627,7 @@ tdx_status tdx_rmsnorm(const void* x, const void* residual, const void* weight, 
   p.T = T;
   p.H = H;
   p.eps = o.eps;
+  p.inv_h = 1.0f / static_cast<float>(H);
   p.inv_scale = o.out_dtype == TDX_FP8_E4M3 ? 1.0f / o.out_scale : 1.0f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return dtype == TDX_BF16 ? launch_norm<bf16>(o.out_dtype, p, st) : launch_norm<float>(o.out_dtype, p, st);
