@@ -33,7 +33,7 @@ __device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __e
 
 // i / d as the high half of i * ceil(2^64 / d): exact as long as i * (the product of d and that - 2^64) < 2^64,
 // that is i < 2^37 for d up to 2^27
-__host__ uint64_t magic_of(int d) { return d == 1 ? 0 : ~UINT64_C(0) / d + 1; }
+uint64_t magic_of(int d) { return d == 1 ? 0 : ~UINT64_C(0) / d + 1; }
 __device__ __forceinline__ int64_t divide(int64_t i, uint64_t magic) {
   return magic != 0 ? static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(i), magic)) : i;
 }
@@ -171,8 +171,8 @@ template <typename T, typename O, int V>
 tdx_status launch_act_v(const ActParams& p, cudaStream_t st) {
   const unsigned grid = act_grid(p, V);
   if (p.dest == nullptr) return launch_rows(tdx_swiglu_kernel<T, O, V, false>, grid, kThreads, 0, st, p);
-  return launch_rows(tdx_swiglu_kernel<T, O, V, true>, std::min(grid, static_cast<unsigned>(act_sms() * kDestBlocks)), kThreads, 0, st,
-                     p);
+  const unsigned most = static_cast<unsigned>(act_sms() * kDestBlocks);
+  return launch_rows(tdx_swiglu_kernel<T, O, V, true>, std::min(grid, most), kThreads, 0, st, p);
 }
 
 template <typename T, typename O>

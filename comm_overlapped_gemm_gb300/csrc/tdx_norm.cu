@@ -25,7 +25,7 @@ constexpr int kThreads = 256;
 // Threads of the kernels for long rows. 256 / 512 / 1024: forwards 4000 x 32768 bf16 225 / 186 / 200 us, 4000 x
 // 20000 to e4m3 117 / 101 / 189; backwards 5000 x 10000 fp32 882 / 262 / 185, 4000 x 32768 bf16 648 / 397 / 284
 constexpr int kLong = 512, kLongBwd = 1024;
-constexpr int kBwdParts = 304;   // most row groups whose partial weight gradients are added at the end
+constexpr int kBwdParts = 304;   // most row groups whose partial weight gradients are added at the end, long rows
 
 struct NormParams {
   const void* x;
@@ -86,7 +86,8 @@ __device__ __forceinline__ float row_scale(float m, float rstd, float* inv, floa
 // bf16 91% of a copy's rate (in fp32, before the sums were taken two at a time and rsqrtf, 78%; now bound by issue
 // slots, as is the e4m3 output there, 67%).
 template <typename T, typename O, int E, int kLanes, bool kSum>
-__global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && sizeof(T) == 2 && E == 32 ? 2 : 1) tdx_rmsnorm_rows_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && sizeof(T) == 2 && E == 32 ? 2 : 1)
+    tdx_rmsnorm_rows_kernel(const __grid_constant__ NormParams p) {
   constexpr int N = kVec<T>;
   constexpr int V = E / N;
   __shared__ float2 sm[32];
@@ -261,7 +262,8 @@ struct NormBwdParams {
 // 45 us (40). Ring depth 2 / 3 / 4 at 16381 x 8192: 158 (32 columns a thread) / 157 / 158 us. Two blocks of
 // 512 threads per SM, at 64 registers, spill: 223 us.
 template <typename T, int E, int kStages, int kMaxThreads, int kBlocks, int kLanes>
-__global__ void __launch_bounds__(kMaxThreads, kBlocks) tdx_rmsnorm_bwd_rows_kernel(const __grid_constant__ NormBwdParams p) {
+__global__ void __launch_bounds__(kMaxThreads, kBlocks)
+    tdx_rmsnorm_bwd_rows_kernel(const __grid_constant__ NormBwdParams p) {
   constexpr int N = kVec<T>;
   constexpr int V = E / N;
   extern __shared__ uint4 ring[];   // [stage][dy, h, dres][vector][thread]
@@ -306,7 +308,8 @@ __global__ void __launch_bounds__(kMaxThreads, kBlocks) tdx_rmsnorm_bwd_rows_ker
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     qw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (at + i * width * N < p.H) qw[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.weight) + at + i * width * N);
+    if (at + i * width * N < p.H)
+      qw[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.weight) + at + i * width * N);
     if (kWeightApart) apart[i * blockDim.x] = qw[i];
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[i][k] = 0.0f;
@@ -447,8 +450,8 @@ __global__ void __launch_bounds__(kLongBwd) tdx_rmsnorm_bwd_kernel(const __grid_
     for (int i = 0; i < N; ++i) out[c + i] = dw[c + i];
 }
 
-// dweight[c] = the sum of column c's partial sums (5 MB at most up to H = 16384, in L2): warp w adds the row groups w, w + 32, ... of 64 columns,
-// the warps' sums follow in order.
+// dweight[c] = the sum of column c's partial sums (5 MB at most up to H = 8192, 10 up to 16384, in L2): warp w adds
+// the row groups w, w + 32, ... of 64 columns, the warps' sums follow in order.
 __global__ void __launch_bounds__(1024) tdx_rmsnorm_dweight_kernel(const float* part, float* dweight, int parts, int H) {
   __shared__ float2 sm[32][33];
   griddep_launch_dependents();
@@ -511,7 +514,8 @@ tdx_status launch_norm_t(const NormParams& p, cudaStream_t st) {
     // 293); fp32 rows take 16 (48076 x 1040 without a residual 80% of a copy's rate, with 32 60%), as do up to one
     // row per SM (1 x 8192 bf16 2.0 us, with 32 2.2)
     const bool wide = sizeof(T) == 2 && p.T > sm_count();
-    if (p.residual != nullptr) return wide ? launch_norm_block<T, O, 32, true>(p, st) : launch_norm_block<T, O, 16, true>(p, st);
+    if (p.residual != nullptr)
+      return wide ? launch_norm_block<T, O, 32, true>(p, st) : launch_norm_block<T, O, 16, true>(p, st);
     return wide ? launch_norm_block<T, O, 32, false>(p, st) : launch_norm_block<T, O, 16, false>(p, st);
   }
   return launch_rows(tdx_rmsnorm_kernel<T, O>, p.T, kLong, 0, st, p);
@@ -530,7 +534,9 @@ tdx_status launch_norm(tdx_dtype out, const NormParams& p, cudaStream_t st) {
 // where a block takes a row, 16 elements a thread (24224 x 2064 bf16: 93% of a copy's rate with three blocks of 160
 // threads, 69% with two)
 constexpr int bwd_block(int H, int e) { return (H + 32 * e - 1) / (32 * e) * 32; }
-constexpr int bwd_blocks(int H) { return H <= 256 ? 4 : H <= 512 ? 2 : H <= 1024 ? 1 : H <= 8192 ? 512 / bwd_block(H, 16) : 1; }
+constexpr int bwd_blocks(int H) {
+  return H <= 256 ? 4 : H <= 512 ? 2 : H <= 1024 ? 1 : H <= 8192 ? 512 / bwd_block(H, 16) : 1;
+}
 // Most row groups whose partial sums of dweight are added at the end: what the workspace holds
 constexpr int bwd_most_parts(int H) { return H <= 16384 ? 152 * bwd_blocks(H) : kBwdParts; }
 

@@ -340,7 +340,8 @@ __device__ __forceinline__ uint32_t lanes_top(uint32_t w) {
 // registers 27.8; with 16 lanes of 16 experts for 256 32.3, at half the blocks; three / five blocks per SM 30.2 /
 // 32.2; the maxima in a loop 33.0. 512 experts, sigmoid with bias, topk 16: 50.9 us at three blocks, 54.5 at two.
 template <typename T, int L, int V, int K, bool kVector>
-__global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 3) tdx_moe_route_rows_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : 3)
+    tdx_moe_route_rows_kernel(const __grid_constant__ RouteParams p) {
   constexpr int kTokens = 32 / L;
   constexpr int kLog = (V == 4 ? 2 : V == 8 ? 3 : 4) + (L == 8 ? 3 : L == 16 ? 4 : 5);
   constexpr uint32_t kLow = (1u << kLog) - 1u;
@@ -639,7 +640,8 @@ __device__ __forceinline__ void store_logits(T* x, int lane, int E, bool vector,
 // token: eight blocks per SM 13.0 us, four 16.7 (for 8 lanes a token more than the compiler's choice is slower:
 // 6.3 against 4.9).
 template <typename T, int L, int V>
-__global__ void __launch_bounds__(kThreads, L == 32 ? (V <= 8 ? 8 : 4) : L == 16 ? 6 : 1) tdx_moe_route_bwd_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(kThreads, L == 32 ? (V <= 8 ? 8 : 4) : L == 16 ? 6 : 1)
+    tdx_moe_route_bwd_kernel(const __grid_constant__ RouteParams p) {
   constexpr int kTokens = 32 / L;
   constexpr int R = kMoeMaxTopk > L ? kMoeMaxTopk / L : 1;
   __shared__ __align__(16) float rows[kWarps * 32 * V];
