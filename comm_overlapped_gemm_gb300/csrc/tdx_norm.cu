@@ -53,16 +53,14 @@ __device__ float block_reduce(float v, float* sm) {
   return r;
 }
 
-// The e4m3 scale of a row, max|y| / 448 (1 where that is 0 or no number), from m = max|h * weight|, and the factors
-// that take h * weight to codes: y / scale = h * weight * 448 / m, the numbers of rows near the ends of fp32's
-// range first multiplied by a power of two, so that 448 / m stays finite and is no subnormal. Every thread
-// computes this: the approximate quotient and rsqrtf (2 ulp each) keep it short.
-__device__ __forceinline__ float row_scale(float m, float rstd, float* inv, float* up) {
-  const float s = m * rstd * (1.0f / 448.0f);
-  if (!(s > 0.0f)) {
-    *inv = rstd;
-    return 1.0f;
-  }
+// The e4m3 scale of a row, m / 448 from m = max|y| (1 where that is 0 or no number), and the factors that take y to
+// codes, y * up * inv. The numbers of rows near the ends of fp32's range are first multiplied by a power of two, so
+// that 448 / m stays finite and is no subnormal. Every thread computes this: the approximate quotient (2 ulp, for a
+// divisor up to 2^126) keeps it short.
+__device__ __forceinline__ float row_scale(float m, float* inv, float* up) {
+  const float s = m * (1.0f / 448.0f);
+  *inv = 1.0f;
+  if (!(s > 0.0f)) return 1.0f;
   if (m < 1e-30f) *up = 0x1p100f;
   if (m > 1e30f) *up = 0x1p-100f;
   *inv = __fdividef(448.0f, m * *up);
@@ -70,22 +68,22 @@ __device__ __forceinline__ float row_scale(float m, float rstd, float* inv, floa
 }
 
 // A row held in registers, E of its elements per thread in 16-byte vectors: one read of x and residual,
-// one reduction for the sum of squares and (where the row's scale is wanted) max|h * weight|, whose
+// one reduction for the sum of squares and (kScaled: row scales are wanted) max|h * weight|, whose
 // product with rstd is max|y|, one write of h and y.
 // kLanes 8, 16, 32: that many lanes of a warp per row (short rows; the reduction is shuffles alone); 0: a
 // block per row, whose reduction takes one barrier.
 // Bound by HBM: 32768 x 7168 bf16 with the residual 268 us (7.0 TB/s, a plain copy's rate 281), 1000000 x
 // 128 152 us (6.9 TB/s; with a warp per row of 128, half of its lanes idle, 200 us). 1024 x 7168 to e4m3 with
-// row scales takes 10.6 us of 7.7: the launch's ramp and tail (a plain addition over as many bytes takes 9.0).
+// row scales takes 10.2 us of 7.7: the launch's ramp and tail (a plain addition over as many bytes takes 9.0).
 // Rows through a ring of cp.async stages in shared memory, as the gradient takes them, came out slower
 // here (311 us): the many independent blocks keep more loads in flight than one block per SM does
 // between two sums.
 // Registers: 64 a thread for 32 bf16 elements, so that four blocks of 224 threads share an SM instead of three
 // (1024 x 7168 to e4m3 11.2 / 11.7 us at the time; five, at 48 registers, spill: 13.8).
 // kSum: there may be a residual. Without one the row waits for its sum as it was read, not in fp32: 6960 x 7184
-// bf16 91% of a copy's rate (in fp32, before the sums were taken two at a time and rsqrtf, 78%; now bound by issue
-// slots, as is the e4m3 output there, 67%).
-template <typename T, typename O, int E, int kLanes, bool kSum>
+// bf16 93% of a copy's rate (in fp32, before the sums were taken two at a time and rsqrtf, 78%; now bound by issue
+// slots, as are the codes there, 75%).
+template <typename T, typename O, int E, int kLanes, bool kSum, bool kScaled>
 __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && sizeof(T) == 2 && E == 32 ? 2 : 1)
     tdx_rmsnorm_rows_kernel(const __grid_constant__ NormParams p) {
   constexpr int N = kVec<T>;
@@ -103,7 +101,6 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && size
   const T* r = static_cast<const T*>(p.residual) + t * p.ld_r + at;
   const T* w = static_cast<const T*>(p.weight) + at;
   T* h = static_cast<T*>(p.h) + t * p.ld_h + at;
-  O* y = static_cast<O*>(p.y) + t * p.ld_y + at;
   uint4 qx[V], qr[V], qw[V];
   f32x2 v[V][N / 2];
   griddep_wait();
@@ -115,9 +112,8 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && size
       qw[i] = *reinterpret_cast<const uint4*>(w + i * width * N);
     }
   }
-  const bool scaled = p.row_scale != nullptr;
   f32x2 ss2 = pair(0.0f, 0.0f);
-  float m = 0.0f;
+  float m = 0.0f;   // max|h * weight|
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if (at + i * width * N < H) {
@@ -131,54 +127,98 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && size
       }
 #pragma unroll
       for (int k = 0; k < N / 2; ++k) ss2 = fma2(v[i][k], v[i][k], ss2);
-      if (kSum || scaled) {
+      if (kScaled) {
         f32x2 g[N / 2];
         unpack(qw[i], g, T{});
 #pragma unroll
-        for (int k = 0; k < N / 2; ++k) v[i][k] = mul2(v[i][k], g[k]);
-      }
-      if (scaled) {
-#pragma unroll
-        for (int k = 0; k < N / 2; ++k) m = fmaxf(m, fmaxf(fabsf(first(v[i][k])), fabsf(second(v[i][k]))));
+        for (int k = 0; k < N / 2; ++k) {
+          const f32x2 hw = mul2(v[i][k], g[k]);
+          m = fmaxf(m, fmaxf(fabsf(first(hw)), fabsf(second(hw))));
+        }
       }
     }
   }
   float ss = first(ss2) + second(ss2);
   ss = lanes_sum<kLanes ? kLanes : 32>(ss);
-  if (scaled) m = lanes_max<kLanes ? kLanes : 32>(m);
+  if (kScaled) m = lanes_max<kLanes ? kLanes : 32>(m);
   if (!kLanes) {
     if (lane == 0) sm[warp] = make_float2(ss, m);
     __syncthreads();
     const float2 a = lane < width / 32 ? sm[lane] : make_float2(0.0f, 0.0f);
     ss = warp_sum(a.x);
-    if (scaled) m = warp_max(a.y);
+    if (kScaled) m = warp_max(a.y);
   }
+  O* y = static_cast<O*>(p.y) + t * p.ld_y + at;
   const float rstd = rsqrtf(fmaf(ss, p.inv_h, p.eps));
-  float inv = rstd * p.inv_scale, up = 1.0f;
-  if (scaled) {
-    const float s = row_scale(m, rstd, &inv, &up);
-    if (at == 0 && H > 0) p.row_scale[t] = s;
-  }
   if (at == 0 && H > 0 && p.rstd != nullptr) p.rstd[t] = rstd;
+  // The thread's i-th vectors of h and of the weight
+  auto operands = [&](int i, f32x2 (&g)[N / 2]) {
+    if (!kSum) {
+      // the row again (the compiler is kept from holding on to it)
+      asm volatile("" : "+r"(qx[i].x), "+r"(qx[i].y), "+r"(qx[i].z), "+r"(qx[i].w));
+      unpack(qx[i], v[i], T{});
+    }
+    unpack(qw[i], g, T{});
+  };
+  float inv = p.inv_scale, up = 1.0f;
+  if (kScaled) {
+    // Where the products have kept well within fp32's range, as those of ordinary rows do, max|y| is m * rstd
+    // and y / scale is h * weight * (448 / m). Other rows (masked to the type's lowest value, of zeros, of large
+    // weights) take both from y itself, which costs a second reduction.
+    const float s = m * rstd * (1.0f / 448.0f);
+    const bool left = H > 0 && !(m > 1e-30f && m < 1e30f && s > 0.0f);
+    if (!left) {
+      inv = __fdividef(448.0f, m);
+      if (at == 0 && H > 0) p.row_scale[t] = s;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (at + i * width * N < H) {
+          f32x2 g[N / 2];
+          operands(i, g);
+#pragma unroll
+          for (int k = 0; k < N / 2; ++k) g[k] = mul2(mul2(v[i][k], g[k]), pair(inv, inv));
+          store_vec(y + i * width * N, g);
+        }
+      }
+    }
+    if (kLanes ? !__any_sync(0xFFFFFFFFu, left) : !left) return;
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (at + i * width * N < H) {
+        f32x2 g[N / 2];
+        operands(i, g);
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+          g[k] = mul2(mul2(v[i][k], pair(rstd, rstd)), g[k]);
+          a = fmaxf(a, fmaxf(fabsf(first(g[k])), fabsf(second(g[k]))));
+        }
+      }
+    }
+    a = lanes_max<kLanes ? kLanes : 32>(a);
+    if (!kLanes) {
+      __syncthreads();   // the sums are read
+      if (lane == 0) sm[warp].y = a;
+      __syncthreads();
+      a = warp_max(lane < width / 32 ? sm[lane].y : 0.0f);
+    }
+    if (!left) return;
+    const float sa = row_scale(a, &inv, &up);
+    if (at == 0) p.row_scale[t] = sa;
+  }
+  // y = h * rstd * weight in this order: h * weight may be infinite where y is not
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if (at + i * width * N < H) {
-      if (!kSum) {
-        // the products again (the compiler is kept from holding on to them)
-        asm volatile("" : "+r"(qx[i].x), "+r"(qx[i].y), "+r"(qx[i].z), "+r"(qx[i].w));
-        f32x2 g[N / 2];
-        unpack(qx[i], v[i], T{});
-        unpack(qw[i], g, T{});
+      f32x2 g[N / 2];
+      operands(i, g);
 #pragma unroll
-        for (int k = 0; k < N / 2; ++k) v[i][k] = mul2(v[i][k], g[k]);
+      for (int k = 0; k < N / 2; ++k) {
+        g[k] = mul2(mul2(v[i][k], pair(rstd, rstd)), g[k]);
+        if (kScaled) g[k] = mul2(g[k], pair(up, up));
+        if (sizeof(O) == 1) g[k] = mul2(g[k], pair(inv, inv));
       }
-      if (up != 1.0f) {
-#pragma unroll
-        for (int k = 0; k < N / 2; ++k) v[i][k] = mul2(v[i][k], pair(up, up));
-      }
-#pragma unroll
-      for (int k = 0; k < N / 2; ++k) v[i][k] = mul2(v[i][k], pair(inv, inv));
-      store_vec(y + i * width * N, v[i]);
+      store_vec(y + i * width * N, g);
     }
   }
 }
@@ -215,7 +255,9 @@ __global__ void __launch_bounds__(kLong) tdx_rmsnorm_kernel(const __grid_constan
   }
   ss = block_reduce<false, kLong>(ss, sm);
   const float rstd = rsqrtf(fmaf(ss, p.inv_h, p.eps));
-  float inv = rstd * p.inv_scale, up = 1.0f;
+  if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[t] = rstd;
+  float inv = p.inv_scale, up = 1.0f;
+  bool within = false;   // as in the kernel above
   if (p.row_scale != nullptr) {
     float m = 0.0f;
     for (int c = threadIdx.x * N; c < p.H; c += kLong * N) {
@@ -226,17 +268,37 @@ __global__ void __launch_bounds__(kLong) tdx_rmsnorm_kernel(const __grid_constan
       for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i] * g[i]));
     }
     m = block_reduce<true, kLong>(m, sm);
-    const float s = row_scale(m, rstd, &inv, &up);
+    float s = m * rstd * (1.0f / 448.0f);
+    within = m > 1e-30f && m < 1e30f && s > 0.0f;
+    inv = __fdividef(448.0f, m);
+    if (!within) {
+      m = 0.0f;
+      for (int c = threadIdx.x * N; c < p.H; c += kLong * N) {
+        float v[N], g[N];
+        load_h(c, v);
+        load_vec(w + c, g);
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i] * rstd * g[i]));
+      }
+      s = row_scale(block_reduce<true, kLong>(m, sm), &inv, &up);
+    }
     if (threadIdx.x == 0) p.row_scale[t] = s;
   }
-  if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[t] = rstd;
   for (int c = threadIdx.x * N; c < p.H; c += kLong * N) {
     float v[N], g[N];
     load_h(c, v);
     load_vec(w + c, g);
     if (h != nullptr) store_vec(h + c, v);
+    if (within) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = v[i] * g[i] * up * inv;
+      for (int i = 0; i < N; ++i) v[i] = v[i] * g[i] * inv;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        v[i] = v[i] * rstd * g[i];
+        if (sizeof(O) == 1) v[i] = v[i] * up * inv;
+      }
+    }
     store_vec(y + c, v);
   }
 }
@@ -489,34 +551,37 @@ bool raise_smem(K kernel, int bytes, std::atomic<bool>* done) {
   return true;
 }
 
-template <typename T, typename O, int E, int kLanes>
+template <typename T, typename O, bool kScaled, int E, int kLanes>
 tdx_status launch_norm_lanes(const NormParams& p, cudaStream_t st) {
   const int rows = kThreads / kLanes;
-  return launch_rows(tdx_rmsnorm_rows_kernel<T, O, E, kLanes, true>,
+  return launch_rows(tdx_rmsnorm_rows_kernel<T, O, E, kLanes, true, kScaled>,
                      static_cast<unsigned>((static_cast<int64_t>(p.T) + rows - 1) / rows), kThreads, 0, st, p);
 }
 
-template <typename T, typename O, int E, bool kSum>
+template <typename T, typename O, bool kScaled, int E, bool kSum>
 tdx_status launch_norm_block(const NormParams& p, cudaStream_t st) {
   const unsigned block = static_cast<unsigned>((p.H + 32 * E - 1) / (32 * E) * 32);
-  return launch_rows(tdx_rmsnorm_rows_kernel<T, O, E, 0, kSum>, p.T, block, 0, st, p);
+  return launch_rows(tdx_rmsnorm_rows_kernel<T, O, E, 0, kSum, kScaled>, p.T, block, 0, st, p);
 }
 
-template <typename T, typename O>
+template <typename T, typename O, bool kScaled>
 tdx_status launch_norm_t(const NormParams& p, cudaStream_t st) {
-  if (p.H <= 64) return launch_norm_lanes<T, O, 8, 8>(p, st);
-  if (p.H <= 128) return launch_norm_lanes<T, O, 8, 16>(p, st);
-  if (p.H <= 256) return launch_norm_lanes<T, O, 8, 32>(p, st);
-  if (p.H <= 512) return launch_norm_lanes<T, O, 16, 32>(p, st);
-  if (p.H <= 1024) return launch_norm_lanes<T, O, 32, 32>(p, st);
+  if (p.H <= 64) return launch_norm_lanes<T, O, kScaled, 8, 8>(p, st);
+  if (p.H <= 128) return launch_norm_lanes<T, O, kScaled, 8, 16>(p, st);
+  if (p.H <= 256) return launch_norm_lanes<T, O, kScaled, 8, 32>(p, st);
+  if (p.H <= 512) return launch_norm_lanes<T, O, kScaled, 16, 32>(p, st);
+  if (p.H <= 1024) return launch_norm_lanes<T, O, kScaled, 32, 32>(p, st);
   if (p.H <= 16384) {
     // 32 elements a thread carry more loads per block of bf16 rows (32768 x 7168 with the residual 268 us, with 16
     // 293); fp32 rows take 16 (48076 x 1040 without a residual 80% of a copy's rate, with 32 60%), as do up to one
     // row per SM (1 x 8192 bf16 2.0 us, with 32 2.2)
-    const bool wide = sizeof(T) == 2 && p.T > sm_count();
-    if (p.residual != nullptr)
-      return wide ? launch_norm_block<T, O, 32, true>(p, st) : launch_norm_block<T, O, 16, true>(p, st);
-    return wide ? launch_norm_block<T, O, 32, false>(p, st) : launch_norm_block<T, O, 16, false>(p, st);
+    if constexpr (sizeof(T) == 2) {
+      if (p.T > sm_count())
+        return p.residual != nullptr ? launch_norm_block<T, O, kScaled, 32, true>(p, st)
+                                     : launch_norm_block<T, O, kScaled, 32, false>(p, st);
+    }
+    return p.residual != nullptr ? launch_norm_block<T, O, kScaled, 16, true>(p, st)
+                                 : launch_norm_block<T, O, kScaled, 16, false>(p, st);
   }
   return launch_rows(tdx_rmsnorm_kernel<T, O>, p.T, kLong, 0, st, p);
 }
@@ -524,9 +589,10 @@ tdx_status launch_norm_t(const NormParams& p, cudaStream_t st) {
 template <typename T>
 tdx_status launch_norm(tdx_dtype out, const NormParams& p, cudaStream_t st) {
   switch (out) {
-    case TDX_BF16: return launch_norm_t<T, bf16>(p, st);
-    case TDX_FP32: return launch_norm_t<T, float>(p, st);
-    default: return launch_norm_t<T, e4m3>(p, st);
+    case TDX_BF16: return launch_norm_t<T, bf16, false>(p, st);
+    case TDX_FP32: return launch_norm_t<T, float, false>(p, st);
+    default:
+      return p.row_scale != nullptr ? launch_norm_t<T, e4m3, true>(p, st) : launch_norm_t<T, e4m3, false>(p, st);
   }
 }
 

@@ -1,0 +1,68 @@
+"""The row-wise operators at the ends of fp32's range, and on the paths that need many rows: finite
+rows whose products overflow, infinities, NaN weights, scores near the smallest float, several rows per
+block, several choices per lane, offsets past 32 bits. Tolerances as in test_gpu_rows.py."""
+import numpy as np
+import pytest
+import torch
+
+import comm_overlapped_gemm_gb300 as tdx
+from oracle import rows as RO
+from test_gpu_rows import CODE, F, PAD, SMALLEST, TORCH, U, dev, host, near, run_norm, run_route, score_code, strided
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------------------- norm
+@pytest.mark.parametrize("T,H", [(6, 64), (200, 1040), (6, 4096), (200, 4096), (6, 33024)])
+@pytest.mark.parametrize("out,mode", [("bf16", ""), ("e4m3", "tensor"), ("e4m3", "rows")])
+@pytest.mark.parametrize("res", [False, True])
+def test_rmsnorm_of_the_lowest_values_is_zero(T, H, out, mode, res):
+    """A row masked to the type's lowest value: its sum of squares is infinite, 1 / root is 0, and
+    so is every h * rstd * weight, whatever the weight."""
+    x = torch.randn(T, H, generator=torch.Generator().manual_seed(H)).bfloat16().cuda()
+    x[1] = torch.finfo(torch.bfloat16).min
+    x[4, 3:7] = torch.finfo(torch.bfloat16).max
+    w = torch.full((H,), 1.5, device="cuda", dtype=torch.bfloat16)
+    r = torch.zeros_like(x) if res else None
+    _, y, scale, rstd = run_norm(x, r, w, "bf16", out, mode == "rows")
+    for t in (1, 4):
+        assert rstd[t].item() == 0.0
+        assert int(torch.count_nonzero(y[t].float())) == 0
+        if mode == "rows":
+            assert scale[t].item() == 1.0
+    assert bool(torch.isfinite(y.float()).all())
+
+
+@pytest.mark.parametrize("T,H", [(4, 64), (200, 1040), (4, 4096), (4, 33024)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("out,mode", [("fp32", ""), ("bf16", ""), ("e4m3", "tensor"), ("e4m3", "rows")])
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("size", [1e30, 2.5e37])
+def test_rmsnorm_of_large_weights(T, H, dtype, out, mode, res, size):
+    """h * weight is beyond fp32 (1e12 * 1e30), y = h * rstd * weight is not: up to 10 sizes."""
+    rng = np.random.default_rng(H)
+    x, xv = dev(1e12 * rng.standard_normal((T, H)), dtype)
+    r, rv = dev(1e12 * rng.standard_normal((T, H)), dtype) if res else (None, None)
+    w, wv = dev(size * (1 + 0.2 * rng.standard_normal(H)), dtype)
+    scale = 2.0 ** 100
+    _, y, rs, rstd = run_norm(x, r, w, dtype, out, mode == "rows", out_scale=scale)
+    _, wrstd, wy = RO.rmsnorm(xv, rv, wv, 1e-6)
+    calc = F * (H / 32 + 64)
+    near(host(rstd), wrstd, calc * wrstd, "rstd")
+    if out == "e4m3":
+        ws = RO.e4m3_row_scale(wy) if mode == "rows" else np.full(T, scale)
+        if mode == "rows":
+            near(host(rs), ws, 2 * calc * ws, "row_scale")
+        wy = np.clip(wy / ws[:, None], -448, 448)
+    near(host(y), wy, (U[out] + 3 * calc) * np.abs(wy) * (1 + 2.0 ** -6) + SMALLEST[out], "y")
+
+
+@pytest.mark.parametrize("H", [64, 4096, 33024])
+def test_rmsnorm_tensor_scale_near_the_smallest(H):
+    """1 / (root * scale) is beyond fp32 and zeros stay zeros; what is not zero saturates."""
+    x = torch.zeros(2, H, device="cuda")
+    x[1, 5] = -1e-10
+    w = torch.ones(H, device="cuda")
+    _, y, _, _ = run_norm(x, None, w, "fp32", "e4m3", eps=1e-12, out_scale=1e-36)
+    assert int(torch.count_nonzero(y.float()[0])) == 0
+    assert y[1, 5].float().item() == -448.0 and int(torch.count_nonzero(y.float()[1])) == 1
