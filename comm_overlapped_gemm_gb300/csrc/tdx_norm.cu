@@ -40,16 +40,16 @@ struct NormParams {
   float eps, inv_scale, inv_h;   // inv_h = 1 / H
 };
 
-// Sum (or maximum) over the block; every thread gets it.
+// Sum (or largest magnitude) over the block; every thread gets it.
 template <bool MAX, int kBlock>
 __device__ float block_reduce(float v, float* sm) {
-  v = MAX ? warp_max(v) : warp_sum(v);
+  v = MAX ? lanes_max_abs<32>(v) : warp_sum(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
   __syncthreads();
   float r = sm[0];
 #pragma unroll
-  for (int i = 1; i < kBlock / 32; ++i) r = MAX ? fmaxf(r, sm[i]) : r + sm[i];
+  for (int i = 1; i < kBlock / 32; ++i) r = MAX ? max_abs(r, sm[i]) : r + sm[i];
   return r;
 }
 
@@ -133,20 +133,20 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && size
 #pragma unroll
         for (int k = 0; k < N / 2; ++k) {
           const f32x2 hw = mul2(v[i][k], g[k]);
-          m = fmaxf(m, fmaxf(fabsf(first(hw)), fabsf(second(hw))));
+          m = max_abs(m, max_abs(fabsf(first(hw)), fabsf(second(hw))));
         }
       }
     }
   }
   float ss = first(ss2) + second(ss2);
   ss = lanes_sum<kLanes ? kLanes : 32>(ss);
-  if (kScaled) m = lanes_max<kLanes ? kLanes : 32>(m);
+  if (kScaled) m = lanes_max_abs<kLanes ? kLanes : 32>(m);
   if (!kLanes) {
     if (lane == 0) sm[warp] = make_float2(ss, m);
     __syncthreads();
     const float2 a = lane < width / 32 ? sm[lane] : make_float2(0.0f, 0.0f);
     ss = warp_sum(a.x);
-    if (kScaled) m = warp_max(a.y);
+    if (kScaled) m = lanes_max_abs<32>(a.y);
   }
   O* y = static_cast<O*>(p.y) + t * p.ld_y + at;
   const float rstd = rsqrtf(fmaf(ss, p.inv_h, p.eps));
@@ -191,16 +191,16 @@ __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && size
 #pragma unroll
         for (int k = 0; k < N / 2; ++k) {
           g[k] = mul2(mul2(v[i][k], pair(rstd, rstd)), g[k]);
-          a = fmaxf(a, fmaxf(fabsf(first(g[k])), fabsf(second(g[k]))));
+          a = max_abs(a, max_abs(fabsf(first(g[k])), fabsf(second(g[k]))));
         }
       }
     }
-    a = lanes_max<kLanes ? kLanes : 32>(a);
+    a = lanes_max_abs<kLanes ? kLanes : 32>(a);
     if (!kLanes) {
       __syncthreads();   // the sums are read
       if (lane == 0) sm[warp].y = a;
       __syncthreads();
-      a = warp_max(lane < width / 32 ? sm[lane].y : 0.0f);
+      a = lanes_max_abs<32>(lane < width / 32 ? sm[lane].y : 0.0f);
     }
     if (!left) return;
     const float sa = row_scale(a, &inv, &up);
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kLong) tdx_rmsnorm_kernel(const __grid_constan
       load_h(c, v);
       load_vec(w + c, g);
 #pragma unroll
-      for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i] * g[i]));
+      for (int i = 0; i < N; ++i) m = max_abs(m, fabsf(v[i] * g[i]));
     }
     m = block_reduce<true, kLong>(m, sm);
     float s = m * rstd * (1.0f / 448.0f);
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kLong) tdx_rmsnorm_kernel(const __grid_constan
         load_h(c, v);
         load_vec(w + c, g);
 #pragma unroll
-        for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i] * rstd * g[i]));
+        for (int i = 0; i < N; ++i) m = max_abs(m, fabsf(v[i] * rstd * g[i]));
       }
       s = row_scale(block_reduce<true, kLong>(m, sm), &inv, &up);
     }

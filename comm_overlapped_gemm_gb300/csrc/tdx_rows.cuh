@@ -133,6 +133,17 @@ __device__ __forceinline__ float lanes_max(float v) {
   for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
 }
+// The larger of two magnitudes (no sign bit); a NaN is larger than any of them
+__device__ __forceinline__ float max_abs(float a, float b) {
+  return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+}
+template <int L>
+__device__ __forceinline__ float lanes_max_abs(float v) {
+  if constexpr (L == 32) return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v)));
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v = max_abs(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
 __device__ __forceinline__ float warp_sum(float v) { return lanes_sum<32>(v); }
 __device__ __forceinline__ float warp_max(float v) { return lanes_max<32>(v); }
 

@@ -66,3 +66,19 @@ def test_rmsnorm_tensor_scale_near_the_smallest(H):
     _, y, _, _ = run_norm(x, None, w, "fp32", "e4m3", eps=1e-12, out_scale=1e-36)
     assert int(torch.count_nonzero(y.float()[0])) == 0
     assert y[1, 5].float().item() == -448.0 and int(torch.count_nonzero(y.float()[1])) == 1
+
+
+@pytest.mark.parametrize("T,H", [(3, 128), (3, 2048), (200, 2048), (3, 33024)])
+@pytest.mark.parametrize("dtype,res", [("bf16", False), ("bf16", True), ("fp32", False)])
+def test_rmsnorm_row_scale_of_a_weight_that_is_no_number(T, H, dtype, res):
+    """max|y| of every row is NaN: the scale is 1, and the other columns are y itself."""
+    g = torch.Generator().manual_seed(H)
+    x, r = (torch.randn(T, H, generator=g).to(TORCH[dtype]).cuda() for _ in range(2))
+    w = torch.ones(H, dtype=TORCH[dtype], device="cuda")
+    w[H - 3] = float("nan")
+    _, q, scale, _ = run_norm(x, r if res else None, w, dtype, "e4m3", True)
+    assert bool((scale == 1.0).all())
+    assert bool(torch.isnan(q[:, H - 3].float()).all())
+    _, one, _, _ = run_norm(x, r if res else None, torch.ones_like(w), dtype, "e4m3", out_scale=1.0)
+    keep = torch.arange(H, device="cuda") != H - 3
+    assert torch.equal(q.float()[:, keep], one.float()[:, keep])
