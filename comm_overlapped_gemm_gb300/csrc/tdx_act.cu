@@ -101,12 +101,16 @@ __global__ void __launch_bounds__(kThreads) tdx_swiglu_kernel(const __grid_const
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (row[v] < 0) continue;
-      float g[N], u[N];
+      f32x2 g[N / 2], u[N / 2];
       unpack(qg[v], g, T{});
       unpack(qu[v], u, T{});
-      const float su = s[v] * p.inv_scale;
 #pragma unroll
-      for (int k = 0; k < N; ++k) g[k] = silu(g[k] * s[v]) * (u[k] * su);
+      for (int k = 0; k < N / 2; ++k) {
+        g[k] = mul2(g[k], pair(s[v], s[v]));
+        g[k] = mul2(pair(silu(first(g[k])), silu(second(g[k]))), mul2(u[k], pair(s[v], s[v])));
+        // the scale last: u / out_scale may be infinite where silu(g) is 0
+        if (sizeof(O) == 1) g[k] = mul2(g[k], pair(p.inv_scale, p.inv_scale));
+      }
       store_vec(static_cast<O*>(p.out) + row[v] * p.ld_out + col[v], g);
     }
   } while (kDest && i - threadIdx.x < p.all);

@@ -82,3 +82,29 @@ def test_rmsnorm_row_scale_of_a_weight_that_is_no_number(T, H, dtype, res):
     _, one, _, _ = run_norm(x, r if res else None, torch.ones_like(w), dtype, "e4m3", out_scale=1.0)
     keep = torch.arange(H, device="cuda") != H - 3
     assert torch.equal(q.float()[:, keep], one.float()[:, keep])
+
+
+# -------------------------------------------------------------------------------------- swiglu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scaled", ["", "rows", "dest"])
+def test_swiglu_to_e4m3_of_lowest_values_is_zero(dtype, scaled):
+    """g * sigmoid(g) is 0, and so is its product with any finite u, whatever the scale it is stored with."""
+    R, I = 6, 32
+    t = torch.finfo(TORCH[dtype])
+    y = torch.zeros(R, 2 * I, dtype=TORCH[dtype], device="cuda")
+    y[0] = t.min
+    y[1, I:] = t.max                          # g = 0
+    y[2, :I], y[2, I:] = -100.0, t.min
+    y[3, :I], y[3, I:] = 1.0, t.max           # infinite over the scale: saturates
+    y[4, :I], y[4, I:] = -1.0, 3e37
+    y[5, :I], y[5, I:] = 2.0, 0.25
+    ones = torch.ones(R, device="cuda")
+    dest = torch.arange(R, dtype=torch.int32, device="cuda") if scaled == "dest" else None
+    out = torch.full((R, I), PAD, device="cuda").to(torch.float8_e4m3fn)
+    o = tdx.make_act_opts(out_dtype=tdx.TDX_FP8_E4M3, out_scale=0.0625, topk=1 if scaled == "dest" else 0)
+    tdx.check(tdx.tdx_swiglu(y, out, ones if scaled else None, dest, R, I, CODE[dtype], o))
+    v = out.float().cpu()
+    assert int(torch.count_nonzero(v[:3])) == 0
+    assert bool((v[3] == 448).all()) and bool((v[4] == -448).all())
+    want = 2.0 / (1.0 + np.exp(-2.0)) * 0.25 / 0.0625
+    assert bool(((v[5] - want).abs() <= 2.0 ** -4 * want).all())
