@@ -25,11 +25,32 @@ struct ActParams {
   float inv_scale;
 };
 
-// a * sigmoid(a) with the approximate exponential and quotient: together within 2^-22 * (2 + |a|) of
-// it, far inside the output's rounding (bf16, e4m3) or of the order of fp32's own. exp(-a) = inf gives -0,
-// as the exact quotient does. With the exact expf and quotient the kernel is bound by issue slots
-// (262144 x 2048 bf16, one vector per thread: 669 us).
-__device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
+// 2^x and 1/x by the special-function unit (2 and 1 ulp), subnormal results 0
+__device__ __forceinline__ float power_of_2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// a * sigmoid(a) of two values, and sigmoid(a). exp(-a) = 2^(-a log2 e) and the reciprocal are approximate: within
+// 2^-22 * (4 + |a|) relative, |a| < 89, which a rounding to 8 bits hides. With the exact expf and quotient the
+// kernel is bound by issue slots (262144 x 2048 bf16, one vector per thread: 669 us). The divisor is taken times
+// 1/16, so that its reciprocal is no subnormal where exp(-a) is below fp32's largest. exp(-a) = inf gives -0
+// and 0, as the exact quotient does.
+constexpr float kLog2e = 1.44269504f, kPart = 0.0625f;
+__device__ __forceinline__ f32x2 silu(f32x2 a) {
+  const f32x2 z = mul2(a, pair(-kLog2e, -kLog2e)), part = pair(kPart, kPart);
+  const f32x2 d = fma2(pair(power_of_2(first(z)), power_of_2(second(z))), part, part);
+  return mul2(mul2(a, part), pair(reciprocal(first(d)), reciprocal(second(d))));
+}
+__device__ __forceinline__ float sigmoid(float a) {
+  return kPart * reciprocal(fmaf(power_of_2(-kLog2e * a), kPart, kPart));
+}
 
 // i / d as the high half of i * ceil(2^64 / d): exact as long as i * (the product of d and that - 2^64) < 2^64,
 // that is i < 2^37 for d up to 2^27
@@ -107,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) tdx_swiglu_kernel(const __grid_const
 #pragma unroll
       for (int k = 0; k < N / 2; ++k) {
         g[k] = mul2(g[k], pair(s[v], s[v]));
-        g[k] = mul2(pair(silu(first(g[k])), silu(second(g[k]))), mul2(u[k], pair(s[v], s[v])));
+        g[k] = mul2(silu(g[k]), mul2(u[k], pair(s[v], s[v])));
         // the scale last: u / out_scale may be infinite where silu(g) is 0
         if (sizeof(O) == 1) g[k] = mul2(g[k], pair(p.inv_scale, p.inv_scale));
       }
@@ -147,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) tdx_swiglu_bwd_kernel(const __grid_c
     unpack(qd[v], d, T{});
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const float s = __fdividef(1.0f, 1.0f + __expf(-g[k]));
+      const float s = sigmoid(g[k]);
       const float ds = d[k] * s;
       d[k] = ds * u[k] * fmaf(g[k], 1.0f - s, 1.0f);
       u[k] = ds * g[k];

@@ -108,3 +108,22 @@ def test_swiglu_to_e4m3_of_lowest_values_is_zero(dtype, scaled):
     assert bool((v[3] == 448).all()) and bool((v[4] == -448).all())
     want = 2.0 / (1.0 + np.exp(-2.0)) * 0.25 / 0.0625
     assert bool(((v[5] - want).abs() <= 2.0 ** -4 * want).all())
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "fp32"), ("fp32", "bf16")])
+def test_swiglu_where_the_sigmoid_is_near_the_smallest_float(dtype, out):
+    """exp(-g) between 2^126 and fp32's largest: the value is small, not zero. exp of an argument of 89 is
+    off by at most 106 steps of 2^-23 in the approximate form."""
+    g = np.linspace(-88.5, -86.0, 64)
+    y, yv = dev(np.concatenate([g, np.full(64, 2.0 ** 100)])[None].repeat(3, 0), dtype)
+    o = torch.full((3, 64), PAD, dtype=TORCH[out], device="cuda")
+    tdx.check(tdx.tdx_swiglu(y, o, None, None, 3, 64, CODE[dtype], tdx.make_act_opts(out_dtype=CODE[out])))
+    want = RO.swiglu(yv)
+    near(host(o), want, (U[out] + F * (24 + 4 * np.abs(yv[:, :64]))) * np.abs(want), "out")
+    do, dov = dev(np.full((3, 64), 2.0 ** 20), dtype)
+    dy = torch.full_like(y, PAD)
+    tdx.check(tdx.tdx_swiglu_bwd(y, do, dy, 3, 64, CODE[dtype]))
+    want = RO.swiglu_bwd(yv, dov)
+    a = np.abs(yv[:, :64])
+    calc = F * (24 + 4 * np.concatenate([a, a], 1)) + 2.0 ** -21   # the sigmoid's own subnormal steps
+    near(host(dy), want, (U[dtype] + calc) * np.abs(want), "dy")
