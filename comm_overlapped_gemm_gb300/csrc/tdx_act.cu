@@ -37,19 +37,30 @@ __device__ __forceinline__ float reciprocal(float x) {
   return r;
 }
 
-// a * sigmoid(a) of two values, and sigmoid(a). exp(-a) = 2^(-a log2 e) and the reciprocal are approximate: within
-// 2^-22 * (4 + |a|) relative, |a| < 89, which a rounding to 8 bits hides. With the exact expf and quotient the
-// kernel is bound by issue slots (262144 x 2048 bf16, one vector per thread: 669 us). The divisor is taken times
-// 1/16, so that its reciprocal is no subnormal where exp(-a) is below fp32's largest. exp(-a) = inf gives -0
-// and 0, as the exact quotient does.
+// a * sigmoid(a) of two values; sigmoid(a) and 1 - sigmoid(a). For fp32 results (kExact) with expf and the IEEE quotient, which
+// costs nothing there (65536 x 2048 fp32 224 us either way). For the others exp(-a) = 2^(-a log2 e) and the
+// reciprocal are approximate: within 2^-22 * (4 + |a|) relative, |a| < 89, which a rounding to 8 bits
+// hides; with the exact forms that kernel is bound by issue slots (262144 x 2048 bf16, one vector per thread:
+// 669 us). The divisor is taken times 1/16, so that its reciprocal is no subnormal where exp(-a) is below fp32's
+// largest. exp(-a) = inf gives -0 and 0, as the exact quotient does.
 constexpr float kLog2e = 1.44269504f, kPart = 0.0625f;
+template <bool kExact>
 __device__ __forceinline__ f32x2 silu(f32x2 a) {
+  if (kExact) return pair(first(a) / (1.0f + expf(-first(a))), second(a) / (1.0f + expf(-second(a))));
   const f32x2 z = mul2(a, pair(-kLog2e, -kLog2e)), part = pair(kPart, kPart);
   const f32x2 d = fma2(pair(power_of_2(first(z)), power_of_2(second(z))), part, part);
   return mul2(mul2(a, part), pair(reciprocal(first(d)), reciprocal(second(d))));
 }
-__device__ __forceinline__ float sigmoid(float a) {
-  return kPart * reciprocal(fmaf(power_of_2(-kLog2e * a), kPart, kPart));
+template <bool kExact>
+__device__ __forceinline__ float sigmoid(float a, float* rest) {
+  if (kExact) {
+    const float e = expf(-a), s = 1.0f / (1.0f + e);
+    *rest = e < INFINITY ? e * s : 1.0f;   // 1 - s without the difference's cancellation
+    return s;
+  }
+  const float s = kPart * reciprocal(fmaf(power_of_2(-kLog2e * a), kPart, kPart));
+  *rest = 1.0f - s;
+  return s;
 }
 
 // i / d as the high half of i * ceil(2^64 / d): exact as long as i * (the product of d and that - 2^64) < 2^64,
@@ -128,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) tdx_swiglu_kernel(const __grid_const
 #pragma unroll
       for (int k = 0; k < N / 2; ++k) {
         g[k] = mul2(g[k], pair(s[v], s[v]));
-        g[k] = mul2(silu(g[k]), mul2(u[k], pair(s[v], s[v])));
+        g[k] = mul2(silu<sizeof(O) == 4>(g[k]), mul2(u[k], pair(s[v], s[v])));
         // the scale last: u / out_scale may be infinite where silu(g) is 0
         if (sizeof(O) == 1) g[k] = mul2(g[k], pair(p.inv_scale, p.inv_scale));
       }
@@ -168,9 +179,10 @@ __global__ void __launch_bounds__(kThreads) tdx_swiglu_bwd_kernel(const __grid_c
     unpack(qd[v], d, T{});
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const float s = sigmoid(g[k]);
+      float rest;
+      const float s = sigmoid<sizeof(T) == 4>(g[k], &rest);
       const float ds = d[k] * s;
-      d[k] = ds * u[k] * fmaf(g[k], 1.0f - s, 1.0f);
+      d[k] = ds * u[k] * fmaf(g[k], rest, 1.0f);
       u[k] = ds * g[k];
     }
     T* o = static_cast<T*>(p.out) + row[v] * p.ld_y + col[v];

@@ -127,3 +127,23 @@ def test_swiglu_where_the_sigmoid_is_near_the_smallest_float(dtype, out):
     a = np.abs(yv[:, :64])
     calc = F * (24 + 4 * np.concatenate([a, a], 1)) + 2.0 ** -21   # the sigmoid's own subnormal steps
     near(host(dy), want, (U[dtype] + calc) * np.abs(want), "dy")
+
+
+def test_swiglu_to_fp32_within_a_few_roundings():
+    """exp (2 F), the sum, the quotient (F each) and two products (F each), and the same for the gradient's
+    five factors: 16 F, for any g whose result is no subnormal."""
+    g = np.linspace(-86.0, 86.0, 4096)
+    y, yv = dev(np.concatenate([g, np.linspace(0.5, 1.5, 4096)])[None].repeat(2, 0), "fp32")
+    o, dy = torch.full((2, 4096), PAD, device="cuda"), torch.full_like(y, PAD)
+    tdx.check(tdx.tdx_swiglu(y, o, None, None, 2, 4096, 2, tdx.make_act_opts(out_dtype=2)))
+    near(host(o), RO.swiglu(yv), 16 * F * np.abs(RO.swiglu(yv)), "out")
+    do, dov = dev(np.ones((2, 4096)), "fp32")
+    tdx.check(tdx.tdx_swiglu_bwd(y, do, dy, 2, 4096, 2))
+    s, a = RO.scores(yv[:, :4096], "sigmoid"), np.abs(yv[:, :4096])
+    mag = np.concatenate([s * (1 + a * (1 - s)) * yv[:, 4096:], s * a], 1)
+    near(host(dy), RO.swiglu_bwd(yv, dov), 16 * F * mag, "dy")
+    half = y.bfloat16()
+    o.fill_(PAD)
+    tdx.check(tdx.tdx_swiglu(half, o, None, None, 2, 4096, 0, tdx.make_act_opts(out_dtype=2)))
+    want = RO.swiglu(half.double().cpu().numpy())
+    near(host(o), want, 16 * F * np.abs(want), "out of bf16")
