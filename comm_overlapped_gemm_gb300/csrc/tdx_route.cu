@@ -681,22 +681,29 @@ __global__ void __launch_bounds__(kThreads, L == 32 ? (V <= 8 ? 8 : 4) : L == 16
     // d: what the chosen score receives, then (but for softmax over the row) what its logit does
     float m = -INFINITY, inv = 0.0f;
     if (p.sigmoid) {
-      float s[R], S = 0.0f, dot = 0.0f;
+      float s[R], S = 0.0f;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         s[r] = id[r] >= 0 ? sigmoid_rn(v[r]) : 0.0f;
+        if (p.renorm) s[r] *= 0x1p40f;   // so that 1 / S is finite however small the scores
         S += s[r];
-        dot += d[r] * s[r];
       }
       if (p.renorm) {
+        // through the gates s / S, which are of size one
+        float dot = 0.0f;
         S = lanes_sum<L>(S);
+        const float one_over = S == 0.0f ? 0.0f : __frcp_rn(S);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          s[r] *= one_over;
+          dot += d[r] * s[r];
+        }
         dot = lanes_sum<L>(dot);
+#pragma unroll
+        for (int r = 0; r < R; ++r) d[r] -= dot;
       }
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (p.renorm) d[r] = S > 0.0f ? (d[r] - dot / S) / S : S != S ? S : 0.0f;
-        d[r] = id[r] >= 0 ? d[r] * s[r] * sigmoid_rn(-v[r]) : 0.0f;
-      }
+      for (int r = 0; r < R; ++r) d[r] = id[r] >= 0 ? d[r] * s[r] * sigmoid_rn(-v[r]) : 0.0f;
     } else if (p.renorm) {
 #pragma unroll
       for (int r = 0; r < R; ++r) m = fmaxf(m, v[r]);

@@ -84,6 +84,31 @@ def test_rmsnorm_row_scale_of_a_weight_that_is_no_number(T, H, dtype, res):
     assert torch.equal(q.float()[:, keep], one.float()[:, keep])
 
 
+# --------------------------------------------------------------------------------------- route
+@pytest.mark.parametrize("T,E,k", [(40, 24, 2), (9, 24, 4), (40, 64, 8), (40, 256, 8), (40, 500, 16), (9, 64, 1)])
+@pytest.mark.parametrize("scale", [1.0, 40.0])
+def test_route_bwd_of_scores_near_the_smallest_float(T, E, k, scale):
+    """Renormalised sigmoid gates of logits between -88.5 and -86 (scores from 3.7e-39 up): the gates are of
+    size one, and so are their gradients. A score is off by a rounding of exp and of the quotient, and
+    below 2^-126 by half of 2^-149, 2^-22 of the smallest: 8 F in all, 16 F in a quotient of two."""
+    rng = np.random.default_rng(E + k)
+    x, xv = dev(rng.uniform(-88.5, -86.0, (T, E)), "fp32")
+    ids = np.argsort(rng.random((T, E)), axis=1)[:, :k]
+    if k > 1:
+        x[1::2], xv[1::2] = -88.0, -88.0
+        x[1::2, 1::2], xv[1::2, 1::2] = -88.0 - 2.0 ** -3, -88.0 - 2.0 ** -3
+    dg, dgv = dev(rng.standard_normal((T, k)), "fp32")
+    out = torch.full((T, E), PAD, device="cuda")
+    o = tdx.make_route_opts(score=tdx.TDX_SCORE_SIGMOID, renorm=1, scale=scale)
+    tdx.check(tdx.tdx_moe_route_bwd(x, torch.from_numpy(ids.astype(np.int32)).cuda(), dg, out, T, E, k, 2, o))
+    want = RO.route_bwd(xv, ids, dgv, "sigmoid", True, scale)
+    sel = np.take_along_axis(RO.scores(xv, "sigmoid"), ids, 1)
+    mag = scale * (sel / sel.sum(1, keepdims=True)) * (np.abs(dgv) + np.abs(dgv).sum(1, keepdims=True))
+    tol = np.zeros((T, E))
+    np.put_along_axis(tol, ids, F * (64 + 4 * k) * mag, 1)
+    near(host(out), want, U["fp32"] * np.abs(want) + tol, "dlogits")
+
+
 # -------------------------------------------------------------------------------------- swiglu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("scaled", ["", "rows", "dest"])
