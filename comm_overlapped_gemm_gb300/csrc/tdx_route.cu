@@ -75,6 +75,7 @@ __device__ __forceinline__ void finish_row(const RouteParams& p, int64_t t, int 
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) v[r] = top == -INFINITY ? 0.0f : __expf(v[r] - top);
+    if (top == -INFINITY) den = 0.0f;
   }
   if (p.renorm) {
     den = 0.0f;
@@ -85,6 +86,7 @@ __device__ __forceinline__ void finish_row(const RouteParams& p, int64_t t, int 
   } else if (p.sigmoid) {
     den = 1.0f;
   }
+  if (m == INFINITY) den = NAN;   // exp(inf - inf) stands in every score of the row
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int j = sub + r * L;
@@ -92,7 +94,7 @@ __device__ __forceinline__ void finish_row(const RouteParams& p, int64_t t, int 
       p.idx[t * p.k + j] = id[r];
       // the approximate quotient, where the sum is no subnormal
       const float q = den < 1e-37f ? v[r] / den : __fdividef(v[r], den);
-      p.gates[t * p.k + j] = nan ? NAN : v[r] == 0.0f ? 0.0f : q * p.scale;
+      p.gates[t * p.k + j] = nan ? NAN : den == 0.0f ? 0.0f : q * p.scale;
       if (p.counts != nullptr) atomicAdd(hist + id[r], 1);
     }
   }

@@ -385,7 +385,8 @@ tdx_status tdx_rmsnorm_bwd(const void* dy, const void* h, const void* weight, co
  *   The topk largest keys are taken in descending order; equal keys (and groups) go to the lowest
  *   index; a NaN key comes after every other.
  *   gate_j = scale * s_j / (renorm ? sum of the chosen s : 1), 0 where that sum is 0 or, with softmax
- *   scores, the logits it runs over are all -inf.
+ *   scores, the logits it runs over are all -inf. With softmax scores a NaN or a +inf among a row's logits
+ *   makes all its gates NaN, chosen or not; with sigmoid scores a NaN shows where it enters.
  * Every step up to the keys rounds to fp32 as written, so ids do not depend on the kernel (but for the
  * order in which the sum of softmax scores with a bias is taken).
  *  logits     device, T x E of `dtype` (TDX_BF16 or TDX_FP32), aligned to the element, any stride.

@@ -36,14 +36,15 @@ def rmsnorm_bwd(dy, h, weight, rstd, dres=None):
 
 
 def scores(logits, score):
-    """softmax over a row (0 for a row of -inf) or sigmoid."""
+    """softmax over a row (0 for a row of -inf, NaN where a logit is +inf) or sigmoid."""
     if score == "sigmoid":
         with np.errstate(over="ignore"):
             return 1.0 / (1.0 + np.exp(-logits))
     m = logits.max(axis=1, keepdims=True)
-    e = np.exp(logits - np.where(np.isneginf(m), 0.0, m))
+    with np.errstate(invalid="ignore"):
+        e = np.exp(logits - np.where(np.isneginf(m), 0.0, m))
     s = e.sum(axis=1, keepdims=True)
-    return e / np.where(s > 0, s, 1.0)
+    return e / np.where(s == 0, 1.0, s)
 
 
 def _descending(key):
@@ -86,11 +87,11 @@ def route(logits, k, score="softmax", bias=None, n_group=1, topk_group=1, group_
     ids = rank[:, :k]
     g = np.take_along_axis(s, ids, 1)
     if renorm:
-        if score == "softmax":   # the softmax of the chosen logits
-            g = scores(np.take_along_axis(logits, ids, 1), "softmax")
+        if score == "softmax":   # the softmax of the chosen logits, where the row's is a number
+            g = np.where(np.isnan(g), g, scores(np.take_along_axis(logits, ids, 1), "softmax"))
         else:
             S = g.sum(axis=1, keepdims=True)
-            g = g / np.where(S > 0, S, 1.0)
+            g = g / np.where(S == 0, 1.0, S)
     return ids, g * scale, margin
 
 

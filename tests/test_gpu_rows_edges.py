@@ -85,6 +85,26 @@ def test_rmsnorm_row_scale_of_a_weight_that_is_no_number(T, H, dtype, res):
 
 
 # --------------------------------------------------------------------------------------- route
+@pytest.mark.parametrize("T,E,k,n_group", [(5, 64, 8, 1), (900, 64, 8, 1), (900, 33, 12, 1), (5, 256, 8, 8), (900, 256, 8, 8),
+                                           (40, 500, 5, 5)])
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_softmax_of_an_infinite_logit_is_no_number(T, E, k, n_group, renorm, bias):
+    """exp(inf - inf) is NaN and stands in every sum: all gates of the row are NaN, the other rows' are not."""
+    g = torch.Generator().manual_seed(E)
+    x = torch.randn(T, E, generator=g)
+    x[1, 7] = float("inf")
+    x[3, 7] = x[3, 2] = float("inf")
+    x[4] = -float("inf")
+    b = 0.01 * torch.randn(E, generator=g).cuda() if bias else None
+    ids, gates = run_route(x, k, bias=b, renorm=renorm, n_group=n_group, topk_group=max(1, n_group - 1))
+    assert np.isnan(gates[[1, 3]]).all()
+    rest = np.delete(np.arange(T), [1, 3])
+    assert np.isfinite(gates[rest]).all() and (gates[4] == 0).all()
+    if not bias:
+        assert (ids[1, 0], ids[3, 0], ids[3, 1]) == (7, 2, 7)
+
+
 @pytest.mark.parametrize("T,E,k", [(40, 24, 2), (9, 24, 4), (40, 64, 8), (40, 256, 8), (40, 500, 16), (9, 64, 1)])
 @pytest.mark.parametrize("scale", [1.0, 40.0])
 def test_route_bwd_of_scores_near_the_smallest_float(T, E, k, scale):

@@ -120,3 +120,15 @@ def test_swiglu_against_differences():
     got = differences(lambda v: (RO.swiglu(v) * do).sum(), y, at)
     assert np.allclose(got, RO.swiglu_bwd(y, do).ravel(), rtol=1e-6, atol=1e-9)
     assert not np.allclose(got, RO.swiglu_bwd(y[:, ::-1], do).ravel(), rtol=1e-6, atol=1e-9)
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_softmax_of_an_infinite_logit_is_no_number(renorm):
+    """exp(inf - inf) is NaN and stands in the sum under every score of the row."""
+    x = np.array([[0.0, np.inf, 1.0], [0.0, 1.0, 2.0]])
+    ids, gates, _ = RO.route(x, 2, "softmax", None, renorm=renorm)
+    assert ids.tolist() == [[1, 2], [2, 1]]
+    assert np.isnan(gates[0]).all() and np.isfinite(gates[1]).all()
+    assert np.isnan(RO.scores(x[:1], "softmax")).all()
+    # also where a bias keeps that expert out of the choice
+    assert np.isnan(RO.route(x[:1], 1, "softmax", np.array([0.0, -np.inf, 0.0]), renorm=renorm)[1]).all()
