@@ -181,7 +181,8 @@ def _first_stream() -> int:
     import torch
     if not torch.cuda.is_initialized():
         return int(torch.cuda.current_stream().cuda_stream) if torch.cuda.is_available() else 0
-    _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _device = torch._C._cuda_getDevice
+    _raw_stream = torch._C._cuda_getCurrentRawStream   # last: another thread that sees it has both
     return _stream(None)
 
 

@@ -165,3 +165,31 @@ def test_swiglu_refusals(tdx):
     assert act(topk=3, rs=FAKE, dest=FAKE) == inv      # 8 rows are no whole number of tokens
     assert act(topk=2, rs=FAKE + 2, dest=FAKE) == ali and act(topk=2, rs=FAKE, dest=FAKE + 2) == ali
     assert act(out=FAKE + 8) == ali and act(y=FAKE + 8) == ali
+
+
+def test_first_stream_from_two_threads(tdx, monkeypatch):
+    """While one thread looks torch's calls up for the first time, another may ask for the stream at any
+    point: here after every bytecode of the first one's way."""
+    import sys
+    import torch
+    for name, value in (("_cuda_getCurrentRawStream", lambda device: 4096 + device), ("_cuda_getDevice", lambda: 3)):
+        monkeypatch.setattr(torch._C, name, value, raising=False)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(tdx, "_raw_stream", None)
+    monkeypatch.setattr(tdx, "_device", None)
+    seen = []
+
+    def other(frame, event, arg):
+        frame.f_trace_opcodes = True
+        if event == "opcode" and frame.f_code is tdx._first_stream.__code__ and tdx._raw_stream is not None:
+            sys.settrace(None)
+            seen.append(tdx._stream(None))
+            sys.settrace(other)
+        return other
+
+    sys.settrace(other)
+    try:
+        first = tdx._stream(None)
+    finally:
+        sys.settrace(None)
+    assert first == 4099 and seen and set(seen) == {4099}
