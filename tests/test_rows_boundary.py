@@ -177,19 +177,20 @@ def test_first_stream_from_two_threads(tdx, monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
     monkeypatch.setattr(tdx, "_raw_stream", None)
     monkeypatch.setattr(tdx, "_device", None)
-    seen = []
+    seen, events = [], getattr(sys, "monitoring", None)
+    if events is None:
+        pytest.skip("no events of single instructions before Python 3.12")
 
-    def other(frame, event, arg):
-        frame.f_trace_opcodes = True
-        if event == "opcode" and frame.f_code is tdx._first_stream.__code__ and tdx._raw_stream is not None:
-            sys.settrace(None)
+    def other(code, offset):
+        if tdx._raw_stream is not None:
             seen.append(tdx._stream(None))
-            sys.settrace(other)
-        return other
 
-    sys.settrace(other)
+    events.use_tool_id(events.DEBUGGER_ID, "two threads")
     try:
+        events.register_callback(events.DEBUGGER_ID, events.events.INSTRUCTION, other)
+        events.set_local_events(events.DEBUGGER_ID, tdx._first_stream.__code__, events.events.INSTRUCTION)
         first = tdx._stream(None)
     finally:
-        sys.settrace(None)
+        events.set_local_events(events.DEBUGGER_ID, tdx._first_stream.__code__, 0)
+        events.free_tool_id(events.DEBUGGER_ID)
     assert first == 4099 and seen and set(seen) == {4099}
