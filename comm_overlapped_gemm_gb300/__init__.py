@@ -152,7 +152,9 @@ def _ptr(x) -> int:
     try:
         return x.data_ptr()
     except AttributeError:
-        return x   # a device pointer already
+        if isinstance(x, int):
+            return x   # a device pointer already
+        raise
 
 
 def _nbytes(x) -> int:

@@ -194,3 +194,14 @@ def test_first_stream_from_two_threads(tdx, monkeypatch):
         events.set_local_events(events.DEBUGGER_ID, tdx._first_stream.__code__, 0)
         events.free_tool_id(events.DEBUGGER_ID)
     assert first == 4099 and seen and set(seen) == {4099}
+
+
+@pytest.mark.parametrize("what", ["abc", b"abc", 1.5, [1], (1, 2), object()])
+def test_what_is_no_tensor_and_no_address_is_refused(tdx, what):
+    """ctypes would take text and bytes for the addresses of their characters."""
+    with pytest.raises((AttributeError, TypeError)):
+        norm(tdx, x=what, T=0)
+    with pytest.raises((AttributeError, TypeError)):
+        tdx.tdx_swiglu(FAKE, FAKE, None, what, 0, 64, 0, stream=0)
+    with pytest.raises((AttributeError, TypeError)):
+        tdx.tdx_ag_gemm([what], FAKE, FAKE, FAKE, 1, 128, 64, 64, 0, stream=0, workspace_bytes=0)
