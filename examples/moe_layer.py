@@ -78,17 +78,18 @@ class MoeLayer:
         """x, residual: [W * T, H] bf16, rank after rank. Returns (out, h)."""
         W, T, H, E, I, k, n = self.W, self.T, self.H, self.E, self.I, self.k, self.W * self.T
         bf16 = tdx.TDX_BF16
+        tokens = self.y
+        if self.e4m3:
+            # the same norm as codes, before h takes the place of a residual that is this layer's own
+            tokens = self.q
+            tdx.check(tdx.tdx_rmsnorm(x, residual, self.norm, None, self.q, self.q_scale, None, n, H, bf16,
+                                      self.quant_opts, stream), "tdx_rmsnorm")
         tdx.check(tdx.tdx_rmsnorm(x, residual, self.norm, self.h, self.y, None, None, n, H, bf16, self.norm_opts, stream),
                   "tdx_rmsnorm")
         tdx.check(tdx.tdx_ag_gemm(self.ranks(self.y), self.router, self.logits, self.ws_router, W, T, H, E, bf16,
                                   self.logit_opts, stream), "tdx_ag_gemm")
         tdx.check(tdx.tdx_moe_route(self.logits, self.bias, self.idx, self.gates, self.counts, n, E, k, tdx.TDX_FP32,
                                     self.route_opts, stream), "tdx_moe_route")
-        tokens = self.y
-        if self.e4m3:
-            tokens = self.q
-            tdx.check(tdx.tdx_rmsnorm(self.h, None, self.norm, None, self.q, self.q_scale, None, n, H, bf16,
-                                      self.quant_opts, stream), "tdx_rmsnorm")
         tdx.check(tdx.tdx_moe_dispatch_gemm(self.ranks(tokens), self.ranks(self.idx), self.up, self.expert_in, self.dest,
                                             None, self.ws_up, W, T, H, 2 * I, E, k, self.code, self.up_opts, stream),
                   "tdx_moe_dispatch_gemm")

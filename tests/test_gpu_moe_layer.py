@@ -114,3 +114,21 @@ def test_layer_in_a_graph_and_two_layers_in_a_row():
     graph.replay()
     torch.cuda.synchronize()
     assert not torch.equal(out2, want[2])
+
+
+def test_experts_and_router_take_one_norm():
+    """The codes for the experts are those of the norm that the router's bf16 tokens come from (of the
+    unrounded x + residual), also where a layer's own outputs are its next inputs."""
+    layer, x, residual = example().random_layer(2, 64, 256, 128, 8, 2, "e4m3", seed=3, score=1, renorm=0)
+    n, H = x.shape
+    for _ in range(2):
+        q, scale = torch.empty_like(layer.q), torch.empty_like(layer.q_scale)
+        tdx.check(tdx.tdx_rmsnorm(x, residual, layer.norm, None, q, scale, None, n, H, 0, layer.quant_opts))
+        want = x.double() + residual.double()
+        want = want / (want.square().mean(1, keepdim=True) + 1e-6).sqrt() * layer.norm.double()
+        out, h = layer.forward(x, residual)
+        layer.status()
+        assert torch.equal(layer.q.view(torch.uint8), q.view(torch.uint8)) and torch.equal(layer.q_scale, scale)
+        near = (layer.y.double() - want).abs() <= 2.0 ** -8 * want.abs() * (1 + 2.0 ** -8)
+        assert bool(near.all())
+        x, residual = out, h
