@@ -96,20 +96,21 @@ def route(logits, k, score="softmax", bias=None, n_group=1, topk_group=1, group_
 
 
 def route_bwd(logits, ids, dgates, score="softmax", renorm=True, scale=1.0):
-    """The gradient of sum(gates * dgates) by the logits, the choice held fixed."""
+    """The gradient of sum(gates * dgates) by the logits, the choice held fixed; places that name one expert add up."""
     s = scores(logits, score)
     sel = np.take_along_axis(s, ids, 1)
     dg = dgates * scale
     d = np.zeros_like(logits)
+    at = (np.arange(len(ids))[:, None], ids)
     if renorm:
         if score == "softmax":
             p = scores(np.take_along_axis(logits, ids, 1), "softmax")
-            np.put_along_axis(d, ids, p * (dg - (dg * p).sum(axis=1, keepdims=True)), 1)
+            np.add.at(d, at, p * (dg - (dg * p).sum(axis=1, keepdims=True)))
             return d
         S = sel.sum(axis=1, keepdims=True)
         S = np.where(S > 0, S, 1.0)
         dg = (dg - (dg * sel).sum(axis=1, keepdims=True) / S) / S
-    np.put_along_axis(d, ids, dg, 1)
+    np.add.at(d, at, dg)
     if score == "softmax":
         return s * (d - (d * s).sum(axis=1, keepdims=True))
     return d * s * scores(-logits, "sigmoid")

@@ -84,6 +84,100 @@ def test_rmsnorm_row_scale_of_a_weight_that_is_no_number(T, H, dtype, res):
     assert torch.equal(q.float()[:, keep], one.float()[:, keep])
 
 
+@pytest.mark.parametrize("T,H", [(200, 1040), (333, 2064), (200, 7168), (160, 16384)])
+@pytest.mark.parametrize("dtype,out,mode", [("bf16", "bf16", ""), ("bf16", "e4m3", "rows"), ("bf16", "e4m3", "tensor"),
+                                            ("bf16", "fp32", ""), ("fp32", "fp32", ""), ("fp32", "e4m3", "rows")])
+@pytest.mark.parametrize("res,pad", [(True, 0), (False, 16), (True, 48)])
+def test_rmsnorm_of_more_rows_than_multiprocessors(T, H, dtype, out, mode, res, pad):
+    rng = np.random.default_rng(T * 7 + H)
+    x, xv = dev(rng.standard_normal((T, H)), dtype)
+    r, rv = dev(3 * rng.standard_normal((T, H)), dtype) if res else (None, None)
+    w, wv = dev(1 + 0.2 * rng.standard_normal(H), dtype)
+    scale = 0.0625
+    h, y, rs, rstd = run_norm(x, r, w, dtype, out, mode == "rows", out_scale=scale, pad=pad)
+    wh, wrstd, wy = RO.rmsnorm(xv, rv, wv, 1e-6)
+    calc = F * (H / 32 + 64)
+    near(host(rstd), wrstd, calc * wrstd, "rstd")
+    if res:
+        near(host(h), wh, U[dtype] * np.abs(wh) + F * np.abs(wh), "h")
+    if out == "e4m3":
+        ws = RO.e4m3_row_scale(wy) if mode == "rows" else np.full(T, scale)
+        if mode == "rows":
+            near(host(rs), ws, 2 * calc * ws, "row_scale")
+        wy = np.clip(wy / ws[:, None], -448, 448)
+    near(host(y), wy, (U[out] + 3 * calc) * np.abs(wy) * (1 + 2.0 ** -6) + SMALLEST[out], "y")
+    again = run_norm(x, r, w, dtype, out, mode == "rows", out_scale=scale, pad=pad)
+    for a, b in zip((h, y, rs, rstd), again):
+        if a is not None:
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("T,H", [(200, 2048), (333, 7168)])
+@pytest.mark.parametrize("target", ["x", "residual"])
+def test_rmsnorm_in_place_of_more_rows_than_multiprocessors(T, H, target):
+    g = torch.Generator().manual_seed(5)
+    x, r = (torch.randn(T, H, generator=g).bfloat16().cuda() for _ in range(2))
+    w = torch.randn(H, generator=g).bfloat16().cuda()
+    h, y, _, rstd = run_norm(x, r, w, "bf16", "bf16")
+    a, b = x.clone(), r.clone()
+    y2, rstd2 = torch.empty_like(y), torch.empty_like(rstd)
+    tdx.check(tdx.tdx_rmsnorm(a, b, w, a if target == "x" else b, y2, None, rstd2, T, H, 0))
+    assert torch.equal(a if target == "x" else b, h) and torch.equal(y2, y) and torch.equal(rstd2, rstd)
+    assert torch.equal(b if target == "x" else a, r if target == "x" else x)
+
+
+# Rows that 152 multiprocessors have in hand at once, by the row's length, and sizes of more than 2 * stages + 1
+# rounds of them, the last one uneven, in every layout of the kernel
+BWD_IN_HAND = [(64, 19456), (128, 9728), (256, 4864), (512, 2432), (1024, 1216), (2560, 456), (1 << 30, 152)]
+BWD_ROUNDS = [(100003, 48), (50021, 112), (25013, 208), (12503, 400), (6211, 1024), (3301, 2064), (1093, 4112), (1200, 7168),
+              (1093, 8192), (801, 8208), (801, 16384), (1000, 20000)]
+
+
+@pytest.mark.parametrize("T,H", BWD_ROUNDS)
+@pytest.mark.parametrize("dtype,res,pad", [("bf16", True, 0), ("bf16", False, 8), ("fp32", True, 8), ("fp32", False, 0)])
+def test_rmsnorm_bwd_of_many_rows_per_block(T, H, dtype, res, pad):
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+
+    def make(scale, *shape):
+        return torch.randn(*shape, generator=g, device="cuda").mul_(scale).to(TORCH[dtype])
+
+    def padded(src):
+        v = strided(T, H, dtype, H + pad)[1]
+        v.copy_(src)
+        return v
+
+    h, dy, w = make(3.0, T, H), make(0.1, T, H), make(0.2, H) + 1
+    dr = make(0.1, T, H) if res else None
+    rstd = 1 / (h.float().square().mean(-1) + 1e-6).sqrt()
+    ld = H + pad if pad else 0
+    o = tdx.make_norm_opts(ld_x=ld, ld_residual=ld, ld_h=ld, ld_y=ld)
+    ws = torch.full((tdx.tdx_rmsnorm_bwd_workspace_size(T, H, CODE[dtype]),), 255, dtype=torch.uint8, device="cuda")
+    dys, hs, drs = padded(dy), padded(h), padded(dr) if res else None
+    got = []
+    for _ in range(3):
+        dxb, dx = strided(T, H, dtype, H + pad)
+        dw = torch.full((H,), PAD, device="cuda")
+        tdx.check(tdx.tdx_rmsnorm_bwd(dys, hs, w, rstd, drs, dx, dw, ws, T, H, CODE[dtype], o))
+        got.append((dxb, dw))
+    assert all(torch.equal(got[0][i], other[i]) for other in got[1:] for i in (0, 1))
+    if pad:
+        assert bool((got[0][0][:, H:].float() == PAD).all())
+    # the formula in 64 bits, on the device
+    hd, dyd, rd = h.double(), dy.double(), rstd.double()[:, None]
+    n, gd = hd * rd, dyd * w.double()
+    want = rd * (gd - n * (gd * n).mean(1, keepdim=True)) + (dr.double() if res else 0)
+    mag = rd * (gd.abs() + n.abs() * (gd * n).abs().mean(1, keepdim=True)) + (dr.double().abs() if res else 0)
+    off = (got[0][0][:, :H].double() - want).abs() - (U[dtype] * want.abs() + F * (H / 32 + 64) * mag)
+    assert float(off.max()) <= 0, "dx"
+    # a column's additions one after another: the rounds, up to 32 rows of a block, up to 19 blocks, 32 warps
+    serial = T / next(rows for most, rows in BWD_IN_HAND if H <= most) + 96
+    off = (got[0][1].double() - (dyd * n).sum(0)).abs() - F * serial * (dyd * n).abs().sum(0)
+    assert float(off.max()) <= 0, "dw"
+    # in place over the gradient that comes in
+    tdx.check(tdx.tdx_rmsnorm_bwd(dys, hs, w, rstd, drs, dys, got[0][1], ws, T, H, CODE[dtype], o))
+    assert torch.equal(dys, got[1][0][:, :H]) and torch.equal(got[0][1], got[1][1])
+
+
 # --------------------------------------------------------------------------------------- route
 @pytest.mark.parametrize("T,E,k,n_group", [(5, 64, 8, 1), (900, 64, 8, 1), (900, 33, 12, 1), (5, 256, 8, 8), (900, 256, 8, 8),
                                            (40, 500, 5, 5)])
@@ -127,6 +221,64 @@ def test_route_bwd_of_scores_near_the_smallest_float(T, E, k, scale):
     tol = np.zeros((T, E))
     np.put_along_axis(tol, ids, F * (64 + 4 * k) * mag, 1)
     near(host(out), want, U["fp32"] * np.abs(want) + tol, "dlogits")
+
+
+@pytest.mark.parametrize("T,E,k", [(700, 64, 16), (700, 20, 12), (900, 128, 16), (700, 33, 9)])
+@pytest.mark.parametrize("score,bias", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_route_of_several_places_per_lane(T, E, k, score, bias, dtype):
+    rng = np.random.default_rng(E * 31 + k)
+    x, xv = dev(1.5 * rng.standard_normal((T, E)), dtype)
+    b, bv = dev(0.05 * rng.standard_normal(E), "fp32") if bias else (None, None)
+    ids, gates = run_route(x, k, dtype, b, score=score_code(score))
+    want, wg, margin = RO.route(xv, k, score, bv)
+    clear = margin > 32 * F
+    assert clear.mean() >= 0.9
+    assert np.array_equal(ids[clear], want[clear])
+    near(gates[clear], wg[clear], F * (E / 16 + 64 + np.abs(xv).max() * 2) * wg[clear], "gates")
+    # ties: a few values only, equal keys in the order of their experts
+    x, xv = dev(np.array([-1.0, -0.25, 0.0, 0.5, 1.25])[rng.integers(0, 5, (T, E))], "bf16")
+    b, bv = dev(rng.integers(-1, 2, E) / 64.0, "fp32") if bias else (None, None)
+    ids, _ = run_route(x, k, "bf16", b, score=score_code(score))
+    key = xv if score == "softmax" and not bias else np.round(RO.scores(xv, score) + (0 if bv is None else bv), 12)
+    if not (score == "softmax" and bias):   # sums of a softmax score and a bias may round together
+        assert np.array_equal(ids, np.argsort(-key, axis=1, kind="stable")[:, :k])
+
+
+@pytest.mark.parametrize("T,E,k", [(700, 64, 16), (700, 24, 10), (900, 128, 16)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_of_several_places_per_lane_whose_keys_differ_in_their_last_bits(T, E, k, score):
+    g = torch.Generator().manual_seed(E)
+    x = (torch.randn(T, 1, generator=g) + 2.0 ** -22 * torch.randint(-6, 7, (T, E), generator=g)).cuda()
+    x[::3] += (torch.rand(x[::3].shape, generator=g) < 0.5).cuda() * 1.0
+    ids, _ = run_route(x, k, score=score_code(score))
+    key = (x if score == "softmax" else 1.0 / (1.0 + torch.exp(-x))).cpu().numpy().astype(np.float64)
+    assert np.array_equal(ids, np.argsort(-key, axis=1, kind="stable")[:, :k])
+
+
+@pytest.mark.parametrize("T,E,k", [(300, 24, 4), (300, 64, 8), (300, 64, 16), (300, 128, 16), (300, 256, 8), (300, 500, 16)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [0, 1])
+def test_route_bwd_of_ids_that_come_twice(T, E, k, score, renorm):
+    """Places that name one expert add up, in pairs and three of a kind, on one lane and on several."""
+    rng = np.random.default_rng(E + k)
+    x, xv = dev(1.5 * rng.standard_normal((T, E)), "fp32")
+    ids = np.argsort(rng.random((T, E)), axis=1)[:, :k]
+    ids[::4, 1] = ids[::4, 0]
+    ids[1::4, k - 1] = ids[1::4, 0]
+    ids[2::4, [1, k - 1]] = ids[2::4, [k // 2]]
+    if k > 8:
+        ids[::4, 8] = ids[::4, 0]
+        ids[1::4, 15 if k > 15 else 9] = ids[1::4, 7 if k > 15 else 1]
+    dg, dgv = dev(rng.standard_normal((T, k)), "fp32")
+    out = torch.full((T, E), PAD, device="cuda")
+    tdx.check(tdx.tdx_moe_route_bwd(x, torch.from_numpy(ids.astype(np.int32)).cuda(), dg, out, T, E, k, 2,
+                                    tdx.make_route_opts(score=score_code(score), renorm=renorm)))
+    want = RO.route_bwd(xv, ids, dgv, score, bool(renorm), 1.0)
+    s = RO.scores(xv, score)
+    S = np.take_along_axis(s, ids, 1).sum(1, keepdims=True)
+    mag = s * np.abs(dgv).sum(1, keepdims=True) * (2 / np.minimum(S, 1) if renorm else 2)
+    near(host(out), want, U["fp32"] * np.abs(want) + F * (E / 16 + 64 + 4 * np.abs(xv).max()) * mag, "dlogits")
 
 
 # -------------------------------------------------------------------------------------- swiglu
@@ -192,3 +344,43 @@ def test_swiglu_to_fp32_within_a_few_roundings():
     tdx.check(tdx.tdx_swiglu(half, o, None, None, 2, 4096, 0, tdx.make_act_opts(out_dtype=2)))
     want = RO.swiglu(half.double().cpu().numpy())
     near(host(o), want, 16 * F * np.abs(want), "out of bf16")
+
+
+# ---------------------------------------------------------------------------------------- sizes
+def test_gradients_and_routing_beyond_2_to_the_31_elements():
+    """Row offsets past 32 bits: the last rows of a tall tensor are those of a short one."""
+    H, T = 8192, 270000                                # 2.2e9 elements
+    gen = torch.Generator().manual_seed(1)
+    h, dy = (torch.ones(T, H, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    tail_h, tail_dy = (torch.randn(5, H, generator=gen).bfloat16().cuda() for _ in range(2))
+    h[-5:], dy[-5:] = tail_h, tail_dy
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    rstd = torch.ones(T, device="cuda")
+    dx, dw, few, dws = torch.empty_like(h), torch.empty(H, device="cuda"), torch.empty_like(tail_h), torch.empty(H, device="cuda")
+    ws = torch.empty(tdx.tdx_rmsnorm_bwd_workspace_size(T, H, 0), dtype=torch.uint8, device="cuda")
+    tdx.check(tdx.tdx_rmsnorm_bwd(dy, h, w, rstd, None, dx, dw, ws, T, H, 0))
+    tdx.check(tdx.tdx_rmsnorm_bwd(tail_dy, tail_h, w, rstd[-5:].clone(), None, few, dws, ws, 5, H, 0))
+    assert torch.equal(dx[-5:], few)
+    assert int(torch.count_nonzero(dx[:-5])) == 0      # g - n * mean(g n) = 1 - 1
+    want = (tail_dy.double() * tail_h.double()).sum(0) + (T - 5)
+    assert float((dw.double() - want).abs().max()) <= F * (T + 32) * (T + 100)
+    del h, dy, dx
+    T, E, k = 4300000, 512, 4                          # 2.2e9 logits
+    x = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(700, E, generator=gen).bfloat16().cuda()
+    x[-700:] = tail
+    idx, gates = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    few_idx, few_gates = torch.empty(700, k, dtype=torch.int32, device="cuda"), torch.empty(700, k, device="cuda")
+    tdx.check(tdx.tdx_moe_route(x, None, idx, gates, None, T, E, k, 0))
+    tdx.check(tdx.tdx_moe_route(tail, None, few_idx, few_gates, None, 700, E, k, 0))
+    assert torch.equal(idx[-700:], few_idx) and torch.equal(gates[-700:], few_gates)
+    assert bool((idx[:-700] == torch.arange(k, device="cuda")).all()) and bool((gates[:-700] == 0.25).all())
+    dg = torch.randn(T, k, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    dl, few = torch.full_like(x, PAD), torch.empty_like(tail)
+    o = tdx.make_route_opts(renorm=0)
+    tdx.check(tdx.tdx_moe_route_bwd(x, idx, dg, dl, T, E, k, 0, o))
+    tdx.check(tdx.tdx_moe_route_bwd(tail, few_idx, dg[-700:].clone(), few, 700, E, k, 0, o))
+    assert torch.equal(dl[-700:], few)
+    s = dg[:-700].sum(1)                               # p (dg_i - p sum dg), p = 2^-9
+    at = torch.arange(0, T - 700, 99991, device="cuda")
+    assert torch.allclose(dl[at, E - 1].float(), -s[at] * 2.0 ** -18, rtol=2.0 ** -7, atol=2.0 ** -38)

@@ -132,3 +132,18 @@ def test_route_softmax_of_an_infinite_logit_is_no_number(renorm):
     assert np.isnan(RO.scores(x[:1], "softmax")).all()
     # also where a bias keeps that expert out of the choice
     assert np.isnan(RO.route(x[:1], 1, "softmax", np.array([0.0, -np.inf, 0.0]), renorm=renorm)[1]).all()
+
+
+@pytest.mark.parametrize("score,renorm", list(itertools.product(["softmax", "sigmoid"], [False, True])))
+def test_route_bwd_of_ids_that_come_twice_against_differences(score, renorm):
+    rng = np.random.default_rng(9)
+    x, dg = rng.standard_normal((3, 7)), rng.standard_normal((3, 4))
+    ids = np.array([[1, 1, 4, 2], [5, 0, 3, 5], [6, 6, 6, 0]])
+
+    def f(x):
+        s = np.take_along_axis(RO.scores(x, score), ids, 1)
+        return (2.5 * (s / s.sum(1, keepdims=True) if renorm else s) * dg).sum()
+
+    at = [(i, j) for i in range(3) for j in range(7)]
+    d = RO.route_bwd(x, ids, dg, score, renorm, 2.5)
+    assert np.allclose(differences(f, x, at), d.ravel(), rtol=1e-6, atol=1e-9)
