@@ -37,12 +37,12 @@ __device__ __forceinline__ float reciprocal(float x) {
   return r;
 }
 
-// a * sigmoid(a) of two values; sigmoid(a) and 1 - sigmoid(a). For fp32 results (kExact) with expf and the IEEE quotient, which
-// costs nothing there (65536 x 2048 fp32 224 us either way). For the others exp(-a) = 2^(-a log2 e) and the
-// reciprocal are approximate: within 2^-22 * (4 + |a|) relative, |a| < 89, which a rounding to 8 bits
-// hides; with the exact forms that kernel is bound by issue slots (262144 x 2048 bf16, one vector per thread:
-// 669 us). The divisor is taken times 1/16, so that its reciprocal is no subnormal where exp(-a) is below fp32's
-// largest. exp(-a) = inf gives -0 and 0, as the exact quotient does.
+// a * sigmoid(a) of two values; sigmoid(a) and 1 - sigmoid(a). For fp32 results (kExact) with expf and the IEEE
+// quotient, which costs nothing there (65536 x 2048 fp32 224 us either way). For the others exp(-a) = 2^(-a log2 e)
+// and the reciprocal are approximate: within 2^-22 * (4 + |a|) relative, |a| < 89, which a rounding to 8 bits hides;
+// with the exact forms that kernel is bound by issue slots (262144 x 2048 bf16, one vector per thread: 669 us). The
+// divisor is taken times 1/16, so that its reciprocal is no subnormal where exp(-a) is below fp32's largest.
+// exp(-a) = inf gives -0 and 0, as the exact quotient does.
 constexpr float kLog2e = 1.44269504f, kPart = 0.0625f;
 template <bool kExact>
 __device__ __forceinline__ f32x2 silu(f32x2 a) {
@@ -77,14 +77,15 @@ __device__ __forceinline__ int64_t place(const ActParams& p, int64_t i, int* c) 
   return r;
 }
 
-// Bound by HBM: 6 bytes an element in bf16, 7.2 TB/s at 262144 x 2048 (450 us, a plain copy's rate 482); 8192 x
-// 2048 takes 16.3 us of 15.1. The call's vectors are dealt out in the order of their addresses, V x kThreads to
+// Bound by HBM: 6 bytes an element in bf16, 7.2 TB/s at 262144 x 2048 (446 us, a plain copy's rate 482); 8192 x
+// 2048 takes 16.1 us of 15.1. The call's vectors are dealt out in the order of their addresses, V x kThreads to
 // a block, whatever the row's length; a thread issues all loads of its V vectors before it computes.
-// V = 1 / 2 / 4 / 8 with 256 threads: 472 / 454 / 468 / 482 us; 128 / 256 / 512 threads with V = 2: 448 / 454 / 459.
+// With scalar products: V = 1 / 2 / 4 / 8 with 256 threads 472 / 454 / 468 / 482 us; 128 / 256 / 512 threads with
+// V = 2 448 / 454 / 459. In pairs of values, with 128 and 2: 446; 131072 x 2048 to e4m3 199 -> 188.
 // kDest: rows are found through dest, which puts a second memory latency in front of a block's loads. So
 // blocks go round and look up their next rows and scales while the loads of the present ones are under way:
-// 8192 x 2048 18.4 us, 262144 x 2048 506 us; a block per piece 19.6 and 545, 8 (all resident) / 10 / 16 blocks
-// per SM that go round 522 / 622 / 509.
+// 8192 x 2048 18.1 us, 262144 x 2048 502 us; at 18.4 and 506 us a block per piece took 19.6 and 545, 8 (all
+// resident) / 10 / 16 blocks per SM that go round 522 / 622 / 509.
 template <typename T, typename O, int V, bool kDest>
 __global__ void __launch_bounds__(kThreads) tdx_swiglu_kernel(const __grid_constant__ ActParams p) {
   constexpr int N = kVec<T>;

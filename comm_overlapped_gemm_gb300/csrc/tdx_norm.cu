@@ -73,16 +73,18 @@ __device__ __forceinline__ float row_scale(float m, float* inv, float* up) {
 // kLanes 8, 16, 32: that many lanes of a warp per row (short rows; the reduction is shuffles alone); 0: a
 // block per row, whose reduction takes one barrier.
 // Bound by HBM: 32768 x 7168 bf16 with the residual 268 us (7.0 TB/s, a plain copy's rate 281), 1000000 x
-// 128 152 us (6.9 TB/s; with a warp per row of 128, half of its lanes idle, 200 us). 1024 x 7168 to e4m3 with
-// row scales takes 10.2 us of 7.7: the launch's ramp and tail (a plain addition over as many bytes takes 9.0).
+// 128 148 us (6.9 TB/s; with a warp per row of 128, half of its lanes idle, 200 us). 1024 x 7168 to e4m3 with
+// row scales takes 10.4 us of 7.7: the launch's ramp and tail (a plain addition over as many bytes takes 9.0).
 // Rows through a ring of cp.async stages in shared memory, as the gradient takes them, came out slower
 // here (311 us): the many independent blocks keep more loads in flight than one block per SM does
 // between two sums.
 // Registers: 64 a thread for 32 bf16 elements, so that four blocks of 224 threads share an SM instead of three
-// (1024 x 7168 to e4m3 11.2 / 11.7 us at the time; five, at 48 registers, spill: 13.8).
+// (1024 x 7168 to e4m3 11.2 / 11.7 us at the time; five, at 48 registers, spill: 13.8). y's address is taken after
+// the reduction: before it, the row scales' instance spills (32768 x 7168 to e4m3 305 us, without 235).
 // kSum: there may be a residual. Without one the row waits for its sum as it was read, not in fp32: 6960 x 7184
 // bf16 93% of a copy's rate (in fp32, before the sums were taken two at a time and rsqrtf, 78%; now bound by issue
-// slots, as are the codes there, 75%).
+// slots, as are the codes there, 74%). Rows just above 1024 columns leave half of two warps idle: 48076 x 1040 bf16
+// 61%.
 template <typename T, typename O, int E, int kLanes, bool kSum, bool kScaled>
 __global__ void __launch_bounds__(kLanes ? kThreads : 16384 / E, !kLanes && sizeof(T) == 2 && E == 32 ? 2 : 1)
     tdx_rmsnorm_rows_kernel(const __grid_constant__ NormParams p) {
@@ -322,7 +324,8 @@ struct NormBwdParams {
 // Bound by HBM (8 bytes an element in bf16 with dres): 16381 x 8192 157 us with the sums' second kernel
 // (6.8 TB/s, a plain copy's rate 161), 100001 x 1024 120 us (123), 8000 x 16384 161 us (157), 262144 x 128
 // 45 us (40). Ring depth 2 / 3 / 4 at 16381 x 8192: 158 (32 columns a thread) / 157 / 158 us. Two blocks of
-// 512 threads per SM, at 64 registers, spill: 223 us.
+// 512 threads per SM, at 64 registers, spill: 223 us. Spills that stay: 48 to 72 bytes in the fp32 instances for up to
+// 256 columns (64 columns 89% of a copy's rate; in bf16, without any, 93%), 28 in the bf16 one for more than 8192.
 template <typename T, int E, int kStages, int kMaxThreads, int kBlocks, int kLanes>
 __global__ void __launch_bounds__(kMaxThreads, kBlocks)
     tdx_rmsnorm_bwd_rows_kernel(const __grid_constant__ NormBwdParams p) {

@@ -334,11 +334,12 @@ __device__ __forceinline__ uint32_t lanes_top(uint32_t w) {
 // A group is a run of 2^n lanes (all of them where there are no groups); entries past its end hold -inf and
 // the word 0, which says that there is nothing.
 //
-// Bound by issue slots, not by HBM: 32768 tokens, softmax, 8 of 64 experts 7.5 us (149 warp instructions a
+// Bound by issue slots, not by HBM: 32768 tokens, softmax, 8 of 64 experts 7.5 us (139 warp instructions a
 // token; HBM 1.6 us), sigmoid with bias, 8 of 256 in 4 of 8 groups 27.4 us (701, some 177 of them for scores: ids
 // have to be those of the definition, so that every sigmoid is an expf and a correctly rounded
 // reciprocal; 150 for the groups, 150 for the maxima, 42 for the sorted lists; HBM 5.3 us), 2.85 of 4
-// instructions a cycle. Registers decide how much of that is reached: 64-bit token numbers 29.6 us, biases in
+// instructions a cycle. Registers decide how much of that is reached (the bounds below cost the bf16 instances and those
+// of 16 places spills of up to 36 bytes; none in fp32 for up to 8 places): 64-bit token numbers 29.6 us, biases in
 // registers 27.8; with 16 lanes of 16 experts for 256 32.3, at half the blocks; three / five blocks per SM 30.2 /
 // 32.2; the maxima in a loop 33.0. 512 experts, sigmoid with bias, topk 16: 50.9 us at three blocks, 54.5 at two.
 template <typename T, int L, int V, int K, bool kVector>
@@ -638,7 +639,7 @@ __device__ __forceinline__ void store_logits(T* x, int lane, int E, bool vector,
 // whole row needs no look at the chosen logits. Choices of the same expert add up in the order of their places.
 // 4 E (softmax over the row: 8 E) bytes and 8 topk bytes a token: 32768 tokens, softmax over 64 experts 4.9 us
 // (HBM 2.8), 128 experts 9.0 us (5.3), 500 experts 30 us (20; in lanes of consecutive experts, read one by one,
-// 89), renormalised sigmoid over 256 13.0 us (5.5), there bound by the latency of a warp's steps for its one
+// 89), renormalised sigmoid over 256 12.9 us (5.5), there bound by the latency of a warp's steps for its one
 // token: eight blocks per SM 13.0 us, four 16.7 (for 8 lanes a token more than the compiler's choice is slower:
 // 6.3 against 4.9).
 template <typename T, int L, int V>

@@ -325,17 +325,20 @@ tdx_status tdx_moe_combine_plan_info(int W, int T, int F, int H, int E, int topk
 /* ---------------------------------------------------------------------------------------------
  * The row-wise operators around the products: root-mean-square norm, routing to experts, gated
  * SiLU, each with its gradient. They read one tensor per operand; W ranks whose tensors lie in one
- * buffer, rank after rank, are one call on W*T rows. All arithmetic is fp32; every output is
- * rounded once (RNE; e4m3 saturates at +-448). Except tdx_rmsnorm_bwd they need no workspace, and
- * they record nothing in a device status word: ids and indexes read on the device are bounds-checked
- * there. Rows of 0 elements are invalid; 0 rows launch nothing (tdx_rmsnorm_bwd still zeroes
+ * buffer, rank after rank, are one call on W*T rows. All arithmetic is fp32, with the approximate
+ * functions that each operator names; every output is rounded once (RNE; e4m3 saturates at +-448).
+ * e4m3 codes are those of the value times its scale's fp32 reciprocal, not of an exact quotient: a
+ * value within the arithmetic's own rounding of the middle between two codes may take either.
+ * Except tdx_rmsnorm_bwd they need no workspace, and they record nothing in a device status word: ids
+ * and indexes read on the device are bounds-checked there. Rows of 0 elements are invalid; 0 rows launch nothing (tdx_rmsnorm_bwd still zeroes
  * dweight). Row strides are in elements, 0 = dense; a stride below the row's length is
  * TDX_ERR_INVALID_ARG. Unless said otherwise pointers are 16-byte aligned and rows and strides are
  * multiples of 16 bytes (TDX_ERR_ALIGNMENT).
  *
  * Root-mean-square norm of x + residual:
  *   h = x + residual (x alone if residual is NULL), rstd = 1 / sqrt(mean(h^2) + eps),
- *   y = h * rstd * weight; the sum h is normalised before it is rounded to `dtype` for h_out.
+ *   y = h * rstd * weight; the sum h is normalised before it is rounded to `dtype` for h_out. The
+ *   inverse root is rsqrtf (2 ulp).
  *  x, residual, h_out  device, T x H of `dtype` (TDX_BF16 or TDX_FP32). residual optional; h_out (the
  *             residual stream for the next layer) optional, only with residual. h_out may be x or
  *             residual itself (same stride); otherwise outputs overlap no input.
@@ -387,6 +390,8 @@ tdx_status tdx_rmsnorm_bwd(const void* dy, const void* h, const void* weight, co
  *   gate_j = scale * s_j / (renorm ? sum of the chosen s : 1), 0 where that sum is 0 or, with softmax
  *   scores, the logits it runs over are all -inf. With softmax scores a NaN or a +inf among a row's logits
  *   makes all its gates NaN, chosen or not; with sigmoid scores a NaN shows where it enters.
+ * Gates, and the gradient's softmax, take approximate exponentials and quotients: within
+ * 2^-24 * (64 + E / 16 + 2 d) of their values, d the spread of the row's logits.
  * Every step up to the keys rounds to fp32 as written, so ids do not depend on the kernel (but for the
  * order in which the sum of softmax scores with a bias is taken).
  *  logits     device, T x E of `dtype` (TDX_BF16 or TDX_FP32), aligned to the element, any stride.

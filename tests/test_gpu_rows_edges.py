@@ -129,8 +129,8 @@ def test_rmsnorm_in_place_of_more_rows_than_multiprocessors(T, H, target):
 # Rows that 152 multiprocessors have in hand at once, by the row's length, and sizes of more than 2 * stages + 1
 # rounds of them, the last one uneven, in every layout of the kernel
 BWD_IN_HAND = [(64, 19456), (128, 9728), (256, 4864), (512, 2432), (1024, 1216), (2560, 456), (1 << 30, 152)]
-BWD_ROUNDS = [(100003, 48), (50021, 112), (25013, 208), (12503, 400), (6211, 1024), (3301, 2064), (1093, 4112), (1200, 7168),
-              (1093, 8192), (801, 8208), (801, 16384), (1000, 20000)]
+BWD_ROUNDS = [(100003, 48), (50021, 112), (25013, 208), (12503, 400), (6211, 1024), (3301, 2064), (1093, 4112),
+              (1200, 7168), (1093, 8192), (801, 8208), (801, 16384), (1000, 20000)]
 
 
 @pytest.mark.parametrize("T,H", BWD_ROUNDS)
@@ -179,8 +179,8 @@ def test_rmsnorm_bwd_of_many_rows_per_block(T, H, dtype, res, pad):
 
 
 # --------------------------------------------------------------------------------------- route
-@pytest.mark.parametrize("T,E,k,n_group", [(5, 64, 8, 1), (900, 64, 8, 1), (900, 33, 12, 1), (5, 256, 8, 8), (900, 256, 8, 8),
-                                           (40, 500, 5, 5)])
+@pytest.mark.parametrize("T,E,k,n_group", [(5, 64, 8, 1), (900, 64, 8, 1), (900, 33, 12, 1), (5, 256, 8, 8),
+                                           (900, 256, 8, 8), (40, 500, 5, 5)])
 @pytest.mark.parametrize("renorm", [0, 1])
 @pytest.mark.parametrize("bias", [False, True])
 def test_route_softmax_of_an_infinite_logit_is_no_number(T, E, k, n_group, renorm, bias):
@@ -256,7 +256,8 @@ def test_route_of_several_places_per_lane_whose_keys_differ_in_their_last_bits(T
     assert np.array_equal(ids, np.argsort(-key, axis=1, kind="stable")[:, :k])
 
 
-@pytest.mark.parametrize("T,E,k", [(300, 24, 4), (300, 64, 8), (300, 64, 16), (300, 128, 16), (300, 256, 8), (300, 500, 16)])
+@pytest.mark.parametrize("T,E,k", [(300, 24, 4), (300, 64, 8), (300, 64, 16), (300, 128, 16), (300, 256, 8),
+                                   (300, 500, 16)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [0, 1])
 def test_route_bwd_of_ids_that_come_twice(T, E, k, score, renorm):
@@ -356,7 +357,8 @@ def test_gradients_and_routing_beyond_2_to_the_31_elements():
     h[-5:], dy[-5:] = tail_h, tail_dy
     w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
     rstd = torch.ones(T, device="cuda")
-    dx, dw, few, dws = torch.empty_like(h), torch.empty(H, device="cuda"), torch.empty_like(tail_h), torch.empty(H, device="cuda")
+    dx, few = torch.empty_like(h), torch.empty_like(tail_h)
+    dw, dws = torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
     ws = torch.empty(tdx.tdx_rmsnorm_bwd_workspace_size(T, H, 0), dtype=torch.uint8, device="cuda")
     tdx.check(tdx.tdx_rmsnorm_bwd(dy, h, w, rstd, None, dx, dw, ws, T, H, 0))
     tdx.check(tdx.tdx_rmsnorm_bwd(tail_dy, tail_h, w, rstd[-5:].clone(), None, few, dws, ws, 5, H, 0))
