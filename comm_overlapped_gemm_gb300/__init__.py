@@ -1,7 +1,8 @@
 """Python binding of libtdx (tile-pipelined collective+GEMM kernels on sm_103a: AllGather+GEMM,
 GEMM+ReduceScatter, GEMM+AllReduce, mixture-of-experts AllToAll dispatch + grouped GEMM and grouped
-GEMM + combine) and of the row-wise operators around them (root-mean-square norm, routing to
-experts, gated SiLU, each with its gradient).
+GEMM + combine), of the row-wise operators around them (root-mean-square norm, routing to
+experts, gated SiLU, each with its gradient) and of the products without communication (linear layer,
+products grouped by expert, the sum of a token's expert rows, each with its gradient).
 
 Argument marshalling only: every function below converts its arguments (torch tensors or raw
 device pointers) into the plain pointers and sizes of the C ABI in ``include/tdx.h`` and calls the
@@ -23,6 +24,7 @@ TDX_BF16, TDX_FP8_E4M3, TDX_FP32 = 0, 1, 2
 TDX_FUSED, TDX_GEMM_ONLY, TDX_MOVE_ONLY, TDX_CONSUMER_ONLY = 0, 1, 2, 3
 TDX_PRODUCER_SM, TDX_PRODUCER_COPY_ENGINE = 0, 1
 TDX_SCORE_SOFTMAX, TDX_SCORE_SIGMOID = 0, 1
+TDX_ACT_NONE, TDX_ACT_RELU, TDX_ACT_GELU, TDX_ACT_GELU_TANH, TDX_ACT_SILU, TDX_ACT_SWIGLU = 0, 1, 2, 3, 4, 5
 OP_AG, OP_RS, OP_AR = 0, 1, 2
 TDX_EPOCH_DEVICE = 0xFFFFFFFF
 
@@ -32,7 +34,9 @@ EXPORTED = ["tdx_opts_default", "tdx_workspace_size", "tdx_workspace_init", "tdx
             "tdx_moe_dispatch_gemm", "tdx_moe_combine_workspace_size", "tdx_moe_combine_plan_info",
             "tdx_moe_gemm_combine", "tdx_norm_opts_default", "tdx_rmsnorm", "tdx_rmsnorm_bwd_workspace_size",
             "tdx_rmsnorm_bwd", "tdx_route_opts_default", "tdx_moe_route", "tdx_moe_route_bwd",
-            "tdx_act_opts_default", "tdx_swiglu", "tdx_swiglu_bwd"]
+            "tdx_act_opts_default", "tdx_swiglu", "tdx_swiglu_bwd", "tdx_linear_opts_default", "tdx_linear",
+            "tdx_linear_act_bwd_workspace_size", "tdx_linear_act_bwd", "tdx_linear_bwd", "tdx_grouped_gemm",
+            "tdx_grouped_gemm_bwd", "tdx_combine_opts_default", "tdx_moe_combine", "tdx_moe_combine_bwd"]
 
 
 class tdx_opts(ctypes.Structure):
@@ -91,6 +95,31 @@ class tdx_act_opts(ctypes.Structure):
     ]
 
 
+class tdx_linear_opts(ctypes.Structure):
+    _fields_ = [
+        ("out_dtype", ctypes.c_int),
+        ("act", ctypes.c_int),
+        ("alpha", ctypes.c_float),
+        ("out_scale", ctypes.c_float),
+        ("dw_dtype", ctypes.c_int),
+        ("accumulate", ctypes.c_int),
+        ("ld_a", ctypes.c_int64),
+        ("ld_b", ctypes.c_int64),
+        ("ld_c", ctypes.c_int64),
+        ("ld_residual", ctypes.c_int64),
+        ("ld_z", ctypes.c_int64),
+        ("device_status", ctypes.c_void_p),
+    ]
+
+
+class tdx_combine_opts(ctypes.Structure):
+    _fields_ = [
+        ("out_dtype", ctypes.c_int),
+        ("ld_z", ctypes.c_int64),
+        ("ld_out", ctypes.c_int64),
+    ]
+
+
 class TdxError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -105,6 +134,7 @@ def _load():
     PP = ctypes.POINTER(ctypes.c_void_p)
     OP = ctypes.POINTER(tdx_opts)
     NP, RP, AP = ctypes.POINTER(tdx_norm_opts), ctypes.POINTER(tdx_route_opts), ctypes.POINTER(tdx_act_opts)
+    LP, CP = ctypes.POINTER(tdx_linear_opts), ctypes.POINTER(tdx_combine_opts)
     sig = {
         "tdx_opts_default": (I, [OP]),
         "tdx_workspace_size": (I, [I, I, I, I, I, I, OP, ctypes.POINTER(SZ)]),
@@ -134,6 +164,16 @@ def _load():
         "tdx_act_opts_default": (I, [AP]),
         "tdx_swiglu": (I, [P, P, P, P, I, I, I, AP, P]),
         "tdx_swiglu_bwd": (I, [P, P, P, I, I, I, AP, P]),
+        "tdx_linear_opts_default": (I, [LP]),
+        "tdx_linear": (I, [P, P, P, P, P, P, P, I, I, I, I, LP, P]),
+        "tdx_linear_act_bwd_workspace_size": (I, [I, I, I, LP, ctypes.POINTER(SZ)]),
+        "tdx_linear_act_bwd": (I, [P, P, P, P, P, SZ, I, I, I, LP, P]),
+        "tdx_linear_bwd": (I, [P, P, P, P, P, P, I, I, I, I, LP, P]),
+        "tdx_grouped_gemm": (I, [P, P, P, P, P, P, P, I, I, I, I, I, LP, P]),
+        "tdx_grouped_gemm_bwd": (I, [P, P, P, P, P, P, I, I, I, I, I, LP, P]),
+        "tdx_combine_opts_default": (I, [CP]),
+        "tdx_moe_combine": (I, [P, P, P, P, I, I, I, I, I, CP, P]),
+        "tdx_moe_combine_bwd": (I, [P, P, P, P, P, P, I, I, I, I, I, CP, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -439,3 +479,75 @@ def tdx_swiglu(y, out, row_scale, dest, R: int, I: int, dtype: int, opts=None, s
 
 def tdx_swiglu_bwd(y, dout, dy, R: int, I: int, dtype: int, opts=None, stream=None) -> int:
     return _lib.tdx_swiglu_bwd(_ptr(y), _ptr(dout), _ptr(dy), R, I, dtype, opts, _stream(stream))
+
+
+# ------------------------------------------------------------- products without communication
+def make_linear_opts(**kw) -> tdx_linear_opts:
+    """A tdx_linear_opts filled with the library defaults, then the given fields. ``device_status`` may be
+    a tensor; the struct keeps it alive."""
+    status = kw.pop("device_status", None)
+    o = _fill_opts(tdx_linear_opts(), _lib.tdx_linear_opts_default, kw)
+    o.device_status = _ptr(status)
+    o._keep = status
+    return o
+
+
+def make_combine_opts(**kw) -> tdx_combine_opts:
+    """A tdx_combine_opts filled with the library defaults, then the given fields."""
+    return _fill_opts(tdx_combine_opts(), _lib.tdx_combine_opts_default, kw)
+
+
+def tdx_linear_opts_default() -> tdx_linear_opts:
+    return make_linear_opts()
+
+
+def tdx_combine_opts_default() -> tdx_combine_opts:
+    return make_combine_opts()
+
+
+def tdx_linear(A, B, bias, residual, row_scale, C, z, M: int, K: int, N: int, dtype: int, opts=None, stream=None) -> int:
+    return _lib.tdx_linear(_ptr(A), _ptr(B), _ptr(bias), _ptr(residual), _ptr(row_scale), _ptr(C), _ptr(z), M, K, N,
+                           dtype, opts, _stream(stream))
+
+
+def tdx_linear_act_bwd_workspace_size(M: int, N: int, dtype: int, opts=None) -> int:
+    out = ctypes.c_size_t(0)
+    st = _lib.tdx_linear_act_bwd_workspace_size(M, N, dtype, opts, ctypes.byref(out))
+    if st != TDX_OK:
+        raise TdxError(st, "tdx_linear_act_bwd_workspace_size")
+    return int(out.value)
+
+
+def tdx_linear_act_bwd(dy, z, dz, dbias, workspace, M: int, N: int, dtype: int, opts=None, stream=None,
+                       workspace_bytes: int | None = None) -> int:
+    wsb = workspace_bytes if workspace_bytes is not None else 0 if workspace is None else _nbytes(workspace)
+    return _lib.tdx_linear_act_bwd(_ptr(dy), _ptr(z), _ptr(dz), _ptr(dbias), _ptr(workspace), wsb, M, N, dtype, opts,
+                                   _stream(stream))
+
+
+def tdx_linear_bwd(dz, A, B, dres, dA, dB, M: int, K: int, N: int, dtype: int, opts=None, stream=None) -> int:
+    return _lib.tdx_linear_bwd(_ptr(dz), _ptr(A), _ptr(B), _ptr(dres), _ptr(dA), _ptr(dB), M, K, N, dtype, opts,
+                               _stream(stream))
+
+
+def tdx_grouped_gemm(X, offsets, B, row_scale, expert_scale, Y, z, R: int, K: int, N: int, E: int, dtype: int,
+                     opts=None, stream=None) -> int:
+    return _lib.tdx_grouped_gemm(_ptr(X), _ptr(offsets), _ptr(B), _ptr(row_scale), _ptr(expert_scale), _ptr(Y), _ptr(z),
+                                 R, K, N, E, dtype, opts, _stream(stream))
+
+
+def tdx_grouped_gemm_bwd(dY, X, offsets, B, dX, dB, R: int, K: int, N: int, E: int, dtype: int, opts=None,
+                         stream=None) -> int:
+    return _lib.tdx_grouped_gemm_bwd(_ptr(dY), _ptr(X), _ptr(offsets), _ptr(B), _ptr(dX), _ptr(dB), R, K, N, E, dtype,
+                                     opts, _stream(stream))
+
+
+def tdx_moe_combine(Z, dest, gates, out, R: int, T: int, H: int, topk: int, dtype: int, opts=None, stream=None) -> int:
+    return _lib.tdx_moe_combine(_ptr(Z), _ptr(dest), _ptr(gates), _ptr(out), R, T, H, topk, dtype, opts,
+                                _stream(stream))
+
+
+def tdx_moe_combine_bwd(dout, Z, dest, gates, dZ, dgates, R: int, T: int, H: int, topk: int, dtype: int, opts=None,
+                        stream=None) -> int:
+    return _lib.tdx_moe_combine_bwd(_ptr(dout), _ptr(Z), _ptr(dest), _ptr(gates), _ptr(dZ), _ptr(dgates), R, T, H, topk,
+                                    dtype, opts, _stream(stream))

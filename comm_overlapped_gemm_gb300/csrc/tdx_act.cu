@@ -1,6 +1,7 @@
 // Gated SiLU between two products and its gradient (tdx_swiglu, tdx_swiglu_bwd).
 #include <algorithm>
 
+#include "tdx_actmath.cuh"
 #include "tdx_rows.cuh"
 
 namespace tdx {
@@ -24,44 +25,6 @@ struct ActParams {
   int64_t ld_y, ld_out;
   float inv_scale;
 };
-
-// 2^x and 1/x by the special-function unit (2 and 1 ulp), subnormal results 0
-__device__ __forceinline__ float power_of_2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float reciprocal(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// a * sigmoid(a) of two values; sigmoid(a) and 1 - sigmoid(a). For fp32 results (kExact) with expf and the IEEE
-// quotient, which costs nothing there (65536 x 2048 fp32 224 us either way). For the others exp(-a) = 2^(-a log2 e)
-// and the reciprocal are approximate: within 2^-22 * (4 + |a|) relative, |a| < 89, which a rounding to 8 bits hides;
-// with the exact forms that kernel is bound by issue slots (262144 x 2048 bf16, one vector per thread: 669 us). The
-// divisor is taken times 1/16, so that its reciprocal is no subnormal where exp(-a) is below fp32's largest.
-// exp(-a) = inf gives -0 and 0, as the exact quotient does.
-constexpr float kLog2e = 1.44269504f, kPart = 0.0625f;
-template <bool kExact>
-__device__ __forceinline__ f32x2 silu(f32x2 a) {
-  if (kExact) return pair(first(a) / (1.0f + expf(-first(a))), second(a) / (1.0f + expf(-second(a))));
-  const f32x2 z = mul2(a, pair(-kLog2e, -kLog2e)), part = pair(kPart, kPart);
-  const f32x2 d = fma2(pair(power_of_2(first(z)), power_of_2(second(z))), part, part);
-  return mul2(mul2(a, part), pair(reciprocal(first(d)), reciprocal(second(d))));
-}
-template <bool kExact>
-__device__ __forceinline__ float sigmoid(float a, float* rest) {
-  if (kExact) {
-    const float e = expf(-a), s = 1.0f / (1.0f + e);
-    *rest = e < INFINITY ? e * s : 1.0f;   // 1 - s without the difference's cancellation
-    return s;
-  }
-  const float s = kPart * reciprocal(fmaf(power_of_2(-kLog2e * a), kPart, kPart));
-  *rest = 1.0f - s;
-  return s;
-}
 
 // i / d as the high half of i * ceil(2^64 / d): exact as long as i * (the product of d and that - 2^64) < 2^64,
 // that is i < 2^37 for d up to 2^27

@@ -16,7 +16,7 @@ using namespace tdx;
 
 namespace {
 
-constexpr uint32_t kVersion = (1u << 16) | 2u;   // 1.2: norm, routing, gated SiLU
+constexpr uint32_t kVersion = (1u << 16) | 3u;   // 1.3: linear layer, products grouped by expert, combine
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -268,6 +268,24 @@ EncodeTiledFn get_encode() {
   });
   return fn;
 }
+
+}  // namespace
+
+namespace tdx {
+bool encode_map(CUtensorMap* m, const void* base, bool fp8, int rank, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box) {
+  EncodeTiledFn enc = get_encode();
+  if (enc == nullptr) return false;
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+             const_cast<void*>(base), reinterpret_cast<const cuuint64_t*>(dims),
+             reinterpret_cast<const cuuint64_t*>(strides), box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace tdx
+
+namespace {
 
 // 2D map over a row-major (rows x cols) matrix; box = box_cols x box_rows; 128- or 64-byte swizzle.
 bool make_map(CUtensorMap* m, const void* base, bool fp8, long long rows, long long cols, int box_cols,

@@ -1,0 +1,274 @@
+// Host side of tdx_linear, tdx_linear_bwd, tdx_grouped_gemm and tdx_grouped_gemm_bwd: argument checks,
+// tensor maps, the choice of tiles and the launches.
+#include <algorithm>
+
+#include "tdx_linear.h"
+#include "tdx_rows.cuh"
+
+namespace tdx {
+
+tdx_linear_opts linear_defaults() {
+  tdx_linear_opts o;
+  std::memset(&o, 0, sizeof(o));
+  o.out_dtype = TDX_BF16;
+  o.act = TDX_ACT_NONE;
+  o.alpha = 1.0f;
+  o.out_scale = 1.0f;
+  o.dw_dtype = TDX_BF16;
+  return o;
+}
+
+namespace {
+
+constexpr int kMostSize = 1 << 30;
+constexpr int64_t kMostBytes = INT64_C(1) << 40;   // a tensor map's strides stay below
+
+// An operand's matrices as the kernel loads them: `rows` x `cols` elements with `cols` contiguous,
+// E of them `step` elements apart
+struct Operand {
+  const void* p;
+  int64_t rows, cols, ld, step;
+  int E;
+};
+
+bool map_of(CUtensorMap* m, const Operand& o, bool fp8, int rank, int box_rows) {
+  const uint64_t elt = fp8 ? 1 : 2;
+  const uint64_t dims[3] = {static_cast<uint64_t>(o.cols), static_cast<uint64_t>(std::max<int64_t>(o.rows, 1)),
+                            static_cast<uint64_t>(o.E)};
+  const uint64_t strides[2] = {o.ld * elt, (o.E > 1 ? o.step : o.ld) * elt};
+  const uint32_t box[3] = {static_cast<uint32_t>(128 / elt), static_cast<uint32_t>(box_rows), 1};
+  return encode_map(m, o.p, fp8, rank, dims, strides, box);
+}
+
+// How a product of about `tiles256` / `tiles1` pair and single tiles with `nkb` K slices runs
+struct Shape {
+  bool pair;
+  int split;
+};
+
+// Microseconds of one K slice (128 bytes of K) of a pair's 256 x 256 and of a single CTA's tile, and of
+// a tile's start and end
+constexpr float kPairSlice = 0.29f, kSingleSlice = 0.17f, kTileCost = 2.0f, kFoldCost = 2.0f;
+
+Shape choose(int64_t tiles256, int64_t tiles1, int64_t most1, int nkb) {
+  const int sms = sm_count() > 0 ? sm_count() : kRefSMs;
+  Shape best = {true, 1};
+  float t = static_cast<float>((tiles256 + sms / 2 - 1) / (sms / 2)) * (nkb * kPairSlice + kTileCost);
+  for (int s = 1; s <= 8; s *= 2) {
+    if (s > 1 && (s > nkb || most1 * s > 2 * sms)) break;
+    const float one = static_cast<float>((tiles1 * s + sms - 1) / sms) *
+                      ((nkb + s - 1) / s * kSingleSlice + kTileCost + (s > 1 ? kFoldCost : 0.0f));
+    if (one < t) {
+      t = one;
+      best = {false, s};
+    }
+  }
+  return best;
+}
+
+tdx_status stride_ok(int64_t ld, int64_t len, size_t elt, int64_t* out) {
+  const tdx_status s = row_stride(ld, len, elt, out);
+  if (s != TDX_OK) return s;
+  return *out * static_cast<int64_t>(elt) < kMostBytes ? TDX_OK : TDX_ERR_UNSUPPORTED;
+}
+
+// The run of one product: p holds sizes (M, N, K, cols, E, offsets) and the epilogue
+tdx_status run(Form form, Group group, bool fp8, LinParams& p, const Operand& a, const Operand& b, cudaStream_t st) {
+  const int bk = fp8 ? 128 : 64;
+  const int64_t rows = p.M, E = p.E;
+  int64_t t256, t1, most1, most256;
+  const int w256 = p.gated ? 128 : 256, w1 = p.gated ? lin_block_n(fp8, false) / 2 : lin_block_n(fp8, false);
+  const int64_t n256 = (p.cols + w256 - 1) / w256, n1 = (p.cols + w1 - 1) / w1;
+  int64_t k = p.K;
+  if (group == kRows) {
+    // tiles of E runs of unknown lengths: at most one part tile more per run that has rows
+    const int64_t runs = std::min(E, rows);
+    most256 = (rows + runs * 255) / 256 * n256;
+    most1 = (rows + runs * 127) / 128 * n1;
+    t256 = std::min((rows + runs * 128) / 256 + 1, most256) * 1;
+    t256 = std::max<int64_t>(std::min((rows / 256 + (runs + 1) / 2) * n256, most256), 1);
+    t1 = std::max<int64_t>(std::min((rows / 128 + (rows > runs * 64 ? (runs + 1) / 2 : runs)) * n1, most1), 1);
+  } else {
+    most256 = t256 = (rows + 255) / 256 * n256 * E;
+    most1 = t1 = (rows + 127) / 128 * n1 * E;
+    if (group == kSums) k = (k + E - 1) / E;
+  }
+  const int nkb = static_cast<int>((k + bk - 1) / bk);
+  const Shape shape = choose(t256, t1, most1, nkb);
+  const int64_t most = shape.pair ? most256 : most1;
+  if (most + kMoeMaxExperts * std::max(n1, n256) >= INT64_C(0x7FFFFFFF)) return TDX_ERR_UNSUPPORTED;
+  const int bn = lin_block_n(fp8, shape.pair);
+  const int width = p.gated ? bn / 2 : bn;
+  const int tm = lin_tile_rows(shape.pair);
+  p.tiles_n = (p.cols + width - 1) / width;
+  p.tiles_m = group == kRows ? 0 : (p.M + tm - 1) / tm;
+  p.items = group == kRows ? 0 : static_cast<int>(most);
+  p.group_n = std::min(p.tiles_n, shape.pair ? 8 : 16);
+  p.split = shape.split;
+  // an operand that one tile alone reads is streamed through L2, others are kept there
+  p.keep_a = p.tiles_n > 1 ? 1 : 0;
+  p.keep_b = group == kRows ? (rows > std::min(E, rows) * tm ? 1 : 0) : (p.tiles_m > 1 ? 1 : 0);
+  const int b_rows = form == NT ? 128 : bk;
+  if (!map_of(&p.tm_a, a, fp8, 2, form == TN ? bk : kBM) || !map_of(&p.tm_b, b, fp8, 3, b_rows)) return TDX_ERR_CUDA;
+  const int want = static_cast<int>(most);
+  if (fp8) return launch_linear_e4m3(group, shape.pair, p, want, st);
+  return form == NN   ? launch_linear_nn(group, shape.pair, p, want, st)
+         : form == NT ? launch_linear_nt(group, shape.pair, p, want, st)
+                      : launch_linear_tn(group, shape.pair, p, want, st);
+}
+
+bool act_known(tdx_activation a) { return a >= TDX_ACT_NONE && a <= TDX_ACT_SWIGLU; }
+
+// The forward product; E = 0: the linear layer, else grouped
+tdx_status forward(const void* A, const int32_t* offsets, const void* B, const void* bias, const void* residual,
+                   const float* row_scale, const float* expert_scale, void* C, void* z, int M, int K, int N, int E,
+                   tdx_dtype dtype, const tdx_linear_opts* opts, void* stream) {
+  const tdx_linear_opts o = opts ? *opts : linear_defaults();
+  if (M < 0 || K <= 0 || N <= 0 || !known(dtype) || !known(o.out_dtype) || !act_known(o.act)) return TDX_ERR_INVALID_ARG;
+  if (A == nullptr || B == nullptr || C == nullptr || !std::isfinite(o.alpha) || !usable_scale(o.out_scale))
+    return TDX_ERR_INVALID_ARG;
+  const bool gated = o.act == TDX_ACT_SWIGLU, fp8 = dtype == TDX_FP8_E4M3;
+  if (gated && N % 2 != 0) return TDX_ERR_INVALID_ARG;
+  if (dtype == TDX_FP32 || M > kMostSize || K > kMostSize || N > kMostSize) return TDX_ERR_UNSUPPORTED;
+  LinParams p;
+  std::memset(&p, 0, sizeof(p));
+  const int64_t cols = gated ? N / 2 : N, elt = fp8 ? 1 : 2, out = static_cast<int64_t>(bytes_of(o.out_dtype));
+  int64_t ld_a, ld_b;
+  tdx_status s;
+  if ((s = stride_ok(o.ld_a, K, elt, &ld_a)) != TDX_OK || (s = stride_ok(o.ld_b, N, elt, &ld_b)) != TDX_OK) return s;
+  if ((s = row_stride(o.ld_c, cols, out, &p.ld_out)) != TDX_OK) return s;
+  if ((s = row_stride(o.ld_residual, cols, 2, &p.ld_res)) != TDX_OK) return s;
+  if ((s = row_stride(o.ld_z, N, 2, &p.ld_z)) != TDX_OK) return s;
+  if (K * elt % 16 != 0 || cols * elt % 16 != 0 || cols * 2 % 16 != 0 || cols * out % 16 != 0) return TDX_ERR_ALIGNMENT;
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(C, 16) || !aligned(bias, 16) || !aligned(residual, 16) ||
+      !aligned(z, 16) || !aligned(row_scale, 4) || !aligned(expert_scale, 4) || !aligned(offsets, 4) ||
+      !aligned(o.device_status, 4))
+    return TDX_ERR_ALIGNMENT;
+  const int64_t step = K * ld_b;
+  if (E > 1 && (ld_b > kMostBytes / K || step * elt >= kMostBytes)) return TDX_ERR_UNSUPPORTED;
+  if (M == 0) return TDX_OK;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.cols = static_cast<int>(cols);
+  p.E = E > 0 ? E : 1;
+  p.offsets = offsets;
+  p.gated = gated ? 1 : 0;
+  p.act = o.act;
+  p.out_type = o.out_dtype;
+  p.alpha = o.alpha;
+  p.inv_out_scale = 1.0f / o.out_scale;
+  p.row_scale = row_scale;
+  p.expert_scale = expert_scale;
+  p.bias = static_cast<const bf16*>(bias);
+  p.residual = static_cast<const bf16*>(residual);
+  p.z = static_cast<bf16*>(z);
+  p.out = C;
+  p.status = o.device_status;
+  return run(NN, E > 0 ? kRows : kFlat, fp8, p, {A, M, K, ld_a, 0, 1}, {B, K, N, ld_b, step, p.E},
+             static_cast<cudaStream_t>(stream));
+}
+
+// Both gradients; E = 0: the linear layer, else grouped
+tdx_status backward(const void* dz, const void* A, const int32_t* offsets, const void* B, const void* dres, void* dA,
+                    void* dB, int M, int K, int N, int E, tdx_dtype dtype, const tdx_linear_opts* opts, void* stream) {
+  const tdx_linear_opts o = opts ? *opts : linear_defaults();
+  if (M < 0 || K <= 0 || N <= 0 || !known(dtype) || !known(o.out_dtype) || !known(o.dw_dtype) || !act_known(o.act))
+    return TDX_ERR_INVALID_ARG;
+  if (dz == nullptr || (dA == nullptr && dB == nullptr) || (dA != nullptr && B == nullptr) ||
+      (dB != nullptr && A == nullptr) || (dres != nullptr && dA == nullptr) || o.act != TDX_ACT_NONE ||
+      !std::isfinite(o.alpha) || o.accumulate < 0 || o.accumulate > 1)
+    return TDX_ERR_INVALID_ARG;
+  if (dtype != TDX_BF16 || o.out_dtype == TDX_FP8_E4M3 || o.dw_dtype == TDX_FP8_E4M3 || M > kMostSize ||
+      K > kMostSize || N > kMostSize)
+    return TDX_ERR_UNSUPPORTED;
+  int64_t ld_a, ld_b, ld_z, ld_da, ld_res;
+  tdx_status s;
+  if ((s = stride_ok(o.ld_a, K, 2, &ld_a)) != TDX_OK || (s = stride_ok(o.ld_b, N, 2, &ld_b)) != TDX_OK ||
+      (s = stride_ok(o.ld_z, N, 2, &ld_z)) != TDX_OK || (s = row_stride(o.ld_residual, K, 2, &ld_res)) != TDX_OK ||
+      (s = row_stride(o.ld_c, K, bytes_of(o.out_dtype), &ld_da)) != TDX_OK)
+    return s;
+  if (K % 8 != 0 || N % 8 != 0) return TDX_ERR_ALIGNMENT;
+  if (!aligned(dz, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(dres, 16) || !aligned(dA, 16) ||
+      !aligned(dB, 16) || !aligned(offsets, 4) || !aligned(o.device_status, 4))
+    return TDX_ERR_ALIGNMENT;
+  const int64_t step = K * ld_b;
+  if (E > 1 && (ld_b > kMostBytes / K || step * 2 >= kMostBytes)) return TDX_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  LinParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.E = E > 0 ? E : 1;
+  p.offsets = offsets;
+  p.act = TDX_ACT_NONE;
+  p.alpha = o.alpha;
+  p.inv_out_scale = 1.0f;
+  p.status = o.device_status;
+  if (dA != nullptr && M > 0) {
+    LinParams q = p;
+    q.M = M;
+    q.N = q.cols = K;
+    q.K = N;
+    q.residual = static_cast<const bf16*>(dres);
+    q.ld_res = ld_res;
+    q.out = dA;
+    q.ld_out = ld_da;
+    q.out_type = o.out_dtype;
+    if ((s = run(NT, E > 0 ? kRows : kFlat, false, q, {dz, M, N, ld_z, 0, 1}, {B, K, N, ld_b, step, p.E}, st)) != TDX_OK)
+      return s;
+  }
+  if (dB != nullptr) {
+    LinParams q = p;
+    q.M = K;
+    q.N = q.cols = N;
+    q.K = M;
+    q.out = dB;
+    q.ld_out = ld_b;
+    q.out_step = step;
+    q.out_type = o.dw_dtype;
+    q.accumulate = o.accumulate;
+    return run(TN, E > 0 ? kSums : kFlat, false, q, {A, M, K, ld_a, 0, 1}, {dz, M, N, ld_z, 0, 1}, st);
+  }
+  return TDX_OK;
+}
+
+}  // namespace
+}  // namespace tdx
+
+using namespace tdx;
+
+extern "C" {
+
+tdx_status tdx_linear_opts_default(tdx_linear_opts* opts) {
+  if (opts == nullptr) return TDX_ERR_INVALID_ARG;
+  *opts = linear_defaults();
+  return TDX_OK;
+}
+
+tdx_status tdx_linear(const void* A, const void* B, const void* bias, const void* residual, const float* row_scale,
+                      void* C, void* z, int M, int K, int N, tdx_dtype dtype, const tdx_linear_opts* opts,
+                      void* stream) {
+  return forward(A, nullptr, B, bias, residual, row_scale, nullptr, C, z, M, K, N, 0, dtype, opts, stream);
+}
+
+tdx_status tdx_linear_bwd(const void* dz, const void* A, const void* B, const void* dres, void* dA, void* dB, int M,
+                          int K, int N, tdx_dtype dtype, const tdx_linear_opts* opts, void* stream) {
+  return backward(dz, A, nullptr, B, dres, dA, dB, M, K, N, 0, dtype, opts, stream);
+}
+
+tdx_status tdx_grouped_gemm(const void* X, const int32_t* offsets, const void* B, const float* row_scale,
+                            const float* expert_scale, void* Y, void* z, int R, int K, int N, int E, tdx_dtype dtype,
+                            const tdx_linear_opts* opts, void* stream) {
+  if (E <= 0 || offsets == nullptr) return TDX_ERR_INVALID_ARG;
+  if (E > kMoeMaxExperts) return TDX_ERR_UNSUPPORTED;
+  return forward(X, offsets, B, nullptr, nullptr, row_scale, expert_scale, Y, z, R, K, N, E, dtype, opts, stream);
+}
+
+tdx_status tdx_grouped_gemm_bwd(const void* dY, const void* X, const int32_t* offsets, const void* B, void* dX,
+                                void* dB, int R, int K, int N, int E, tdx_dtype dtype, const tdx_linear_opts* opts,
+                                void* stream) {
+  if (E <= 0 || offsets == nullptr) return TDX_ERR_INVALID_ARG;
+  if (E > kMoeMaxExperts) return TDX_ERR_UNSUPPORTED;
+  return backward(dY, X, offsets, B, nullptr, dX, dB, R, K, N, E, dtype, opts, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,653 @@
+// The product kernel behind tdx_linear, tdx_linear_bwd, tdx_grouped_gemm and tdx_grouped_gemm_bwd:
+// D = A @ B with fp32 accumulators in Tensor Memory and an epilogue of scales, bias, activation,
+// residual and one rounding.
+//
+// Forms. A is M x K, B is K x N; either may lie in memory with K or with its other dimension
+// contiguous, and the tensor cores take both, so no operand is ever transposed by a pass of its own:
+//   NN  A rows along K, B rows along N      (the layer itself)
+//   NT  A rows along K, B stored N x K      (input gradient: dz @ weights^T)
+//   TN  A stored K x M, B rows along N      (weight gradient: inputs^T @ dz)
+// Groups. kFlat: one product. kRows: the M rows fall into E runs, run e multiplied by B[e]. kSums:
+// the K rows of both operands fall into E runs, run e summed into output e.
+//
+// Roles (12 warps, one CTA per SM, persistent over tiles):
+//   warp 0 lane 0  TMA loads of 128-byte K slices into a ring of shared-memory slots
+//   warp 1 lane 0  tcgen05.mma into one of two accumulators; commits free slots, hand over accumulators
+//   warp 2         kSums: a run's last slice also holds rows of the next run; they are cleared in shared
+//                  memory, in both operands (0 times a foreign infinity would still be a NaN)
+//   warps 4-11     epilogue: Tensor Memory -> registers -> output, while the next tile is multiplied
+//
+// Pairs (kPair): two CTAs run one 2-SM MMA stream on a 256 x 256 tile, each staging its 128 rows of A
+// and half of B. Single CTAs take 128 x BN tiles; when they are fewer than the SMs a cluster of `split`
+// CTAs shares a tile's K slices, and the partial accumulators are added through distributed shared
+// memory in rank order, so no workspace is needed and the bits do not change from call to call.
+//
+// Every wait on a barrier is bounded; one that runs out sets *status (if given) and ends the kernel's work.
+#pragma once
+
+#include <atomic>
+
+#include "tdx_actmath.cuh"
+#include "tdx_linear.h"
+#include "tdx_rows.cuh"
+
+namespace tdx {
+
+constexpr int kLinStages = 6;
+
+template <bool FP8, Form FORM, Group GROUP, bool PAIR>
+struct LinCfg {
+  static constexpr int ELT = FP8 ? 1 : 2;
+  static constexpr int BN = lin_block_n(FP8, PAIR);
+  static constexpr int BK = 128 / ELT;                 // K per slot
+  static constexpr int UMMA_K = 32 / ELT;
+  static constexpr int BOX_N = 128 / ELT;              // columns of a box of 128-byte rows
+  static constexpr int BOX_BYTES = BK * 128;           // box of BK rows (operand with K not contiguous)
+  static constexpr bool A_MN = FORM == TN;             // A's rows lie along M
+  static constexpr bool B_MN = FORM != NT;             // B's rows lie along N
+  static constexpr int A_BOXES = A_MN ? kBM / BOX_N : 1;
+  static constexpr int A_BYTES = kBM * 128;
+  static constexpr int N_CTA = PAIR ? BN / 2 : BN;     // columns of B this CTA stages
+  static constexpr int B_BOXES = B_MN ? N_CTA / BOX_N : N_CTA / 128;
+  static constexpr int B_BOX_STEP = B_MN ? BOX_BYTES : 128 * 128;
+  static constexpr int B_BYTES = N_CTA * 128;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = STAGE_BYTES > 32768 ? 4 : kLinStages;
+  static constexpr int TM = PAIR ? 2 * kBM : kBM;      // rows of a tile
+  static constexpr int TMEM_COLS = 2 * BN;
+  static constexpr int NUM_BARS = 3 * STAGES + 5;      // full, empty, tail per slot; accumulators; drain
+  static constexpr int TABLE = GROUP == kFlat ? 0 : 2 * (kMoeMaxExperts + 1) + 2;   // ints
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NUM_BARS * 8 + 64 + TABLE * 4;
+  static constexpr int PART_LD = BN + 4;               // row pitch of a partial: 16 bytes past the banks' period
+  static constexpr uint32_t IDESC = (1u << 4) | ((FP8 ? 0u : 1u) << 7) | ((FP8 ? 0u : 1u) << 10) |
+                                    ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
+                                    (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
+  static_assert(!FP8 || FORM == NN, "e4m3 operands: the forward product only");
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+  static_assert(PAIR || kBM * PART_LD * 4 <= STAGES * STAGE_BYTES, "a partial fits the ring");
+};
+
+// ------------------------------------------------------------------------------------ bounded waits
+static __device__ __noinline__ bool lin_wait_slow(uint32_t* status, uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 15u) == 0u) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > kLinTimeoutNs) {
+        if (status != nullptr) *status = TDX_ERR_TIMEOUT;
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool lin_wait(uint32_t* status, uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_try_wait(bar, parity) || lin_wait_slow(status, bar, parity, abort_flag);
+}
+
+// ------------------------------------------------------------------------------------------- tiles
+struct LinTile {
+  int e;            // expert (0 without groups)
+  int m0, mend;     // first row of this CTA's tile, end of its rows
+  int nt;           // tile column
+  int k0;           // first K index
+  int klen;         // K indexes of the whole tile
+  int kb0, kb1;     // this CTA's slices
+};
+
+// Position `pos` of tm x tn tiles: columns in groups of gn; inside a group rows outer, columns inner, so
+// that the tiles at work at one time share few rows of A and few columns of B
+__device__ __forceinline__ void lin_raster(int pos, int tm, int tn, int gn, int* mt, int* nt) {
+  const int per = tm * gn, full = tn / gn;
+  const int g = pos / per;
+  const int w = g < full ? gn : tn - full * gn;
+  const int q = pos - g * per;
+  *mt = q / w;
+  *nt = g * gn + (q - *mt * w);
+}
+
+template <class C, Group GROUP, bool PAIR>
+__device__ __forceinline__ LinTile lin_tile(const LinParams& p, const int* off, const int* cum, int it, int crank) {
+  LinTile t;
+  int mt;
+  t.k0 = 0;
+  t.klen = p.K;
+  if constexpr (GROUP == kRows) {
+    const int q = it / p.tiles_n;
+    int lo = 0, hi = p.E;   // cum[lo] <= q < cum[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cum[mid] <= q) lo = mid;
+      else hi = mid;
+    }
+    t.e = lo;
+    lin_raster(it - cum[lo] * p.tiles_n, cum[lo + 1] - cum[lo], p.tiles_n, p.group_n, &mt, &t.nt);
+    t.m0 = off[lo] + mt * C::TM;
+    t.mend = off[lo + 1];
+  } else {
+    int pos = it;
+    t.e = 0;
+    if constexpr (GROUP == kSums) {
+      const int per = p.tiles_m * p.tiles_n;
+      t.e = it / per;
+      pos = it - t.e * per;
+      t.k0 = off[t.e];
+      t.klen = off[t.e + 1] - off[t.e];
+    }
+    lin_raster(pos, p.tiles_m, p.tiles_n, p.group_n, &mt, &t.nt);
+    t.m0 = mt * C::TM;
+    t.mend = p.M;
+  }
+  const int nkb = (t.klen + C::BK - 1) / C::BK;
+  if constexpr (PAIR) {
+    t.m0 += crank * kBM;
+    t.kb0 = 0;
+    t.kb1 = nkb;
+  } else {
+    t.kb0 = static_cast<int>(static_cast<int64_t>(nkb) * crank / p.split);
+    t.kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (crank + 1) / p.split);
+  }
+  return t;
+}
+
+// One warp: the runs' ends as given, clamped to [0, rows] and never descending, and the count of tiles
+// (of tile_rows rows) in front of each run
+__device__ __forceinline__ void lin_table(const int32_t* offsets, int E, int rows, int tile_rows, int* off, int* cum) {
+  const int lane = threadIdx.x & 31;
+  int32_t v[(kMoeMaxExperts + 32) / 32];
+#pragma unroll
+  for (int i = 0; i < (kMoeMaxExperts + 32) / 32; ++i) {
+    const int e = i * 32 + lane;
+    v[i] = e <= E ? min(max(__ldg(offsets + e), 0), rows) : 0;
+  }
+  int last = 0, tiles = 0;
+#pragma unroll
+  for (int i = 0; i < (kMoeMaxExperts + 32) / 32; ++i) {
+    if (i * 32 > E) break;
+    int hi = v[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xFFFFFFFFu, hi, o);
+      if (lane >= o) hi = max(hi, up);
+    }
+    hi = max(hi, last);
+    int before = __shfl_up_sync(0xFFFFFFFFu, hi, 1);
+    if (lane == 0) before = last;
+    const int e = i * 32 + lane;
+    // run e - 1 ends here
+    int n = e > 0 && e <= E ? (hi - before + tile_rows - 1) / tile_rows : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xFFFFFFFFu, n, o);
+      if (lane >= o) n += up;
+    }
+    if (e <= E) {
+      off[e] = hi;
+      cum[e] = tiles + n;
+    }
+    last = __shfl_sync(0xFFFFFFFFu, hi, 31);
+    tiles += __shfl_sync(0xFFFFFFFFu, n, 31);
+  }
+}
+
+// ---------------------------------------------------------------------------------------- epilogue
+struct LinRow {
+  int64_t out, res, z;   // element offsets of the row
+  float scale;
+};
+
+template <class C, Group GROUP>
+__device__ __forceinline__ LinRow lin_row(const LinParams& p, const LinTile& t, int row, float tile_scale) {
+  LinRow r;
+  r.out = static_cast<int64_t>(row) * p.ld_out + (GROUP == kSums ? t.e * p.out_step : 0);
+  r.res = static_cast<int64_t>(row) * p.ld_res;
+  r.z = static_cast<int64_t>(row) * p.ld_z;
+  r.scale = p.row_scale != nullptr ? tile_scale * p.row_scale[row] : tile_scale;
+  return r;
+}
+
+// 8 output columns from `col` of one row: v the accumulators (SWIGLU: of the gate), u those of the other half
+__device__ __forceinline__ void lin_finish(const LinParams& p, const LinRow& r, int col, float (&v)[8], float (&u)[8]) {
+  const bool gated = p.act == TDX_ACT_SWIGLU;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= r.scale;
+  if (gated) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] *= r.scale;
+  }
+  if (p.bias != nullptr) {
+    float b[8];
+    load_vec(p.bias + col, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += b[i];
+    if (gated) {
+      load_vec(p.bias + p.cols + col, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] += b[i];
+    }
+  }
+  if (p.z != nullptr) {
+    store_vec(p.z + r.z + col, v);
+    if (gated) store_vec(p.z + r.z + p.cols + col, u);
+  }
+  if (p.act != TDX_ACT_NONE) {
+    act_forward(p.act, p.out_type == TDX_FP32, v);
+    if (gated) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= u[i];
+    }
+  }
+  if (p.residual != nullptr) {
+    float b[8];
+    load_vec(p.residual + r.res + col, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += b[i];
+  }
+  if (p.out_type == TDX_BF16) {
+    bf16* o = static_cast<bf16*>(p.out) + r.out + col;
+    if (p.accumulate) {
+      float b[8];
+      load_vec(o, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += b[i];
+    }
+    store_vec(o, v);
+  } else if (p.out_type == TDX_FP32) {
+    float* o = static_cast<float*>(p.out) + r.out + col;
+    if (p.accumulate) {
+      float b[4], c[4];
+      load_vec(o, b);
+      load_vec(o + 4, c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] += b[i];
+        v[4 + i] += c[i];
+      }
+    }
+    store_vec<8>(o, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= p.inv_out_scale;
+    store_vec(static_cast<e4m3*>(p.out) + r.out + col, v);
+  }
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// ------------------------------------------------------------------------------------------ kernel
+template <bool FP8, Form FORM, Group GROUP, bool PAIR>
+__global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid_constant__ LinParams p) {
+  using C = LinCfg<FP8, FORM, GROUP, PAIR>;
+  constexpr int BN = C::BN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + C::STAGES * C::A_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + C::NUM_BARS);   // [0] Tensor Memory base, [1] abort
+  int* off = reinterpret_cast<int*>(misc + 16);
+  int* cum = off + kMoeMaxExperts + 1;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + C::STAGES), tail0 = smem_u32(bars + 2 * C::STAGES);
+  const uint32_t tfull0 = smem_u32(bars + 3 * C::STAGES), tempty0 = smem_u32(bars + 3 * C::STAGES + 2);
+  const uint32_t drain_bar = smem_u32(bars + 3 * C::STAGES + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = PAIR ? 2 : p.split;   // CTAs per cluster
+  const int crank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const bool leader = !PAIR || crank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      // kSums pairs: both CTAs arrive, as either may have a tail to clear first
+      mbar_init(full0 + 8 * s, PAIR && GROUP == kSums ? 2 : 1);
+      mbar_init(empty0 + 8 * s, 1);
+      mbar_init(tail0 + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull0 + 8 * a, 1);
+      mbar_init(tempty0 + 8 * a, PAIR ? 2 * kNumEpiWarps : kNumEpiWarps);
+    }
+    mbar_init(drain_bar, 1);
+    misc[1] = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&p.tm_a);
+    tma_prefetch_map(&p.tm_b);
+  }
+  if (warp == kMmaWarp) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(&misc[0]), C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&misc[0]), C::TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  griddep_wait();
+  if constexpr (GROUP != kFlat) {
+    if (warp == kCopyWarp0) lin_table(p.offsets, p.E, GROUP == kRows ? p.M : p.K, C::TM, off, cum);
+  }
+  if (S > 1) cluster_sync_all();
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = misc[0];
+  const int cid = blockIdx.x / S, ncl = gridDim.x / S;
+  const int items = GROUP == kRows ? cum[p.E] * p.tiles_n : p.items;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool stop = false;
+      const uint64_t keep_a = policy_of(p.keep_a), keep_b = policy_of(p.keep_b);
+      for (int it = cid; it < items && !stop; it += ncl) {
+        const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, it, crank);
+        // the tile's first column of each half of B (SWIGLU: gate columns, then the other half's)
+        const int n0 = t.nt * (p.gated ? BN / 2 : BN);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          if (!lin_wait(p.status, empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
+            stop = true;
+            break;
+          }
+          const bool tail = GROUP == kSums && (kb + 1) * C::BK > t.klen;
+          const uint32_t own = (tail ? tail0 : full0) + 8 * stage;
+          uint32_t bar = own;
+          if (!PAIR || tail) {
+            mbar_arrive_expect_tx(own, C::STAGE_BYTES);
+          } else {
+            bar = mapa_shared(own, 0);   // both CTAs' slices count on the leader's barrier
+            if (leader) mbar_arrive_expect_tx(own, 2 * C::STAGE_BYTES);
+            else if (GROUP == kSums) mbar_arrive_cluster(bar);
+          }
+          const int k = t.k0 + kb * C::BK;
+          const uint32_t a = smem_u32(sA + stage * C::A_BYTES), b = smem_u32(sB + stage * C::B_BYTES);
+          if constexpr (C::A_MN) {
+#pragma unroll
+            for (int j = 0; j < C::A_BOXES; ++j) {
+              if (PAIR && !tail) tma_load_2d_pair_hint(a + j * C::BOX_BYTES, &p.tm_a, bar, t.m0 + j * C::BOX_N, k, keep_a);
+              else tma_load_2d_hint(a + j * C::BOX_BYTES, &p.tm_a, bar, t.m0 + j * C::BOX_N, k, keep_a);
+            }
+          } else {
+            if (PAIR) tma_load_2d_pair_hint(a, &p.tm_a, bar, k, t.m0, keep_a);
+            else tma_load_2d_hint(a, &p.tm_a, bar, k, t.m0, keep_a);
+          }
+#pragma unroll
+          for (int j = 0; j < C::B_BOXES; ++j) {
+            const uint32_t dst = b + j * C::B_BOX_STEP;
+            const int c = PAIR ? crank * C::N_CTA + j * (C::B_MN ? C::BOX_N : 128) : j * (C::B_MN ? C::BOX_N : 128);
+            const int n = p.gated && c >= BN / 2 ? p.cols + n0 + c - BN / 2 : n0 + c;
+            const int x = C::B_MN ? n : k, y = C::B_MN ? k : n, z = GROUP == kRows ? t.e : 0;
+            if (PAIR && !tail) tma_load_3d_pair_hint(dst, &p.tm_b, bar, x, y, z, keep_b);
+            else tma_load_3d_hint(dst, &p.tm_b, bar, x, y, z, keep_b);
+          }
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && leader) {
+      int stage = 0, local = 0;
+      uint32_t phase = 0;
+      bool stop = false;
+      for (int it = cid; it < items && !stop; it += ncl, ++local) {
+        const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, it, crank);
+        const int acc = local & 1;
+        if (!lin_wait(p.status, tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          if (!lin_wait(p.status, full0 + 8 * stage, phase, abort_flag)) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(sA + stage * C::A_BYTES), b = smem_u32(sB + stage * C::B_BYTES);
+#pragma unroll
+          for (int k = 0; k < C::BK / C::UMMA_K; ++k) {
+            const uint64_t ad = C::A_MN ? smem_desc(a + k * C::UMMA_K * 128, C::BOX_BYTES, 1024, 2u)
+                                        : smem_desc(a + k * 32, 16, 1024, 2u);
+            const uint64_t bd = C::B_MN ? smem_desc(b + k * C::UMMA_K * 128, C::BOX_BYTES, 1024, 2u)
+                                        : smem_desc(b + k * 32, 16, 1024, 2u);
+            const uint32_t accum = kb > t.kb0 || k > 0 ? 1u : 0u;
+            if constexpr (PAIR) {
+              if constexpr (FP8) umma_f8_pair(d, ad, bd, C::IDESC, accum);
+              else umma_bf16_pair(d, ad, bd, C::IDESC, accum);
+            } else {
+              if constexpr (FP8) umma_f8(d, ad, bd, C::IDESC, accum);
+              else umma_bf16(d, ad, bd, C::IDESC, accum);
+            }
+          }
+          if constexpr (PAIR) tc_commit_pair_multicast(empty0 + 8 * stage, static_cast<uint16_t>(0x3));
+          else tc_commit(empty0 + 8 * stage);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (stop) break;
+        if constexpr (PAIR) tc_commit_pair_multicast(tfull0 + 8 * acc, static_cast<uint16_t>(0x3));
+        else tc_commit(tfull0 + 8 * acc);
+      }
+      // every MMA issued has completed once this barrier flips
+      if constexpr (PAIR) tc_commit_pair(drain_bar);
+      else tc_commit(drain_bar);
+      int none = 0;
+      lin_wait(p.status, drain_bar, 0, &none);
+    }
+  } else if (GROUP == kSums && warp == kCopyWarp0) {
+    int slot = 0;           // of the next slice
+    uint32_t par = 0;       // parity each slot's tail barrier is waited for next
+    for (int it = cid; it < items; it += ncl) {
+      const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, it, crank);
+      const int n = t.kb1 - t.kb0, valid = t.klen - (t.kb1 - 1) * C::BK;
+      slot = (slot + n) % C::STAGES;
+      if (n == 0 || valid >= C::BK) continue;
+      const int s = slot == 0 ? C::STAGES - 1 : slot - 1;
+      const bool ok = lin_wait(p.status, tail0 + 8 * s, (par >> s) & 1u, abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      par ^= 1u << s;
+      // a K row is one 128-byte line of every box (the swizzle permutes 16-byte units inside a line)
+      const int units = (C::BK - valid) * 8;
+      for (int i = lane; i < units; i += 32) {
+        const int at = valid * 128 + i * 16;
+#pragma unroll
+        for (int j = 0; j < C::A_BOXES; ++j)
+          *reinterpret_cast<uint4*>(sA + s * C::A_BYTES + j * C::BOX_BYTES + at) = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int j = 0; j < C::B_BOXES; ++j)
+          *reinterpret_cast<uint4*>(sB + s * C::B_BYTES + j * C::BOX_BYTES + at) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_cluster(mapa_shared(full0 + 8 * s, 0));
+        else mbar_arrive(full0 + 8 * s);
+      }
+    }
+  } else if (warp >= kEpiWarp0) {
+    const int quarter = warp & 3, half = (warp - kEpiWarp0) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    int local = 0;
+    for (int it = cid; it < items; it += ncl, ++local) {
+      const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, it, crank);
+      const int acc = local & 1;
+      const bool none = t.kb0 == t.kb1;   // nothing was multiplied: zeros
+      const bool ok = lin_wait(p.status, tfull0 + 8 * acc, (local >> 1) & 1, abort_flag);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN) + lanes;
+      const int in_tile = quarter * 32 + lane;
+      if (!PAIR && S > 1) {
+        // this CTA's partial, into the ring (its slots are free: every MMA of the tile has completed)
+        float* part = reinterpret_cast<float*>(smem);
+#pragma unroll 1
+        for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld_32x32b_x32(d + c, r);
+          tmem_ld_wait(r);
+          if (t.m0 + in_tile < t.mend) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              float4 q = make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]), __uint_as_float(r[i + 2]),
+                                     __uint_as_float(r[i + 3]));
+              if (none) q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              *reinterpret_cast<float4*>(part + in_tile * C::PART_LD + c + i) = q;
+            }
+          }
+        }
+        break;   // one tile per cluster
+      }
+      const int row = t.m0 + in_tile;
+      const bool row_ok = row < t.mend;
+      float scale = p.alpha;
+      if (GROUP == kRows && p.expert_scale != nullptr) scale *= p.expert_scale[t.e];
+      LinRow lr = {};
+      if (row_ok) lr = lin_row<C, GROUP>(p, t, row, scale);
+      const int width = p.gated ? BN / 2 : BN;
+      const int n0 = t.nt * width;
+#pragma unroll 1
+      for (int c = half * (width / 2); c < (half + 1) * (width / 2); c += 32) {
+        uint32_t r[32], q[32];
+        if (n0 + c >= p.cols) break;
+        __syncwarp();
+        tmem_ld_32x32b_x32(d + c, r);
+        if (p.gated) {
+          tmem_ld_32x32b_x32(d + BN / 2 + c, q);
+          tmem_ld_wait(q);
+        }
+        tmem_ld_wait(r);
+        if (row_ok) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            if (n0 + c + i < p.cols) {
+              float v[8], u[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                v[k] = none ? 0.0f : __uint_as_float(r[i + k]);
+                u[k] = none || !p.gated ? 0.0f : __uint_as_float(q[i + k]);
+              }
+              lin_finish(p, lr, n0 + c + i, v, u);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_cluster(mapa_shared(tempty0 + 8 * acc, 0));
+        else mbar_arrive(tempty0 + 8 * acc);
+      }
+    }
+  }
+
+  griddep_launch_dependents();
+  __syncthreads();
+  if (!PAIR && S > 1) {
+    cluster_sync_all();   // every partial of the tile is written
+    if (cid < items && warp >= kEpiWarp0 && !*abort_flag) {
+      const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, cid, crank);
+      const int width = p.gated ? BN / 2 : BN;
+      const int n0 = t.nt * width, groups = width / 8;
+      const int rows = min(kBM, t.mend - t.m0);
+      float scale = p.alpha;
+      if (GROUP == kRows && p.expert_scale != nullptr) scale *= p.expert_scale[t.e];
+      const uint32_t part = smem_u32(smem);
+      const int units = ((rows - crank + S - 1) / S) * groups;   // rows crank, crank + S, ...
+      for (int i = threadIdx.x - kEpiWarp0 * 32; i < units; i += kEpiThreads) {
+        const int r = crank + (i / groups) * S, c = (i % groups) * 8;
+        if (n0 + c >= p.cols) continue;
+        float v[8] = {}, u[8] = {};
+        for (int s = 0; s < S; ++s) {
+          const uint32_t at = mapa_shared(part + (r * C::PART_LD + c) * 4, s);
+          const float4 a = ld_cluster_f4(at), b = ld_cluster_f4(at + 16);
+          v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+          v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+          if (p.gated) {
+            const float4 x = ld_cluster_f4(at + BN / 2 * 4), y = ld_cluster_f4(at + BN / 2 * 4 + 16);
+            u[0] += x.x; u[1] += x.y; u[2] += x.z; u[3] += x.w;
+            u[4] += y.x; u[5] += y.y; u[6] += y.z; u[7] += y.w;
+          }
+        }
+        lin_finish(p, lin_row<C, GROUP>(p, t, t.m0 + r, scale), n0 + c, v, u);
+      }
+    }
+  }
+  if (*abort_flag) {
+    // loads that nothing waited for are given ample time to land before the shared memory is given up
+    for (int i = 0; i < 256; ++i) __nanosleep(1000);
+  }
+  __syncwarp();
+  tc_fence_before();
+  if (S > 1) cluster_sync_all();   // no CTA leaves while its peer may read from it, load into it or arrive on it
+  else __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// -------------------------------------------------------------------------------------------- host
+template <bool FP8, Form FORM, Group GROUP, bool PAIR>
+tdx_status launch_linear_t(const LinParams& p, int want, cudaStream_t stream) {
+  using C = LinCfg<FP8, FORM, GROUP, PAIR>;
+  auto* kernel = tdx_linear_kernel<FP8, FORM, GROUP, PAIR>;
+  // per device: raised shared-memory limit and, for pairs, the clusters that are resident together
+  static std::atomic<int> ready[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return TDX_ERR_CUDA;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.blockDim = dim3(kNumThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = PAIR ? 2 : p.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  int most = dev >= 0 && dev < 64 ? ready[dev].load(std::memory_order_relaxed) : 0;
+  if (most == 0) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
+      return TDX_ERR_CUDA;
+    most = sm_count();
+    if (PAIR) {
+      cfg.gridDim = dim3(2 * most, 1, 1);
+      cfg.attrs = attr + 1;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return TDX_ERR_CUDA;
+      most = n;
+    }
+    if (most <= 0) return TDX_ERR_CUDA;
+    if (dev >= 0 && dev < 64) ready[dev].store(most, std::memory_order_relaxed);
+  }
+  // `want` clusters of work; with a split one cluster per tile, else persistent
+  const int clusters = !PAIR && p.split > 1 ? want : (want < most ? want : most);
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters) * (PAIR ? 2 : p.split), 1, 1);
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR || p.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? TDX_OK : TDX_ERR_CUDA;
+}
+
+template <bool FP8, Form FORM, Group GROUP>
+tdx_status launch_linear_g(const LinParams& p, bool pair, int want, cudaStream_t stream) {
+  return pair ? launch_linear_t<FP8, FORM, GROUP, true>(p, want, stream)
+              : launch_linear_t<FP8, FORM, GROUP, false>(p, want, stream);
+}
+
+}  // namespace tdx

@@ -1,0 +1,50 @@
+// Shared by the product kernel's instances and their host side.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "../../include/tdx.h"
+#include "tdx_internal.h"
+
+namespace tdx {
+
+enum Form { NN, NT, TN };                 // see tdx_linear.cuh
+enum Group { kFlat, kRows, kSums };
+constexpr uint64_t kLinTimeoutNs = 4000000000ull;
+
+// Tile columns: pairs 256. Single CTAs 128, and 256 for e4m3, whose 128-column boxes would not split
+// a 128-column tile into gate and up halves.
+constexpr int lin_block_n(bool fp8, bool pair) { return pair || fp8 ? 256 : 128; }
+constexpr int lin_tile_rows(bool pair) { return pair ? 2 * kBM : kBM; }
+
+struct LinParams {
+  CUtensorMap tm_a, tm_b;
+  int M, N, K;              // output rows, accumulator columns, summed length (kRows: M, kSums: K over all runs)
+  int cols;                 // output columns: N, or N / 2 for SWIGLU
+  int E;
+  const int32_t* offsets;
+  int tiles_m, tiles_n, items, group_n;
+  int split;                // CTAs that share a tile's K slices (single CTAs)
+  int keep_a, keep_b;       // L2 policies of the operands' loads (policy_of)
+  int gated;                // act == TDX_ACT_SWIGLU
+  tdx_activation act;
+  tdx_dtype out_type;
+  int accumulate;
+  float alpha, inv_out_scale;
+  const float* row_scale;
+  const float* expert_scale;
+  const __nv_bfloat16* bias;
+  const __nv_bfloat16* residual;
+  __nv_bfloat16* z;
+  void* out;
+  int64_t ld_out, ld_res, ld_z;
+  int64_t out_step;         // kSums: elements between two experts' outputs
+  uint32_t* status;
+};
+
+tdx_status launch_linear_nn(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream);
+tdx_status launch_linear_nt(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream);
+tdx_status launch_linear_tn(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream);
+tdx_status launch_linear_e4m3(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream);
+
+}  // namespace tdx

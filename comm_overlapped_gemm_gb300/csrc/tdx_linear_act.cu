@@ -1,0 +1,218 @@
+// Gradient of the linear layer's activation and bias (tdx_linear_act_bwd).
+#include <algorithm>
+
+#include "tdx_actmath.cuh"
+#include "tdx_linear.h"
+#include "tdx_rows.cuh"
+
+namespace tdx {
+
+tdx_linear_opts linear_defaults();
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowsAhead = 4;       // rows whose loads a thread has in flight
+constexpr int kMostBlocks = 2432;   // 16 blocks on each of 152 SMs: row chunks are cut to about that many
+
+struct ActBwdParams {
+  const bf16* dy;
+  const bf16* z;
+  bf16* dz;
+  float* part;      // [chunks][N], or dbias itself for one chunk; NULL: no sums
+  int M, cols, chunk;
+  int lanes;        // lanes of a row, a power of two; threads / lanes rows at a time
+  int64_t ld_dy, ld_z;
+};
+
+// dz of the N values z (gates) and u, given dy; SWIGLU alone uses u, and leaves its gradient there
+template <int ACT>
+__device__ __forceinline__ void act_backward(float (&dy)[8], const float (&z)[8], float (&u)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = z[i];
+    if (ACT == TDX_ACT_RELU) {
+      dy[i] = x > 0.0f ? dy[i] : 0.0f;
+    } else if (ACT == TDX_ACT_GELU) {
+      dy[i] *= fmaf(x * kInvRoot2Pi, power_of_2(-0.5f * kLog2e * x * x), 0.5f * erfcf(-kHalfRoot * x));
+    } else if (ACT == TDX_ACT_GELU_TANH) {
+      float rest;
+      const float s = sigmoid<false>(gelu_arg(x), &rest);
+      dy[i] *= s * fmaf(x * rest, kGelu2 * fmaf(3.0f * kGeluCube * x, x, 1.0f), 1.0f);
+    } else if (ACT == TDX_ACT_SILU) {
+      float rest;
+      const float s = sigmoid<false>(x, &rest);
+      dy[i] *= s * fmaf(x, rest, 1.0f);
+    } else if (ACT == TDX_ACT_SWIGLU) {
+      float rest;
+      const float s = sigmoid<false>(x, &rest), ds = dy[i] * s;
+      dy[i] = ds * u[i] * fmaf(x, rest, 1.0f);
+      u[i] = ds * x;
+    }
+  }
+}
+
+// Bound by HBM. A warp reads whole lines of a row (several rows where a row is short), a thread keeps the
+// sums of its 8 columns (16 for SWIGLU) in registers over the rows of its chunk; they are joined in shared memory
+// in a fixed order.
+template <int ACT>
+__global__ void __launch_bounds__(kThreads) tdx_linear_act_bwd_kernel(const __grid_constant__ ActBwdParams p) {
+  constexpr bool kGated = ACT == TDX_ACT_SWIGLU;
+  constexpr int kSums = kGated ? 16 : 8;
+  __shared__ float sm[kThreads][kSums + 1];
+  griddep_launch_dependents();
+  const int at = threadIdx.x % p.lanes, sub = threadIdx.x / p.lanes, step = kThreads / p.lanes;
+  const int col = (blockIdx.x * p.lanes + at) * 8;
+  const bool mine = col < p.cols;
+  const int64_t first = static_cast<int64_t>(blockIdx.y) * p.chunk;
+  const int64_t end = first + p.chunk < p.M ? first + p.chunk : p.M;
+  float sum[kSums] = {};
+  griddep_wait();
+  if (mine) {
+    for (int64_t r0 = first + sub; r0 < end; r0 += kRowsAhead * step) {
+      uint4 qd[kRowsAhead], qz[kRowsAhead], qu[kRowsAhead];
+#pragma unroll
+      for (int k = 0; k < kRowsAhead; ++k) {
+        const int64_t r = r0 + k * step;
+        if (r < end) {
+          qd[k] = __ldcs(reinterpret_cast<const uint4*>(p.dy + r * p.ld_dy + col));
+          if (ACT != TDX_ACT_NONE) qz[k] = __ldcs(reinterpret_cast<const uint4*>(p.z + r * p.ld_z + col));
+          if (kGated) qu[k] = __ldcs(reinterpret_cast<const uint4*>(p.z + r * p.ld_z + p.cols + col));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kRowsAhead; ++k) {
+        const int64_t r = r0 + k * step;
+        if (r < end) {
+          float d[8], z[8], u[8];
+          unpack(qd[k], d, bf16{});
+          if (ACT != TDX_ACT_NONE) unpack(qz[k], z, bf16{});
+          if (kGated) unpack(qu[k], u, bf16{});
+          act_backward<ACT>(d, z, u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] = __fadd_rn(sum[i], d[i]);   // of dz as computed: same bits with and without dz
+          if (kGated) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[kSums - 8 + i] = __fadd_rn(sum[kSums - 8 + i], u[i]);
+          }
+          if (p.dz != nullptr) {
+            store_vec(p.dz + r * p.ld_z + col, d);
+            if (kGated) store_vec(p.dz + r * p.ld_z + p.cols + col, u);
+          }
+        }
+      }
+    }
+  }
+  if (p.part == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < kSums; ++i) sm[threadIdx.x][i] = sum[i];
+  __syncthreads();
+  const int64_t row = static_cast<int64_t>(blockIdx.y) * (kGated ? 2 : 1) * p.cols;
+  for (int i = threadIdx.x; i < p.lanes * kSums; i += kThreads) {
+    const int lane = i / kSums, k = i % kSums;
+    const int c = (blockIdx.x * p.lanes + lane) * 8 + (k & 7);
+    if (c >= p.cols) continue;
+    float a = 0.0f;
+    for (int s = 0; s < step; ++s) a += sm[s * p.lanes + lane][k];
+    p.part[row + c + (k >= 8 ? p.cols : 0)] = a;
+  }
+}
+
+int lanes_of(int cols) {
+  int n = 1;
+  while (n < 32 && n * 8 < cols) n *= 2;
+  return n;
+}
+int col_blocks(int cols) { return (cols + lanes_of(cols) * 8 - 1) / (lanes_of(cols) * 8); }
+
+// Rows of a chunk: as many chunks as kMostBlocks allows, but no shorter than every thread's rows in flight
+int chunk_rows(int M, int cols) {
+  const int chunks = std::max(1, kMostBlocks / col_blocks(cols));
+  const int least = kThreads / lanes_of(cols) * kRowsAhead;
+  return std::max(static_cast<int>((static_cast<int64_t>(M) + chunks - 1) / chunks), least);
+}
+int chunks_of(int M, int cols) {
+  const int rows = chunk_rows(M, cols);
+  return std::max(1, static_cast<int>((static_cast<int64_t>(M) + rows - 1) / rows));
+}
+
+tdx_status launch_act(tdx_activation act, const ActBwdParams& p, dim3 grid, cudaStream_t st) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaSuccess;
+  switch (act) {
+    case TDX_ACT_RELU: e = cudaLaunchKernelEx(&cfg, tdx_linear_act_bwd_kernel<TDX_ACT_RELU>, p); break;
+    case TDX_ACT_GELU: e = cudaLaunchKernelEx(&cfg, tdx_linear_act_bwd_kernel<TDX_ACT_GELU>, p); break;
+    case TDX_ACT_GELU_TANH: e = cudaLaunchKernelEx(&cfg, tdx_linear_act_bwd_kernel<TDX_ACT_GELU_TANH>, p); break;
+    case TDX_ACT_SILU: e = cudaLaunchKernelEx(&cfg, tdx_linear_act_bwd_kernel<TDX_ACT_SILU>, p); break;
+    case TDX_ACT_SWIGLU: e = cudaLaunchKernelEx(&cfg, tdx_linear_act_bwd_kernel<TDX_ACT_SWIGLU>, p); break;
+    default: e = cudaLaunchKernelEx(&cfg, tdx_linear_act_bwd_kernel<TDX_ACT_NONE>, p); break;
+  }
+  return e == cudaSuccess ? TDX_OK : TDX_ERR_CUDA;
+}
+
+tdx_status check_sizes(int M, int N, tdx_dtype dtype, const tdx_linear_opts& o) {
+  if (M < 0 || N <= 0 || !known(dtype) || o.act < TDX_ACT_NONE || o.act > TDX_ACT_SWIGLU) return TDX_ERR_INVALID_ARG;
+  if (o.act == TDX_ACT_SWIGLU && N % 2 != 0) return TDX_ERR_INVALID_ARG;
+  return dtype != TDX_BF16 || M > (1 << 30) || N > (1 << 28) ? TDX_ERR_UNSUPPORTED : TDX_OK;
+}
+
+}  // namespace
+}  // namespace tdx
+
+using namespace tdx;
+
+extern "C" {
+
+tdx_status tdx_linear_act_bwd_workspace_size(int M, int N, tdx_dtype dtype, const tdx_linear_opts* opts, size_t* bytes) {
+  if (bytes == nullptr) return TDX_ERR_INVALID_ARG;
+  const tdx_linear_opts o = opts ? *opts : linear_defaults();
+  const tdx_status s = check_sizes(M, N, dtype, o);
+  if (s != TDX_OK) return s;
+  *bytes = static_cast<size_t>(chunks_of(M, o.act == TDX_ACT_SWIGLU ? N / 2 : N)) * N * sizeof(float);
+  return TDX_OK;
+}
+
+tdx_status tdx_linear_act_bwd(const void* dy, const void* z, void* dz, float* dbias, void* workspace,
+                              size_t workspace_bytes, int M, int N, tdx_dtype dtype, const tdx_linear_opts* opts,
+                              void* stream) {
+  const tdx_linear_opts o = opts ? *opts : linear_defaults();
+  size_t need = 0;
+  tdx_status s = tdx_linear_act_bwd_workspace_size(M, N, dtype, &o, &need);
+  if (s != TDX_OK) return s;
+  const bool gated = o.act == TDX_ACT_SWIGLU;
+  if (dy == nullptr || (dz == nullptr && dbias == nullptr) || (o.act != TDX_ACT_NONE && z == nullptr))
+    return TDX_ERR_INVALID_ARG;
+  ActBwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.cols = gated ? N / 2 : N;
+  if ((s = row_stride(o.ld_c, p.cols, 2, &p.ld_dy)) != TDX_OK || (s = row_stride(o.ld_z, N, 2, &p.ld_z)) != TDX_OK)
+    return s;
+  if (p.cols % 8 != 0) return TDX_ERR_ALIGNMENT;
+  if (!aligned(dy, 16) || !aligned(z, 16) || !aligned(dz, 16) || !aligned(dbias, 16)) return TDX_ERR_ALIGNMENT;
+  if (dbias != nullptr && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need))
+    return TDX_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int chunks = chunks_of(M, p.cols);
+  if (M == 0 && dbias == nullptr) return TDX_OK;
+  p.dy = static_cast<const bf16*>(dy);
+  p.z = static_cast<const bf16*>(z);
+  p.dz = static_cast<bf16*>(dz);
+  p.M = M;
+  p.chunk = chunk_rows(M, p.cols);
+  p.lanes = lanes_of(p.cols);
+  if (dbias != nullptr) p.part = chunks > 1 ? static_cast<float*>(workspace) : dbias;
+  s = launch_act(o.act, p, dim3(static_cast<unsigned>(col_blocks(p.cols)), static_cast<unsigned>(chunks), 1), st);
+  if (s != TDX_OK || dbias == nullptr || chunks == 1) return s;
+  return launch_sum_parts(static_cast<const float*>(workspace), dbias, chunks, N, st);
+}
+
+}  // extern "C"

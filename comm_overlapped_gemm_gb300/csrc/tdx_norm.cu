@@ -658,6 +658,11 @@ tdx_status check_sizes(int T, int H, tdx_dtype dtype) {
 }
 
 }  // namespace
+
+tdx_status launch_sum_parts(const float* part, float* out, int parts, int n, cudaStream_t st) {
+  return launch_rows(tdx_rmsnorm_dweight_kernel, (n + 63) / 64, 1024, 0, st, part, out, parts, n);
+}
+
 }  // namespace tdx
 
 using namespace tdx;
@@ -754,8 +759,7 @@ tdx_status tdx_rmsnorm_bwd(const void* dy, const void* h, const void* weight, co
     s = dtype == TDX_BF16 ? launch_norm_bwd<bf16>(p, &parts, st) : launch_norm_bwd<float>(p, &parts, st);
     if (s != TDX_OK) return s;
   }
-  return launch_rows(tdx_rmsnorm_dweight_kernel, (H + 63) / 64, 1024, 0, st,
-                     static_cast<const float*>(part), dweight, parts, H);
+  return launch_sum_parts(part, dweight, parts, H, st);
 }
 
 }  // extern "C"

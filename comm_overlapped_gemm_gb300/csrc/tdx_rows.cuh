@@ -182,5 +182,7 @@ inline tdx_status row_stride(int64_t ld, int64_t len, size_t elt, int64_t* out) 
 }
 
 int sm_count();   // SMs of the current device, 0 if unknown
+// out[c] = the sum of part[0 .. parts)[c] in a fixed order, n even columns
+tdx_status launch_sum_parts(const float* part, float* out, int parts, int n, cudaStream_t st);
 
 }  // namespace tdx

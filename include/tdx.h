@@ -1,8 +1,10 @@
 /*
  * tdx.h -- C ABI of the tile-pipelined collective+GEMM library (sm_103a): AllGather+GEMM,
  * GEMM+ReduceScatter, GEMM+AllReduce, the mixture-of-experts AllToAll dispatch + grouped GEMM and
- * grouped GEMM + combine, and the row-wise operators around these products (root-mean-square norm,
- * routing to experts, gated SiLU, with their gradients).
+ * grouped GEMM + combine, the row-wise operators around these products (root-mean-square norm,
+ * routing to experts, gated SiLU, with their gradients), and the products that need no communication:
+ * the linear layer, the products grouped by expert and the sum of a token's expert rows, with their
+ * gradients.
  *
  * What the operations are. The Triton-distributed article on cronfeed.work ("Triton-distributed
  * is turning communication into compiler territory"), section "The first move was to expose the
@@ -448,6 +450,133 @@ tdx_status tdx_swiglu(const void* y, void* out, const float* row_scale, const in
  *  y, dy      device, R x 2I of `dtype`; dy may be y itself. dout: R x I of `dtype`. */
 tdx_status tdx_swiglu_bwd(const void* y, const void* dout, void* dy, int R, int I, tdx_dtype dtype,
                           const tdx_act_opts* opts, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Products without communication, with their gradients: the linear layer (tdx_linear), the products
+ * grouped by expert over ragged rows (tdx_grouped_gemm) and the sum of a token's expert rows
+ * (tdx_moe_combine). W ranks whose tensors lie in one buffer, rank after rank, are one call.
+ * Products of bf16 or e4m3 operands are accumulated in fp32 on the tensor cores, in one fixed order
+ * for given sizes; the epilogue is fp32 and every output is rounded once (RNE; e4m3 saturates at
+ * +-448). No call needs a workspace but tdx_linear_act_bwd. Pointers are 16-byte aligned, rows and
+ * strides multiples of 16 bytes (TDX_ERR_ALIGNMENT); fp32 vectors named "scale" and offsets 4-byte.
+ * Row strides are in elements, 0 = dense; below the row's length: TDX_ERR_INVALID_ARG. Outputs overlap
+ * no input unless said so. Sizes K, N, E, H, topk are at least 1; M, R or T of 0 launch nothing but
+ * the zeroing that the formula asks for. A wait inside a kernel that runs out (4 s) ends that kernel's
+ * work and sets opts->device_status. */
+typedef enum {
+  TDX_ACT_NONE = 0,
+  TDX_ACT_RELU = 1,
+  TDX_ACT_GELU = 2,        /* x * Phi(x), Phi the normal distribution function */
+  TDX_ACT_GELU_TANH = 3,   /* 0.5 x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) */
+  TDX_ACT_SILU = 4,        /* x * sigmoid(x) */
+  TDX_ACT_SWIGLU = 5       /* columns [0, N/2) are gates: silu(x[i]) * x[N/2 + i], N/2 output columns */
+} tdx_activation;
+
+typedef struct tdx_linear_opts {
+  tdx_dtype out_dtype;       /* forward: of C or Y (TDX_BF16, the default, TDX_FP32 or TDX_FP8_E4M3);
+                                backward: of dA or dX (TDX_BF16 or TDX_FP32) */
+  tdx_activation act;        /* default TDX_ACT_NONE */
+  float alpha;               /* multiplies the product (the scales of e4m3 operands); default 1, finite */
+  float out_scale;           /* e4m3 output is stored as C / out_scale; default 1; positive and
+                                finite, as its reciprocal */
+  tdx_dtype dw_dtype;        /* backward: of dB (TDX_BF16, the default, or TDX_FP32) */
+  int accumulate;            /* backward: 1 adds to dB as it is (the sum is fp32, then rounded to
+                                dw_dtype); default 0 overwrites it */
+  int64_t ld_a, ld_b;        /* row strides of A or X; of B (and of dB) */
+  int64_t ld_c;              /* of C or Y; backward: of dA or dX */
+  int64_t ld_residual;       /* of residual; tdx_linear_bwd: of dres */
+  int64_t ld_z;              /* of z; backward: of dz or dY (tdx_linear_act_bwd: of z and dz) */
+  uint32_t* device_status;   /* optional device word, set to TDX_ERR_TIMEOUT if a wait ran out and
+                                otherwise left as it is */
+} tdx_linear_opts;
+tdx_status tdx_linear_opts_default(tdx_linear_opts* opts);
+
+/* Linear layer:  v = alpha * row_scale[m] * (A @ B) + bias,  C = act(v) + residual.
+ *  A          device, M x K of `dtype` (TDX_BF16 or TDX_FP8_E4M3); B: K x N of `dtype`.
+ *  bias       optional, N bf16. residual: optional, as C but bf16; C may be residual itself where it
+ *             is bf16 (same stride).
+ *  row_scale  optional, M fp32: the scales of A's rows (tdx_rmsnorm's row_scale).
+ *  C          device, M x N of opts->out_dtype (M x N/2 for TDX_ACT_SWIGLU).
+ *  z          optional, M x N bf16: v, for tdx_linear_act_bwd (C takes act(v) of the unrounded v).
+ * N is a multiple of 8 (bf16) or 16 (e4m3), for TDX_ACT_SWIGLU N/2 is; for e4m3 outputs the output's
+ * columns are multiples of 16.
+ * Activations take approximate exponentials for bf16 and e4m3 outputs, within 2^-22 * (4 + |x|) of the
+ * value (TDX_ACT_GELU_TANH: |x| the exponent's size, 1.6 |x + 0.045 x^3|), and exact ones for fp32. */
+tdx_status tdx_linear(const void* A, const void* B, const void* bias, const void* residual,
+                      const float* row_scale, void* C, void* z, int M, int K, int N, tdx_dtype dtype,
+                      const tdx_linear_opts* opts, void* stream);
+
+/* Gradient of the activation and the bias:  dz = dy * act'(z),  dbias = sum_m dz[m] (unrounded).
+ *  dy         device, M x N bf16 (M x N/2 for TDX_ACT_SWIGLU; opts->ld_c is its stride).
+ *  z, dz      device, M x N bf16; dz may be z itself or, but for TDX_ACT_SWIGLU, dy (same stride). For
+ *             TDX_ACT_NONE z and dz may be NULL (dz is dy); else dz may be NULL where dbias is not.
+ *  dbias      optional, N fp32, overwritten; partial sums over rows are added in a fixed order.
+ *  workspace  tdx_linear_act_bwd_workspace_size() bytes, 256-byte aligned, for dbias only; needs no
+ *             initialisation.
+ *  dtype      TDX_BF16. */
+tdx_status tdx_linear_act_bwd_workspace_size(int M, int N, tdx_dtype dtype, const tdx_linear_opts* opts,
+                                             size_t* bytes);
+tdx_status tdx_linear_act_bwd(const void* dy, const void* z, void* dz, float* dbias, void* workspace,
+                              size_t workspace_bytes, int M, int N, tdx_dtype dtype,
+                              const tdx_linear_opts* opts, void* stream);
+
+/* Gradients of the product:  dA = alpha * dz @ B^T + dres,  dB = alpha * A^T @ dz (+ dB).
+ *  dz         device, M x N bf16; A: M x K bf16 (needed for dB); B: K x N bf16 (needed for dA).
+ *  dres       optional, M x K bf16, with dA only; dA may be dres itself where it is bf16 (same stride).
+ *  dA         optional, M x K of opts->out_dtype. dB: optional, K x N of opts->dw_dtype. One of the two.
+ *  dtype      TDX_BF16. opts->act must be TDX_ACT_NONE. */
+tdx_status tdx_linear_bwd(const void* dz, const void* A, const void* B, const void* dres, void* dA,
+                          void* dB, int M, int K, int N, tdx_dtype dtype, const tdx_linear_opts* opts,
+                          void* stream);
+
+/* Products grouped by expert: rows offsets[e] .. offsets[e+1]-1 of X times B[e],
+ *   v = alpha * row_scale[r] * expert_scale[e] * (X[r] @ B[e]),  Y[r] = act(v).
+ * Rows in front of offsets[0] and from offsets[E] on are left as they are in Y and z.
+ *  X          device, R x K of `dtype` (TDX_BF16 or TDX_FP8_E4M3), rows grouped by expert, as
+ *             tdx_moe_dispatch_gemm lays them out.
+ *  offsets    device, E + 1 int32, ascending (its expert_offsets). Entries are read on the device, taken
+ *             into [0, R] and raised to the largest entry before them.
+ *  B          device, E x K x N of `dtype`, expert e's at e * K * ld_b.
+ *  row_scale  optional, R fp32; expert_scale: optional, E fp32.
+ *  Y, z       as C and z of tdx_linear. E <= 512. */
+tdx_status tdx_grouped_gemm(const void* X, const int32_t* offsets, const void* B, const float* row_scale,
+                            const float* expert_scale, void* Y, void* z, int R, int K, int N, int E,
+                            tdx_dtype dtype, const tdx_linear_opts* opts, void* stream);
+
+/* Their gradients:  dX[r] = alpha * dY[r] @ B[e]^T,  dB[e] = alpha * X_e^T @ dY_e (+ dB[e]) over the
+ * expert's rows; 0 (+ dB[e]) for an expert without rows. Rows of no expert are left as they are in dX.
+ *  dY         device, R x N bf16; X: R x K bf16 (needed for dB); B: E x K x N bf16 (needed for dX).
+ *  dX         optional, R x K of opts->out_dtype. dB: optional, E x K x N of opts->dw_dtype, expert e's at
+ *             e * K * ld_b. One of the two. dtype TDX_BF16, opts->act TDX_ACT_NONE. */
+tdx_status tdx_grouped_gemm_bwd(const void* dY, const void* X, const int32_t* offsets, const void* B,
+                                void* dX, void* dB, int R, int K, int N, int E, tdx_dtype dtype,
+                                const tdx_linear_opts* opts, void* stream);
+
+/* Sum of a token's expert rows:  out[t] = sum_j gates[t][j] * Z[dest[t][j]], j ascending in fp32. With
+ * gates NULL (all 1) it is the gradient of the dispatch by the tokens.
+ *  Z          device, R x H of `dtype` (TDX_BF16 or TDX_FP32).
+ *  dest       device, T x topk int32 (4-byte aligned), as tdx_moe_dispatch_gemm writes it. An entry outside
+ *             [0, R) adds nothing.
+ *  gates      optional, T x topk fp32 (4-byte aligned).
+ *  out        device, T x H of opts->out_dtype (TDX_BF16 or TDX_FP32). 1 <= topk <= 16. */
+typedef struct tdx_combine_opts {
+  tdx_dtype out_dtype;       /* default TDX_BF16 */
+  int64_t ld_z, ld_out;      /* row strides of Z (and dZ), of out (and dout) */
+} tdx_combine_opts;
+tdx_status tdx_combine_opts_default(tdx_combine_opts* opts);
+tdx_status tdx_moe_combine(const void* Z, const int32_t* dest, const float* gates, void* out, int R, int T,
+                           int H, int topk, tdx_dtype dtype, const tdx_combine_opts* opts, void* stream);
+
+/* Its gradient:  dZ[dest[t][j]] = gates[t][j] * dout[t],  dgates[t][j] = sum_h dout[t][h] * Z[dest[t][j]][h].
+ * With gates NULL it is the dispatch itself: each token's row copied to its experts' rows.
+ *  dout       device, T x H of `dtype`; Z, dZ: R x H of `dtype`. dZ: optional; rows that dest does not name
+ *             are left as they are. It may be Z itself (same stride). dest names a row once at most: of two
+ *             writers of one row either may stay.
+ *  dgates     optional (then Z is needed), T x topk fp32 (4-byte aligned), 0 for an entry outside [0, R).
+ *  One of dZ and dgates is given. */
+tdx_status tdx_moe_combine_bwd(const void* dout, const void* Z, const int32_t* dest, const float* gates,
+                               void* dZ, float* dgates, int R, int T, int H, int topk, tdx_dtype dtype,
+                               const tdx_combine_opts* opts, void* stream);
 
 /* Synchronise `stream`, then read the workspace's device status word into *out (TDX_OK, or the
  * first device-side error since tdx_workspace_init). If detail is not NULL it receives 8 words:
