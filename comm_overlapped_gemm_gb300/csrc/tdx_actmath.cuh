@@ -55,35 +55,27 @@ __device__ __forceinline__ float times_sigmoid(float a, float b) {
 constexpr float kGelu2 = 1.59576912f, kGeluCube = 0.044715f, kHalfRoot = 0.70710678f, kInvRoot2Pi = 0.39894228f;
 __device__ __forceinline__ float gelu_arg(float a) { return kGelu2 * a * fmaf(kGeluCube * a, a, 1.0f); }
 
-// One activation over n values (the gate's alone for TDX_ACT_SWIGLU). Exact forms for fp32 results; the
-// approximate ones err by 2^-22 * (4 + |exponent|) relative, which a rounding to 8 bits hides.
-template <int N, bool kExact>
-__device__ __forceinline__ void act_forward(tdx_activation act, float (&v)[N]) {
-  switch (act) {
-    case TDX_ACT_RELU:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];   // a NaN stays one
-      break;
-    case TDX_ACT_GELU:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * erfcf(-kHalfRoot * v[i]);
-      break;
-    case TDX_ACT_GELU_TANH:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = times_sigmoid<kExact>(v[i], gelu_arg(v[i]));
-      break;
-    case TDX_ACT_SILU:
-    case TDX_ACT_SWIGLU:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = times_sigmoid<kExact>(v[i], v[i]);
-      break;
-    default: break;
-  }
+// One value, exact forms and GELU with the error function: called, not unrolled. (The epilogues run these once per
+// column; unrolled for every activation they filled the instruction cache.)
+static __device__ __noinline__ float act_exact(tdx_activation act, float v) {
+  if (act == TDX_ACT_GELU) return 0.5f * v * erfcf(-kHalfRoot * v);
+  return times_sigmoid<true>(v, act == TDX_ACT_GELU_TANH ? gelu_arg(v) : v);
 }
+
+// One activation over N values (the gate's alone for TDX_ACT_SWIGLU). Exact forms for fp32 results; the
+// approximate ones err by 2^-22 * (4 + |exponent|) relative, which a rounding to 8 bits hides.
 template <int N>
 __device__ __forceinline__ void act_forward(tdx_activation act, bool exact, float (&v)[N]) {
-  if (exact) act_forward<N, true>(act, v);
-  else act_forward<N, false>(act, v);
+  if (act == TDX_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];   // a NaN stays one
+  } else if (exact || act == TDX_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_exact(act, v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = times_sigmoid<false>(v[i], act == TDX_ACT_GELU_TANH ? gelu_arg(v[i]) : v[i]);
+  }
 }
 
 }  // namespace tdx

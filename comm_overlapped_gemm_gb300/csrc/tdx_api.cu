@@ -272,12 +272,15 @@ EncodeTiledFn get_encode() {
 }  // namespace
 
 namespace tdx {
-bool encode_map(CUtensorMap* m, const void* base, bool fp8, int rank, const uint64_t* dims, const uint64_t* strides,
+bool encode_map(CUtensorMap* m, const void* base, int elt, int rank, const uint64_t* dims, const uint64_t* strides,
                 const uint32_t* box) {
   EncodeTiledFn enc = get_encode();
   if (enc == nullptr) return false;
   const cuuint32_t ones[3] = {1, 1, 1};
-  return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+  const CUtensorMapDataType type = elt == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  return enc(m, type, static_cast<cuuint32_t>(rank),
              const_cast<void*>(base), reinterpret_cast<const cuuint64_t*>(dims),
              reinterpret_cast<const cuuint64_t*>(strides), box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

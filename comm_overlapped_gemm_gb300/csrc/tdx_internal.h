@@ -151,9 +151,9 @@ cudaError_t launch_fused_fp8(int op, int block_n, int pm, const KParams& p, int 
 int fused_max_grid_bf16(int op, int pm, int sms, int block_n);
 int fused_max_grid_fp8(int op, int pm, int sms, int block_n);
 cudaError_t launch_fill_zero(void* dst, size_t bytes, cudaStream_t stream);
-// Tiled tensor map over bf16 or e4m3 elements, 2 or 3 dimensions (innermost first), 128-byte swizzle;
+// Tiled tensor map over elements of 1 (bytes), 2 (bf16) or 4 bytes (fp32), 2 or 3 dimensions (innermost first), 128-byte swizzle;
 // strides (bytes) of dimensions 1 and up, box rows of 128 bytes.
-bool encode_map(CUtensorMap* m, const void* base, bool fp8, int rank, const uint64_t* dims, const uint64_t* strides,
+bool encode_map(CUtensorMap* m, const void* base, int elt, int rank, const uint64_t* dims, const uint64_t* strides,
                 const uint32_t* box);
 
 // MoE: the fused dispatch + grouped GEMM kernel and the fused grouped GEMM + combine kernel

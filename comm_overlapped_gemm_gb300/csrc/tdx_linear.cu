@@ -37,7 +37,7 @@ bool map_of(CUtensorMap* m, const Operand& o, bool fp8, int rank, int box_rows) 
                             static_cast<uint64_t>(o.E)};
   const uint64_t strides[2] = {o.ld * elt, (o.E > 1 ? o.step : o.ld) * elt};
   const uint32_t box[3] = {static_cast<uint32_t>(128 / elt), static_cast<uint32_t>(box_rows), 1};
-  return encode_map(m, o.p, fp8, rank, dims, strides, box);
+  return encode_map(m, o.p, static_cast<int>(elt), rank, dims, strides, box);
 }
 
 // How a product of about `tiles256` / `tiles1` pair and single tiles with `nkb` K slices runs
@@ -110,6 +110,21 @@ tdx_status run(Form form, Group group, bool fp8, LinParams& p, const Operand& a,
   p.keep_b = group == kRows ? (rows > std::min(E, rows) * tm ? 1 : 0) : (p.tiles_m > 1 ? 1 : 0);
   const int b_rows = form == NT ? 128 : bk;
   if (!map_of(&p.tm_a, a, fp8, 2, form == TN ? bk : kBM) || !map_of(&p.tm_b, b, fp8, 3, b_rows)) return TDX_ERR_CUDA;
+  if (form != TN && !map_of(&p.tm_few, a, fp8, 2, kFewRows)) return TDX_ERR_CUDA;
+  const int64_t out = static_cast<int64_t>(bytes_of(p.out_type));
+  p.wide = aligned(p.out, 32) && p.ld_out * out % 32 == 0 && p.out_step * out % 32 == 0;
+  p.wide_z = aligned(p.z, 32) && p.ld_z % 16 == 0 && (!p.gated || p.cols % 16 == 0);
+  // a warp's columns of a tile (half of them) are whole 128-byte rows; strides as tensor maps take them
+  p.tma_out = p.out_type != TDX_FP8_E4M3 && !p.accumulate && width / 2 * out >= 128 && p.ld_out * out < kMostBytes &&
+              p.out_step * out < kMostBytes;
+  if (p.tma_out) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(p.cols), static_cast<uint64_t>(p.M),
+                              static_cast<uint64_t>(group == kSums ? p.E : 1)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(p.ld_out * out),
+                                 static_cast<uint64_t>((group == kSums && E > 1 ? p.out_step : p.ld_out) * out)};
+    const uint32_t box[3] = {static_cast<uint32_t>(128 / out), 32, 1};
+    if (!encode_map(&p.tm_c, p.out, p.out_type == TDX_FP32 ? 4 : 2, 3, dims, strides, box)) return TDX_ERR_CUDA;
+  }
   const int want = static_cast<int>(most);
   if (fp8) return launch_linear_e4m3(group, shape.pair, p, want, st);
   return form == NN   ? launch_linear_nn(group, shape.pair, p, want, st)

@@ -26,6 +26,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "tdx_actmath.cuh"
 #include "tdx_linear.h"
@@ -34,6 +35,8 @@
 namespace tdx {
 
 constexpr int kLinStages = 6;
+constexpr int kStoreBytes = 4096;   // an epilogue warp's staging: 32 rows of 128 bytes
+
 
 template <bool FP8, Form FORM, Group GROUP, bool PAIR>
 struct LinCfg {
@@ -52,12 +55,16 @@ struct LinCfg {
   static constexpr int B_BOX_STEP = B_MN ? BOX_BYTES : 128 * 128;
   static constexpr int B_BYTES = N_CTA * 128;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = STAGE_BYTES > 32768 ? 4 : kLinStages;
   static constexpr int TM = PAIR ? 2 * kBM : kBM;      // rows of a tile
   static constexpr int TMEM_COLS = 2 * BN;
-  static constexpr int NUM_BARS = 3 * STAGES + 5;      // full, empty, tail per slot; accumulators; drain
   static constexpr int TABLE = GROUP == kFlat ? 0 : 2 * (kMoeMaxExperts + 1) + 2;   // ints
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + NUM_BARS * 8 + 64 + TABLE * 4;
+  // staging for the output's TMA stores, but for the e4m3 kernel of single CTAs, whose slots are larger
+  static constexpr int STORE = STAGE_BYTES > 32768 ? 0 : kNumEpiWarps * kStoreBytes;
+  static constexpr int OTHER = 1024 + STORE + 64 + TABLE * 4 + (3 * kLinStages + 5) * 8;
+  static constexpr int FIT = (227 * 1024 - OTHER) / STAGE_BYTES;
+  static constexpr int STAGES = FIT < kLinStages ? FIT : kLinStages;
+  static constexpr int NUM_BARS = 3 * STAGES + 5;      // full, empty, tail per slot; accumulators; drain
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + STORE + NUM_BARS * 8 + 64 + TABLE * 4;
   static constexpr int PART_LD = BN + 4;               // row pitch of a partial: 16 bytes past the banks' period
   static constexpr uint32_t IDESC = (1u << 4) | ((FP8 ? 0u : 1u) << 7) | ((FP8 ? 0u : 1u) << 10) |
                                     ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
@@ -207,70 +214,116 @@ __device__ __forceinline__ LinRow lin_row(const LinParams& p, const LinTile& t, 
   return r;
 }
 
-// 8 output columns from `col` of one row: v the accumulators (SWIGLU: of the gate), u those of the other half
-__device__ __forceinline__ void lin_finish(const LinParams& p, const LinRow& r, int col, float (&v)[8], float (&u)[8]) {
-  const bool gated = p.act == TDX_ACT_SWIGLU;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= r.scale;
-  if (gated) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] *= r.scale;
-  }
-  if (p.bias != nullptr) {
-    float b[8];
-    load_vec(p.bias + col, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-    if (gated) {
-      load_vec(p.bias + p.cols + col, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] += b[i];
+// Of the epilogue's steps the forward product (NN) alone has scales of rows, bias, z and activation, the weight
+// gradient (TN) alone the addition to its output; the others' instances do without their code.
+template <Form FORM>
+struct LinSteps {
+  static constexpr bool kForward = FORM == NN, kResidual = FORM != TN, kAccumulate = FORM == TN;
+};
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+// N values in bf16 at o, the first 8 alone unless `both`; 16 go out as one 32-byte store where the address
+// allows it: a sector of L2 is then written once, not half by half
+template <int N>
+__device__ __forceinline__ void store_bf16(bf16* o, const float (&v)[N], bool both, bool wide) {
+  const uint4 a = pack8(v);
+  if (N == 16 && both) {
+    const uint4 b = pack8(v + N - 8);
+    if (wide) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(a.x), "r"(a.y), "r"(a.z),
+                   "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                   : "memory");
+    } else {
+      st_v4(o, a);
+      st_v4(o + 8, b);
     }
+  } else {
+    st_v4(o, a);
   }
-  if (p.z != nullptr) {
-    store_vec(p.z + r.z + col, v);
-    if (gated) store_vec(p.z + r.z + p.cols + col, u);
+}
+// v += N values of bf16 at b
+template <int N>
+__device__ __forceinline__ void add_bf16(float (&v)[N], const bf16* b, bool both) {
+#pragma unroll
+  for (int h = 0; h < N; h += 8) {
+    if (h > 0 && !both) break;
+    float w[8];
+    load_vec(b + h, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[h + i] += w[i];
   }
-  if (p.act != TDX_ACT_NONE) {
-    act_forward(p.act, p.out_type == TDX_FP32, v);
-    if (gated) {
+}
+
+// Columns col .. col + N (8, or 16 of which the last 8 count if `both`) of one row: v the accumulators (SWIGLU: of
+// the gate), u those of the other half. v becomes the values to round; z is stored.
+template <Form FORM, int N>
+__device__ __forceinline__ void lin_values(const LinParams& p, const LinRow& r, int col, bool both, float (&v)[N],
+                                           float (&u)[N]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= u[i];
-    }
-  }
-  if (p.residual != nullptr) {
-    float b[8];
-    load_vec(p.residual + r.res + col, b);
+  for (int i = 0; i < N; ++i) v[i] *= r.scale;
+  if constexpr (LinSteps<FORM>::kForward) {
+    if (p.bias != nullptr) add_bf16(v, p.bias + col, both);
+    if (p.z != nullptr) store_bf16(p.z + r.z + col, v, both, p.wide_z);
+    if (p.act != TDX_ACT_NONE) {
+      act_forward(p.act, p.out_type == TDX_FP32, v);
+      if (p.gated) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-  }
-  if (p.out_type == TDX_BF16) {
-    bf16* o = static_cast<bf16*>(p.out) + r.out + col;
-    if (p.accumulate) {
-      float b[8];
-      load_vec(o, b);
+        for (int i = 0; i < N; ++i) u[i] *= r.scale;
+        if (p.bias != nullptr) add_bf16(u, p.bias + p.cols + col, both);
+        if (p.z != nullptr) store_bf16(p.z + r.z + p.cols + col, u, both, p.wide_z);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += b[i];
-    }
-    store_vec(o, v);
-  } else if (p.out_type == TDX_FP32) {
-    float* o = static_cast<float*>(p.out) + r.out + col;
-    if (p.accumulate) {
-      float b[4], c[4];
-      load_vec(o, b);
-      load_vec(o + 4, c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] += b[i];
-        v[4 + i] += c[i];
+        for (int i = 0; i < N; ++i) v[i] *= u[i];
       }
     }
-    store_vec<8>(o, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= p.inv_out_scale;
-    store_vec(static_cast<e4m3*>(p.out) + r.out + col, v);
   }
+  if constexpr (LinSteps<FORM>::kResidual) {
+    if (p.residual != nullptr) add_bf16(v, p.residual + r.res + col, both);
+  }
+}
+
+// Round them and store them
+template <Form FORM, int N>
+__device__ __forceinline__ void lin_store(const LinParams& p, const LinRow& r, int col, bool both, float (&v)[N]) {
+  if (p.out_type == TDX_BF16) {
+    bf16* o = static_cast<bf16*>(p.out) + r.out + col;
+    if (LinSteps<FORM>::kAccumulate && p.accumulate) add_bf16(v, o, both);
+    store_bf16(o, v, both, p.wide);
+  } else if (p.out_type == TDX_FP32) {
+    float* o = static_cast<float*>(p.out) + r.out + col;
+#pragma unroll
+    for (int h = 0; h < N; h += 4) {
+      if (h >= 8 && !both) break;
+      float4 w = make_float4(v[h], v[h + 1], v[h + 2], v[h + 3]);
+      if (LinSteps<FORM>::kAccumulate && p.accumulate) {
+        const float4 old = *reinterpret_cast<const float4*>(o + h);
+        w = make_float4(w.x + old.x, w.y + old.y, w.z + old.z, w.w + old.w);
+      }
+      *reinterpret_cast<float4*>(o + h) = w;
+    }
+  } else if constexpr (LinSteps<FORM>::kForward) {
+#pragma unroll
+    for (int h = 0; h < N; h += 8) {
+      if (h > 0 && !both) break;
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = v[h + i] * p.inv_out_scale;
+      store_vec(static_cast<e4m3*>(p.out) + r.out + col + h, w);
+    }
+  }
+}
+
+__device__ __forceinline__ void st_shared_v4(uint8_t* row, int unit, int lane, uint4 q) {
+  *reinterpret_cast<uint4*>(row + ((unit ^ (lane & 7)) * 16)) = q;
+}
+
+// TMA store of a staged box (coordinates innermost first), in this thread's bulk group
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
 }
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -291,7 +344,8 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + C::STAGES * C::A_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES);
+  uint8_t* staging = smem + C::STAGES * C::STAGE_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + C::STORE);
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + C::NUM_BARS);   // [0] Tensor Memory base, [1] abort
   int* off = reinterpret_cast<int*>(misc + 16);
   int* cum = off + kMoeMaxExperts + 1;
@@ -319,6 +373,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
     fence_mbar_init();
     tma_prefetch_map(&p.tm_a);
     tma_prefetch_map(&p.tm_b);
+    if (p.tma_out) tma_prefetch_map(&p.tm_c);
   }
   if (warp == kMmaWarp) {
     if constexpr (PAIR) {
@@ -351,16 +406,24 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
         const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, it, crank);
         // the tile's first column of each half of B (SWIGLU: gate columns, then the other half's)
         const int n0 = t.nt * (p.gated ? BN / 2 : BN);
-        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        // A tile of few rows loads only them, in boxes of kFewRows: the rows that a box fills with zeros past
+        // the end of A cost as much as real ones (1 x 8192 x 8192: streaming B alone 23 us, with boxes of 8 or 16
+        // rows of A 23, of 64 rows 31, of 128 rows 33). The accumulators of the rows behind are never read.
+        const int few = !PAIR && !C::A_MN && t.mend - t.m0 <= 4 * kFewRows ? (t.mend - t.m0 + kFewRows - 1) / kFewRows : 0;
+        const uint32_t bytes = few > 0 ? few * kFewRows * 128 + C::B_BYTES : C::STAGE_BYTES;
+        // One slice; a tail slice is counted on this CTA's own tail barrier. Two instances of the code: with the
+        // choice made per load in one loop, the loop and not the tensor cores set the pace (one run of 2048 rows, 2048 x
+        // 57344: 379 us against 272).
+        auto issue = [&](int kb, auto is_tail) {
+          constexpr bool kTail = decltype(is_tail)::value;
           if (!lin_wait(p.status, empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
             stop = true;
-            break;
+            return;
           }
-          const bool tail = GROUP == kSums && (kb + 1) * C::BK > t.klen;
-          const uint32_t own = (tail ? tail0 : full0) + 8 * stage;
+          const uint32_t own = (kTail ? tail0 : full0) + 8 * stage;
           uint32_t bar = own;
-          if (!PAIR || tail) {
-            mbar_arrive_expect_tx(own, C::STAGE_BYTES);
+          if constexpr (!PAIR || kTail) {
+            mbar_arrive_expect_tx(own, bytes);
           } else {
             bar = mapa_shared(own, 0);   // both CTAs' slices count on the leader's barrier
             if (leader) mbar_arrive_expect_tx(own, 2 * C::STAGE_BYTES);
@@ -370,26 +433,38 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
           if constexpr (C::A_MN) {
 #pragma unroll
             for (int j = 0; j < C::A_BOXES; ++j) {
-              if (PAIR && !tail) tma_load_2d_pair_hint(a + j * C::BOX_BYTES, &p.tm_a, bar, t.m0 + j * C::BOX_N, k, keep_a);
-              else tma_load_2d_hint(a + j * C::BOX_BYTES, &p.tm_a, bar, t.m0 + j * C::BOX_N, k, keep_a);
+              if constexpr (PAIR && !kTail)
+                tma_load_2d_pair_hint(a + j * C::BOX_BYTES, &p.tm_a, bar, t.m0 + j * C::BOX_N, k, keep_a);
+              else
+                tma_load_2d_hint(a + j * C::BOX_BYTES, &p.tm_a, bar, t.m0 + j * C::BOX_N, k, keep_a);
             }
+          } else if constexpr (PAIR) {
+            tma_load_2d_pair_hint(a, &p.tm_a, bar, k, t.m0, keep_a);
+          } else if (few == 0) {
+            tma_load_2d_hint(a, &p.tm_a, bar, k, t.m0, keep_a);
           } else {
-            if (PAIR) tma_load_2d_pair_hint(a, &p.tm_a, bar, k, t.m0, keep_a);
-            else tma_load_2d_hint(a, &p.tm_a, bar, k, t.m0, keep_a);
+            for (int j = 0; j < few; ++j)
+              tma_load_2d_hint(a + j * kFewRows * 128, &p.tm_few, bar, k, t.m0 + j * kFewRows, keep_a);
           }
 #pragma unroll
           for (int j = 0; j < C::B_BOXES; ++j) {
             const uint32_t dst = b + j * C::B_BOX_STEP;
-            const int c = PAIR ? crank * C::N_CTA + j * (C::B_MN ? C::BOX_N : 128) : j * (C::B_MN ? C::BOX_N : 128);
-            const int n = p.gated && c >= BN / 2 ? p.cols + n0 + c - BN / 2 : n0 + c;
+            const int c = (PAIR ? crank * C::N_CTA : 0) + j * (C::B_MN ? C::BOX_N : 128);
+            const int n = LinSteps<FORM>::kForward && p.gated && c >= BN / 2 ? p.cols + n0 + c - BN / 2 : n0 + c;
             const int x = C::B_MN ? n : k, y = C::B_MN ? k : n, z = GROUP == kRows ? t.e : 0;
-            if (PAIR && !tail) tma_load_3d_pair_hint(dst, &p.tm_b, bar, x, y, z, keep_b);
+            if constexpr (PAIR && !kTail) tma_load_3d_pair_hint(dst, &p.tm_b, bar, x, y, z, keep_b);
             else tma_load_3d_hint(dst, &p.tm_b, bar, x, y, z, keep_b);
           }
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
+        };
+        const bool tail = GROUP == kSums && t.kb1 > t.kb0 && t.kb1 * C::BK > t.klen;
+        const int whole = tail ? t.kb1 - 1 : t.kb1;
+        for (int kb = t.kb0; kb < whole && !stop; ++kb) issue(kb, std::false_type{});
+        if constexpr (GROUP == kSums) {
+          if (tail && !stop) issue(whole, std::true_type{});
         }
       }
     }
@@ -518,29 +593,58 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
       if (row_ok) lr = lin_row<C, GROUP>(p, t, row, scale);
       const int width = p.gated ? BN / 2 : BN;
       const int n0 = t.nt * width;
+      // rows of 128 bytes go out through shared memory as TMA stores, which drop what lies past the output's
+      // edges; not where the tile's rows end inside this warp's 32 and the next run's follow
+      const int warp_row = t.m0 + quarter * 32;
+      const bool box = C::STORE > 0 && p.tma_out && warp_row + (GROUP == kRows ? 31 : 0) < t.mend;
+      uint8_t* stage_row = staging + (warp - kEpiWarp0) * kStoreBytes + lane * 128;
+      const int last = min((half + 1) * (width / 2), p.cols - n0);
+      const int box_cols = p.out_type == TDX_BF16 ? 64 : 32;
+      // a rolled loop over 16 columns: unrolled over the tile its code came from L2 anew with every tile
 #pragma unroll 1
-      for (int c = half * (width / 2); c < (half + 1) * (width / 2); c += 32) {
-        uint32_t r[32], q[32];
-        if (n0 + c >= p.cols) break;
+      for (int c = half * (width / 2); c < last; c += 16) {
+        uint32_t r[16], q[16];
+        float v[16], u[16];
         __syncwarp();
-        tmem_ld_32x32b_x32(d + c, r);
-        if (p.gated) {
-          tmem_ld_32x32b_x32(d + BN / 2 + c, q);
+        tmem_ld_32x32b_x16(d + c, r);
+        if (LinSteps<FORM>::kForward && p.gated) {
+          tmem_ld_32x32b_x16(d + BN / 2 + c, q);
           tmem_ld_wait(q);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) u[i] = none ? 0.0f : __uint_as_float(q[i]);
         }
         tmem_ld_wait(r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = none ? 0.0f : __uint_as_float(r[i]);
+        const int col = n0 + c, in_box = c & (box_cols - 1);
+        const bool both = c + 8 < last;
+        if (box && in_box == 0) {
+          if (lane == 0) bulk_wait_read_all();   // the staging's last store has been read
+          __syncwarp();
+        }
         if (row_ok) {
+          lin_values<FORM>(p, lr, col, both, v, u);
+          if (!box) {
+            lin_store<FORM>(p, lr, col, both, v);
+          } else if (p.out_type == TDX_BF16) {
+            // 16-byte units of a row, permuted as the 128-byte swizzle has them
+            st_shared_v4(stage_row, in_box / 8, lane, pack8(v));
+            st_shared_v4(stage_row, in_box / 8 + 1, lane, pack8(v + 8));
+          } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            if (n0 + c + i < p.cols) {
-              float v[8], u[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                v[k] = none ? 0.0f : __uint_as_float(r[i + k]);
-                u[k] = none || !p.gated ? 0.0f : __uint_as_float(q[i + k]);
-              }
-              lin_finish(p, lr, n0 + c + i, v, u);
-            }
+            for (int k = 0; k < 4; ++k)
+              st_shared_v4(stage_row, in_box / 4 + k, lane,
+                           make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
+                                      __float_as_uint(v[4 * k + 3])));
+          }
+        }
+        if (box && (in_box + 16 == box_cols || c + 16 >= last)) {
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&p.tm_c, smem_u32(staging + (warp - kEpiWarp0) * kStoreBytes), col - in_box, warp_row,
+                         GROUP == kSums ? t.e : 0);
+            bulk_commit();
           }
         }
       }
@@ -551,6 +655,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
         else mbar_arrive(tempty0 + 8 * acc);
       }
     }
+    if (lane == 0) bulk_wait_read_all();   // the stores read this CTA's shared memory
   }
 
   griddep_launch_dependents();
@@ -575,13 +680,15 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
           const float4 a = ld_cluster_f4(at), b = ld_cluster_f4(at + 16);
           v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
           v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
-          if (p.gated) {
+          if (LinSteps<FORM>::kForward && p.gated) {
             const float4 x = ld_cluster_f4(at + BN / 2 * 4), y = ld_cluster_f4(at + BN / 2 * 4 + 16);
             u[0] += x.x; u[1] += x.y; u[2] += x.z; u[3] += x.w;
             u[4] += y.x; u[5] += y.y; u[6] += y.z; u[7] += y.w;
           }
         }
-        lin_finish(p, lin_row<C, GROUP>(p, t, t.m0 + r, scale), n0 + c, v, u);
+        const LinRow lr = lin_row<C, GROUP>(p, t, t.m0 + r, scale);
+        lin_values<FORM>(p, lr, n0 + c, false, v, u);
+        lin_store<FORM>(p, lr, n0 + c, false, v);
       }
     }
   }

@@ -11,6 +11,7 @@ namespace tdx {
 enum Form { NN, NT, TN };                 // see tdx_linear.cuh
 enum Group { kFlat, kRows, kSums };
 constexpr uint64_t kLinTimeoutNs = 4000000000ull;
+constexpr int kFewRows = 16;   // rows of the small boxes of A
 
 // Tile columns: pairs 256. Single CTAs 128, and 256 for e4m3, whose 128-column boxes would not split
 // a 128-column tile into gate and up halves.
@@ -18,7 +19,9 @@ constexpr int lin_block_n(bool fp8, bool pair) { return pair || fp8 ? 256 : 128;
 constexpr int lin_tile_rows(bool pair) { return pair ? 2 * kBM : kBM; }
 
 struct LinParams {
-  CUtensorMap tm_a, tm_b;
+  CUtensorMap tm_a, tm_b;   // operands
+  CUtensorMap tm_few;       // A in boxes of few rows
+  CUtensorMap tm_c;         // output in boxes of 32 rows of 128 bytes
   int M, N, K;              // output rows, accumulator columns, summed length (kRows: M, kSums: K over all runs)
   int cols;                 // output columns: N, or N / 2 for SWIGLU
   int E;
@@ -39,6 +42,8 @@ struct LinParams {
   void* out;
   int64_t ld_out, ld_res, ld_z;
   int64_t out_step;         // kSums: elements between two experts' outputs
+  int tma_out;              // output through tm_c (bf16 or fp32, not added to, whole 128-byte columns per warp)
+  int wide, wide_z;         // output and z in 32-byte stores: 32-byte aligned rows
   uint32_t* status;
 };
 
