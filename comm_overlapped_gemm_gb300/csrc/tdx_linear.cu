@@ -117,6 +117,7 @@ tdx_status run(Form form, Group group, bool fp8, LinParams& p, const Operand& a,
   // a warp's columns of a tile (half of them) are whole 128-byte rows; strides as tensor maps take them
   p.tma_out = p.out_type != TDX_FP8_E4M3 && !p.accumulate && width / 2 * out >= 128 && p.ld_out * out < kMostBytes &&
               p.out_step * out < kMostBytes;
+  p.plain = p.bias == nullptr && p.z == nullptr && p.act == TDX_ACT_NONE;
   if (p.tma_out) {
     const uint64_t dims[3] = {static_cast<uint64_t>(p.cols), static_cast<uint64_t>(p.M),
                               static_cast<uint64_t>(group == kSums ? p.E : 1)};
@@ -218,8 +219,10 @@ tdx_status backward(const void* dz, const void* A, const int32_t* offsets, const
   p.alpha = o.alpha;
   p.inv_out_scale = 1.0f;
   p.status = o.device_status;
+  const bool both = dA != nullptr && dB != nullptr && M > 0;
   if (dA != nullptr && M > 0) {
     LinParams q = p;
+    q.overlap = both ? kOverlapFirst : kOverlapNone;
     q.M = M;
     q.N = q.cols = K;
     q.K = N;
@@ -241,6 +244,7 @@ tdx_status backward(const void* dz, const void* A, const int32_t* offsets, const
     q.out_step = step;
     q.out_type = o.dw_dtype;
     q.accumulate = o.accumulate;
+    q.overlap = both ? kOverlapSecond : kOverlapNone;
     return run(TN, E > 0 ? kSums : kFlat, false, q, {A, M, K, ld_a, 0, 1}, {dz, M, N, ld_z, 0, 1}, st);
   }
   return TDX_OK;

@@ -335,6 +335,76 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+// A warp's columns [begin, last) of a tile that are scaled, rounded and stored, perhaps with a residual added, and
+// nothing else, in boxes of 128-byte rows. 32 columns at a time (the accumulators behind `last` are read, not stored), values in
+// pairs, the next columns' residual on its way. The general loop takes four times the instructions: 8192 x 512 x 8192
+// 68 us with it, 57 with this one.
+template <bool F32, bool RES>
+__device__ __forceinline__ void lin_plain(const LinParams& p, const LinRow& lr, uint32_t d, bool none, bool row_ok, int n0,
+                                          int begin, int last, uint8_t* stage, int warp_row, int z) {
+  const int lane = threadIdx.x & 31;
+  uint8_t* stage_row = stage + lane * 128;
+  const f32x2 scale = pair(lr.scale, lr.scale);
+  uint4 res[4];
+  auto fetch = [&](int c) {
+    const uint4* at = reinterpret_cast<const uint4*>(p.residual + lr.res + n0 + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (row_ok && c + 8 * i < last) res[i] = at[i];
+  };
+  if (RES) fetch(begin);
+#pragma unroll 1
+  for (int c = begin; c < last; c += 32) {
+    uint32_t r[32];
+    f32x2 v[16];
+    __syncwarp();
+    if (none) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) r[i] = 0u;
+    } else {
+      tmem_ld_32x32b_x32(d + c, r);
+      tmem_ld_wait(r);
+    }
+    const int in_box = F32 ? 0 : c & 32;
+    if (in_box == 0) {
+      if (lane == 0) bulk_wait_read_all();   // the staging's last store has been read
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = mul2(pair(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), scale);
+    if (RES) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f32x2 w[4];
+        unpack(res[i], w, bf16{});
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[4 * i + k] = add2(v[4 * i + k], w[k]);
+      }
+      if (c + 32 < last) fetch(c + 32);
+    }
+    // 16-byte units of a row, permuted as the 128-byte swizzle has them
+#pragma unroll
+    for (int i = 0; i < 16; i += F32 ? 2 : 4) {
+      uint4 q;
+      if (F32)
+        q = make_uint4(__float_as_uint(first(v[i])), __float_as_uint(second(v[i])), __float_as_uint(first(v[i + 1])),
+                       __float_as_uint(second(v[i + 1])));
+      else
+        q = make_uint4(pack_bf16(first(v[i]), second(v[i])), pack_bf16(first(v[i + 1]), second(v[i + 1])),
+                       pack_bf16(first(v[i + 2]), second(v[i + 2])), pack_bf16(first(v[i + 3]), second(v[i + 3])));
+      st_shared_v4(stage_row, F32 ? i / 2 : in_box / 8 + i / 4, lane, q);
+    }
+    if (F32 || in_box == 32 || c + 32 >= last) {
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&p.tm_c, smem_u32(stage), n0 + c - in_box, warp_row, z);
+        bulk_commit();
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------------------------------ kernel
 template <bool FP8, Form FORM, Group GROUP, bool PAIR>
 __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid_constant__ LinParams p) {
@@ -385,7 +455,8 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
     }
   }
   tc_fence_before();
-  griddep_wait();
+  if (p.overlap != kOverlapSecond) griddep_wait();
+  if (p.overlap == kOverlapFirst) griddep_launch_dependents();
   if constexpr (GROUP != kFlat) {
     if (warp == kCopyWarp0) lin_table(p.offsets, p.E, GROUP == kRows ? p.M : p.K, C::TM, off, cum);
   }
@@ -559,11 +630,14 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
       const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, it, crank);
       const int acc = local & 1;
       const bool none = t.kb0 == t.kb1;   // nothing was multiplied: zeros
+      const int in_tile = quarter * 32 + lane, row = t.m0 + in_tile;
+      const bool row_ok = row < t.mend;
+      const int width = LinSteps<FORM>::kForward && p.gated ? BN / 2 : BN;
+      const int n0 = t.nt * width, first = half * (width / 2), last = min(first + width / 2, p.cols - n0);
       const bool ok = lin_wait(p.status, tfull0 + 8 * acc, (local >> 1) & 1, abort_flag);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
       const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN) + lanes;
-      const int in_tile = quarter * 32 + lane;
       if (!PAIR && S > 1) {
         // this CTA's partial, into the ring (its slots are free: every MMA of the tile has completed)
         float* part = reinterpret_cast<float*>(smem);
@@ -585,24 +659,28 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
         }
         break;   // one tile per cluster
       }
-      const int row = t.m0 + in_tile;
-      const bool row_ok = row < t.mend;
       float scale = p.alpha;
       if (GROUP == kRows && p.expert_scale != nullptr) scale *= p.expert_scale[t.e];
       LinRow lr = {};
       if (row_ok) lr = lin_row<C, GROUP>(p, t, row, scale);
-      const int width = p.gated ? BN / 2 : BN;
-      const int n0 = t.nt * width;
       // rows of 128 bytes go out through shared memory as TMA stores, which drop what lies past the output's
       // edges; not where the tile's rows end inside this warp's 32 and the next run's follow
       const int warp_row = t.m0 + quarter * 32;
       const bool box = C::STORE > 0 && p.tma_out && warp_row + (GROUP == kRows ? 31 : 0) < t.mend;
       uint8_t* stage_row = staging + (warp - kEpiWarp0) * kStoreBytes + lane * 128;
-      const int last = min((half + 1) * (width / 2), p.cols - n0);
-      const int box_cols = p.out_type == TDX_BF16 ? 64 : 32;
+      const int box_cols = p.out_type == TDX_BF16 ? 64 : 32, z = GROUP == kSums ? t.e : 0;
+      uint8_t* stage = staging + (warp - kEpiWarp0) * kStoreBytes;
+      if (box && p.plain && p.out_type == TDX_FP32 && !(LinSteps<FORM>::kResidual && p.residual != nullptr)) {
+        lin_plain<true, false>(p, lr, d, none, row_ok, n0, first, last, stage, warp_row, z);
+      } else if (box && p.plain && p.out_type == TDX_BF16) {
+        if (LinSteps<FORM>::kResidual && p.residual != nullptr)
+          lin_plain<false, true>(p, lr, d, none, row_ok, n0, first, last, stage, warp_row, z);
+        else
+          lin_plain<false, false>(p, lr, d, none, row_ok, n0, first, last, stage, warp_row, z);
+      } else
       // a rolled loop over 16 columns: unrolled over the tile its code came from L2 anew with every tile
 #pragma unroll 1
-      for (int c = half * (width / 2); c < last; c += 16) {
+      for (int c = first; c < last; c += 16) {
         uint32_t r[16], q[16];
         float v[16], u[16];
         __syncwarp();
@@ -642,8 +720,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(&p.tm_c, smem_u32(staging + (warp - kEpiWarp0) * kStoreBytes), col - in_box, warp_row,
-                         GROUP == kSums ? t.e : 0);
+            tma_store_3d(&p.tm_c, smem_u32(stage), col - in_box, warp_row, z);
             bulk_commit();
           }
         }
@@ -700,6 +777,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
   tc_fence_before();
   if (S > 1) cluster_sync_all();   // no CTA leaves while its peer may read from it, load into it or arrive on it
   else __syncthreads();
+  if (p.overlap == kOverlapSecond) griddep_wait();   // see LinParams
   if (warp == kMmaWarp) {
     tc_fence_after();
     if constexpr (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);

@@ -18,6 +18,12 @@ constexpr int kFewRows = 16;   // rows of the small boxes of A
 constexpr int lin_block_n(bool fp8, bool pair) { return pair || fp8 ? 256 : 128; }
 constexpr int lin_tile_rows(bool pair) { return pair ? 2 * kBM : kBM; }
 
+// Two products of one call that read nothing of each other's: the first lets the second be launched as soon as it has
+// itself waited for the stream's earlier work, so the second, which then need not wait for anything, takes the SMs
+// that the first leaves idle; before it ends it waits for the first, so that what follows in the stream
+// waits for both.
+enum Overlap { kOverlapNone, kOverlapFirst, kOverlapSecond };
+
 struct LinParams {
   CUtensorMap tm_a, tm_b;   // operands
   CUtensorMap tm_few;       // A in boxes of few rows
@@ -44,6 +50,8 @@ struct LinParams {
   int64_t out_step;         // kSums: elements between two experts' outputs
   int tma_out;              // output through tm_c (bf16 or fp32, not added to, whole 128-byte columns per warp)
   int wide, wide_z;         // output and z in 32-byte stores: 32-byte aligned rows
+  int plain;                // no bias, z nor activation: the short epilogue where tma_out is set
+  int overlap;
   uint32_t* status;
 };
 
