@@ -22,6 +22,7 @@ LIB = os.path.join(LIBDIR, "libtdx.so")
 SOURCES = ["tdx_api.cu", "tdx_kernel_bf16.cu", "tdx_kernel_fp8.cu", "tdx_moe.cu",
            "tdx_norm.cu", "tdx_route.cu", "tdx_act.cu",
            "tdx_linear.cu", "tdx_linear_nn.cu", "tdx_linear_nt.cu", "tdx_linear_tn.cu", "tdx_linear_e4m3.cu",
+           "tdx_linear_nn_long.cu", "tdx_linear_nt_long.cu", "tdx_linear_tn_long.cu", "tdx_linear_e4m3_long.cu",
            "tdx_linear_act.cu", "tdx_combine.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",

@@ -126,11 +126,13 @@ tdx_status run(Form form, Group group, bool fp8, LinParams& p, const Operand& a,
     const uint32_t box[3] = {static_cast<uint32_t>(128 / out), 32, 1};
     if (!encode_map(&p.tm_c, p.out, p.out_type == TDX_FP32 ? 4 : 2, 3, dims, strides, box)) return TDX_ERR_CUDA;
   }
-  const int want = static_cast<int>(most);
-  if (fp8) return launch_linear_e4m3(group, shape.pair, p, want, st);
-  return form == NN   ? launch_linear_nn(group, shape.pair, p, want, st)
-         : form == NT ? launch_linear_nt(group, shape.pair, p, want, st)
-                      : launch_linear_tn(group, shape.pair, p, want, st);
+  // index: NN, NT, TN, NN of e4m3
+  static LinLaunch* const launch[2][4] = {
+      {launch_linear_nn, launch_linear_nt, launch_linear_tn, launch_linear_e4m3},
+      {launch_linear_nn_long, launch_linear_nt_long, launch_linear_tn_long, launch_linear_e4m3_long}};
+  // more slices in a tile than one segment (kSums: a run may have all rows)
+  const bool longer = p.out_type == TDX_FP32 && (p.K + bk - 1) / bk > kLinSegment;
+  return launch[longer][fp8 ? 3 : form](group, shape.pair, p, static_cast<int>(most), st);
 }
 
 bool act_known(tdx_activation a) { return a >= TDX_ACT_NONE && a <= TDX_ACT_SWIGLU; }

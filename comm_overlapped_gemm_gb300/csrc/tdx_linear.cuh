@@ -406,7 +406,7 @@ __device__ __forceinline__ void lin_plain(const LinParams& p, const LinRow& lr, 
 }
 
 // ------------------------------------------------------------------------------------------ kernel
-template <bool FP8, Form FORM, Group GROUP, bool PAIR>
+template <bool FP8, Form FORM, Group GROUP, bool PAIR, bool LONG>
 __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid_constant__ LinParams p) {
   using C = LinCfg<FP8, FORM, GROUP, PAIR>;
   constexpr int BN = C::BN;
@@ -546,10 +546,10 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
       bool stop = false;
       for (int it = cid; it < items && !stop; it += ncl, ++local) {
         const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, it, crank);
-        const int acc = local & 1;
+        int acc = local & 1;
         if (!lin_wait(p.status, tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, abort_flag)) break;
         tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
+        uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
           if (!lin_wait(p.status, full0 + 8 * stage, phase, abort_flag)) {
             stop = true;
@@ -557,13 +557,27 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
           }
           tc_fence_after();
           const uint32_t a = smem_u32(sA + stage * C::A_BYTES), b = smem_u32(sB + stage * C::B_BYTES);
+          const int in_segment = LONG ? (kb - t.kb0) % kLinSegment : kb - t.kb0;
+          if (LONG && in_segment == 0 && kb > t.kb0) {
+            // the epilogue takes what is summed so far; on with the other accumulator
+            if constexpr (PAIR) tc_commit_pair_multicast(tfull0 + 8 * acc, static_cast<uint16_t>(0x3));
+            else tc_commit(tfull0 + 8 * acc);
+            ++local;
+            acc = local & 1;
+            if (!lin_wait(p.status, tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, abort_flag)) {
+              stop = true;
+              break;
+            }
+            tc_fence_after();
+            d = tmem_base + static_cast<uint32_t>(acc * BN);
+          }
 #pragma unroll
           for (int k = 0; k < C::BK / C::UMMA_K; ++k) {
             const uint64_t ad = C::A_MN ? smem_desc(a + k * C::UMMA_K * 128, C::BOX_BYTES, 1024, 2u)
                                         : smem_desc(a + k * 32, 16, 1024, 2u);
             const uint64_t bd = C::B_MN ? smem_desc(b + k * C::UMMA_K * 128, C::BOX_BYTES, 1024, 2u)
                                         : smem_desc(b + k * 32, 16, 1024, 2u);
-            const uint32_t accum = kb > t.kb0 || k > 0 ? 1u : 0u;
+            const uint32_t accum = in_segment > 0 || k > 0 ? 1u : 0u;
             if constexpr (PAIR) {
               if constexpr (FP8) umma_f8_pair(d, ad, bd, C::IDESC, accum);
               else umma_bf16_pair(d, ad, bd, C::IDESC, accum);
@@ -628,14 +642,64 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
     int local = 0;
     for (int it = cid; it < items; it += ncl, ++local) {
       const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, it, crank);
-      const int acc = local & 1;
       const bool none = t.kb0 == t.kb1;   // nothing was multiplied: zeros
       const int in_tile = quarter * 32 + lane, row = t.m0 + in_tile;
       const bool row_ok = row < t.mend;
       const int width = LinSteps<FORM>::kForward && p.gated ? BN / 2 : BN;
       const int n0 = t.nt * width, first = half * (width / 2), last = min(first + width / 2, p.cols - n0);
-      const bool ok = lin_wait(p.status, tfull0 + 8 * acc, (local >> 1) & 1, abort_flag);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      bool ok = true;
+      auto release = [&](int acc) {   // the accumulator may be overwritten
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) mbar_arrive_cluster(mapa_shared(tempty0 + 8 * acc, 0));
+          else mbar_arrive(tempty0 + 8 * acc);
+        }
+      };
+      if constexpr (LONG) {
+        // The tensor cores truncate every addition to an accumulator, always toward zero: 9e-10 relative for each
+        // K, 1e-6 at 1024 and 9e-6 at 65536 against 4e-7 for sums rounded to nearest. A result that stays fp32 takes
+        // the sum of segments of kLinSegment slices, added here in fp32; the last one's accumulator gets the total.
+        const int segments = (t.kb1 - t.kb0 + kLinSegment - 1) / kLinSegment;
+        if (segments > 1) {
+          float sum[BN / 2];
+          const int base = p.gated ? half * (BN / 4) : half * (BN / 2), skip = p.gated ? BN / 4 : 0;
+#pragma unroll 1
+          for (int g = 0; g < segments && ok; ++g, local += g < segments) {
+            ok = __all_sync(0xFFFFFFFFu, lin_wait(p.status, tfull0 + 8 * (local & 1), (local >> 1) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t at = tmem_base + static_cast<uint32_t>((local & 1) * BN) + lanes + base;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < BN / 2; i += 16) {
+              uint32_t r[16];
+              tmem_ld_32x32b_x16(at + i + (i >= BN / 4 ? skip : 0), r);
+              tmem_ld_wait(r);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) sum[i + k] = g == 0 ? __uint_as_float(r[k]) : sum[i + k] + __uint_as_float(r[k]);
+            }
+            if (g + 1 < segments) {
+              release(local & 1);
+            } else {
+#pragma unroll
+              for (int i = 0; i < BN / 2; i += 16) {
+                uint32_t r[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(sum[i + k]);
+                tmem_st_32x32b_x16(at + i + (i >= BN / 4 ? skip : 0), r);
+              }
+              tmem_st_wait();
+            }
+          }
+        } else {
+          ok = __all_sync(0xFFFFFFFFu, lin_wait(p.status, tfull0 + 8 * (local & 1), (local >> 1) & 1, abort_flag));
+        }
+      } else {
+        ok = __all_sync(0xFFFFFFFFu, lin_wait(p.status, tfull0 + 8 * (local & 1), (local >> 1) & 1, abort_flag));
+      }
+      if (!ok) break;
+      const int acc = local & 1;
       tc_fence_after();
       const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN) + lanes;
       if (!PAIR && S > 1) {
@@ -725,12 +789,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (PAIR) mbar_arrive_cluster(mapa_shared(tempty0 + 8 * acc, 0));
-        else mbar_arrive(tempty0 + 8 * acc);
-      }
+      release(acc);
     }
     if (lane == 0) bulk_wait_read_all();   // the stores read this CTA's shared memory
   }
@@ -786,10 +845,10 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
 }
 
 // -------------------------------------------------------------------------------------------- host
-template <bool FP8, Form FORM, Group GROUP, bool PAIR>
+template <bool FP8, Form FORM, Group GROUP, bool PAIR, bool LONG>
 tdx_status launch_linear_t(const LinParams& p, int want, cudaStream_t stream) {
   using C = LinCfg<FP8, FORM, GROUP, PAIR>;
-  auto* kernel = tdx_linear_kernel<FP8, FORM, GROUP, PAIR>;
+  auto* kernel = tdx_linear_kernel<FP8, FORM, GROUP, PAIR, LONG>;
   // per device: raised shared-memory limit and, for pairs, the clusters that are resident together
   static std::atomic<int> ready[64];
   int dev = 0;
@@ -830,10 +889,10 @@ tdx_status launch_linear_t(const LinParams& p, int want, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? TDX_OK : TDX_ERR_CUDA;
 }
 
-template <bool FP8, Form FORM, Group GROUP>
+template <bool FP8, Form FORM, Group GROUP, bool LONG>
 tdx_status launch_linear_g(const LinParams& p, bool pair, int want, cudaStream_t stream) {
-  return pair ? launch_linear_t<FP8, FORM, GROUP, true>(p, want, stream)
-              : launch_linear_t<FP8, FORM, GROUP, false>(p, want, stream);
+  return pair ? launch_linear_t<FP8, FORM, GROUP, true, LONG>(p, want, stream)
+              : launch_linear_t<FP8, FORM, GROUP, false, LONG>(p, want, stream);
 }
 
 }  // namespace tdx

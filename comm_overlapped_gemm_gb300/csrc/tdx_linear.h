@@ -11,6 +11,7 @@ namespace tdx {
 enum Form { NN, NT, TN };                 // see tdx_linear.cuh
 enum Group { kFlat, kRows, kSums };
 constexpr uint64_t kLinTimeoutNs = 4000000000ull;
+constexpr int kLinSegment = 16;   // K slices summed on the tensor cores alone, for fp32 results
 constexpr int kFewRows = 16;   // rows of the small boxes of A
 
 // Tile columns: pairs 256. Single CTAs 128, and 256 for e4m3, whose 128-column boxes would not split
@@ -55,9 +56,10 @@ struct LinParams {
   uint32_t* status;
 };
 
-tdx_status launch_linear_nn(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream);
-tdx_status launch_linear_nt(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream);
-tdx_status launch_linear_tn(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream);
-tdx_status launch_linear_e4m3(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream);
+// Instances by operand type, form and group; each form's in a file of its own, those that sum segments in fp32
+// (for fp32 results) in another. `want`: clusters of work.
+using LinLaunch = tdx_status(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream);
+LinLaunch launch_linear_nn, launch_linear_nt, launch_linear_tn, launch_linear_e4m3;
+LinLaunch launch_linear_nn_long, launch_linear_nt_long, launch_linear_tn_long, launch_linear_e4m3_long;
 
 }  // namespace tdx

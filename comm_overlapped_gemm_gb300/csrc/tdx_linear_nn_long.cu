@@ -1,0 +1,11 @@
+// bf16 instances of the product kernel, form NN, sums of segments in fp32.
+#include "tdx_linear.cuh"
+
+namespace tdx {
+
+tdx_status launch_linear_nn_long(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream) {
+  return g == kFlat ? launch_linear_g<false, NN, kFlat, true>(p, pair, want, stream)
+                    : launch_linear_g<false, NN, kRows, true>(p, pair, want, stream);
+}
+
+}  // namespace tdx

@@ -388,3 +388,40 @@ def test_grouped_offsets_out_of_order():
     o = tdx.make_linear_opts(dw_dtype=tdx.TDX_FP32)
     tdx.check(tdx.tdx_grouped_gemm_bwd(dY, X, off, None, None, dB, R, K, N, 5, tdx.TDX_BF16, o))
     same(dB, P.grouped_bwd(f64(dY), f64(X), sane, f64(B))[1][0], F32)
+
+
+# -------------------------------------------------------------------------------- long fp32 sums
+@pytest.mark.parametrize("M,N", [(8, 128), (100, 272), (2048, 2304)])
+def test_fp32_results_of_long_sums(M, N):
+    """The tensor cores truncate each of a sum's additions, which for terms of one sign drifts with K. fp32 results
+    add segments of 16 slices (1024 of K in bf16: 64 additions within 2^-22 each, 80 with the margin above) in
+    fp32, K / 1024 additions within 2^-24 each: whatever K, the error stays below that of the segments' own."""
+    g = gen(M)
+    K = 32768
+    A = (torch.rand(M, K, generator=g) + 0.5).to(BF).cuda()
+    B = (torch.rand(K, N, generator=g) + 0.5).to(BF).cuda()
+    lim = 80 * 2.0 ** -22 + (K / 1024 + 8) * 2.0 ** -24
+    want = A.double() @ B.double()
+    C, _ = run_linear(A, B, out=F32)
+    assert float(((C.double() - want) / want).abs().max()) <= lim
+    off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    C, _ = run_linear(A, B[None], out=F32, offsets=off)
+    assert float(((C.double() - want) / want).abs().max()) <= lim
+    # the weight gradient over K rows, plain and grouped, and the input gradient over K columns
+    X, off = A.t().contiguous(), torch.tensor([0, K - 5, K], dtype=torch.int32, device="cuda")
+    o = tdx.make_linear_opts(dw_dtype=tdx.TDX_FP32, out_dtype=tdx.TDX_FP32)
+    if M % 8 == 0:
+        dB, dBg = torch.empty(M, N, device="cuda"), torch.empty(2, M, N, device="cuda")
+        tdx.check(tdx.tdx_linear_bwd(B, X, None, None, None, dB, K, M, N, tdx.TDX_BF16, o))
+        tdx.check(tdx.tdx_grouped_gemm_bwd(B, X, off, None, None, dBg, K, M, N, 2, tdx.TDX_BF16, o))
+        assert float(((dB.double() - want) / want).abs().max()) <= lim
+        assert float(((dBg.double().sum(0) - want) / want).abs().max()) <= lim
+    dA = torch.empty(M, N, device="cuda")
+    tdx.check(tdx.tdx_linear_bwd(A, None, B.t().contiguous(), None, dA, None, M, N, K, tdx.TDX_BF16, o))
+    assert float(((dA.double() - want) / want).abs().max()) <= lim
+    # act and gate over summed segments
+    C, z = run_linear(A, B * 2.0 ** -15, out=F32, act="swiglu", z=True)
+    w = (want * 2.0 ** -15).cpu().numpy()
+    close(z, w, lim * np.abs(w), BF)
+    y = P.act("swiglu", w)
+    close(C, y, (2.2 * lim + 2.0 ** -21 * (4 + np.abs(w[:, :N // 2]))) * np.abs(y), F32)
