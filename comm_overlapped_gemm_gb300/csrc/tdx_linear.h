@@ -11,7 +11,7 @@ namespace tdx {
 enum Form { NN, NT, TN };                 // see tdx_linear.cuh
 enum Group { kFlat, kRows, kSums };
 constexpr uint64_t kLinTimeoutNs = 4000000000ull;
-constexpr int kLinSegment = 16;   // K slices summed on the tensor cores alone, for fp32 results
+constexpr int kLinSegment = 14;   // K slices summed on the tensor cores alone, for fp32 results
 constexpr int kFewRows = 16;   // rows of the small boxes of A
 
 // Tile columns: pairs 256. Single CTAs 128, and 256 for e4m3, whose 128-column boxes would not split

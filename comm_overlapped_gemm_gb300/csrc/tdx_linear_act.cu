@@ -13,47 +13,58 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRowsAhead = 4;       // rows whose loads a thread has in flight
-constexpr int kMostBlocks = 2432;   // 16 blocks on each of 152 SMs: row chunks are cut to about that many
+constexpr int kMostBlocks = 912;    // 6 blocks for each of 152 SMs
 
 struct ActBwdParams {
   const bf16* dy;
   const bf16* z;
   bf16* dz;
-  float* part;      // [chunks][N], or dbias itself for one chunk; NULL: no sums
-  int M, cols, chunk;
+  float* part;      // [row groups][N], or dbias itself for one group; NULL: no sums
+  int M, cols;
   int lanes;        // lanes of a row, a power of two; threads / lanes rows at a time
   int64_t ld_dy, ld_z;
 };
 
-// dz of the N values z (gates) and u, given dy; SWIGLU alone uses u, and leaves its gradient there
+// sigmoid of two values whose exponents times -log2(e) are z, and what is left to 1
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 z, f32x2* rest) {
+  const f32x2 part = pair(kPart, kPart);
+  const f32x2 d = fma2(pair(power_of_2(first(z)), power_of_2(second(z))), part, part);
+  const f32x2 s = mul2(part, pair(reciprocal(first(d)), reciprocal(second(d))));
+  *rest = fma2(s, pair(-1.0f, -1.0f), pair(1.0f, 1.0f));
+  return s;
+}
+
+// dz of two values z (gates), given dy; SWIGLU alone uses u, and leaves its gradient there. In pairs: one value at a
+// time, 73% of the issue slots held the loads up (16381 x 8192 GELU_TANH 133 us).
 template <int ACT>
-__device__ __forceinline__ void act_backward(float (&dy)[8], const float (&z)[8], float (&u)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = z[i];
-    if (ACT == TDX_ACT_RELU) {
-      dy[i] = x > 0.0f ? dy[i] : 0.0f;
-    } else if (ACT == TDX_ACT_GELU) {
-      dy[i] *= fmaf(x * kInvRoot2Pi, power_of_2(-0.5f * kLog2e * x * x), 0.5f * erfcf(-kHalfRoot * x));
-    } else if (ACT == TDX_ACT_GELU_TANH) {
-      float rest;
-      const float s = sigmoid<false>(gelu_arg(x), &rest);
-      dy[i] *= s * fmaf(x * rest, kGelu2 * fmaf(3.0f * kGeluCube * x, x, 1.0f), 1.0f);
-    } else if (ACT == TDX_ACT_SILU) {
-      float rest;
-      const float s = sigmoid<false>(x, &rest);
-      dy[i] *= s * fmaf(x, rest, 1.0f);
-    } else if (ACT == TDX_ACT_SWIGLU) {
-      float rest;
-      const float s = sigmoid<false>(x, &rest), ds = dy[i] * s;
-      dy[i] = ds * u[i] * fmaf(x, rest, 1.0f);
-      u[i] = ds * x;
+__device__ __forceinline__ void act_backward(f32x2& dy, f32x2 x, f32x2& u) {
+  auto both = [](float v) { return pair(v, v); };
+  f32x2 rest;
+  if (ACT == TDX_ACT_RELU) {
+    dy = pair(first(x) > 0.0f ? first(dy) : 0.0f, second(x) > 0.0f ? second(dy) : 0.0f);
+  } else if (ACT == TDX_ACT_GELU) {
+    auto one = [](float v) {
+      return fmaf(v * kInvRoot2Pi, power_of_2(-0.5f * kLog2e * v * v), 0.5f * erfcf(-kHalfRoot * v));
+    };
+    dy = mul2(dy, pair(one(first(x)), one(second(x))));
+  } else if (ACT == TDX_ACT_GELU_TANH) {
+    const f32x2 square = mul2(x, x);
+    const f32x2 z = mul2(x, fma2(both(-kLog2e * kGelu2 * kGeluCube), square, both(-kLog2e * kGelu2)));
+    const f32x2 s = sigmoid2(z, &rest);
+    const f32x2 slope = fma2(both(3.0f * kGelu2 * kGeluCube), square, both(kGelu2));
+    dy = mul2(mul2(dy, s), fma2(mul2(x, rest), slope, both(1.0f)));
+  } else if (ACT == TDX_ACT_SILU || ACT == TDX_ACT_SWIGLU) {
+    const f32x2 ds = mul2(dy, sigmoid2(mul2(x, both(-kLog2e)), &rest));
+    dy = mul2(ds, fma2(x, rest, both(1.0f)));
+    if (ACT == TDX_ACT_SWIGLU) {
+      dy = mul2(dy, u);
+      u = mul2(ds, x);
     }
   }
 }
 
 // Bound by HBM. A warp reads whole lines of a row (several rows where a row is short), a thread keeps the
-// sums of its 8 columns (16 for SWIGLU) in registers over the rows of its chunk; they are joined in shared memory
+// sums of its 8 columns (16 for SWIGLU) in registers over its rows; they are joined in shared memory
 // in a fixed order.
 template <int ACT>
 __global__ void __launch_bounds__(kThreads) tdx_linear_act_bwd_kernel(const __grid_constant__ ActBwdParams p) {
@@ -64,17 +75,17 @@ __global__ void __launch_bounds__(kThreads) tdx_linear_act_bwd_kernel(const __gr
   const int at = threadIdx.x % p.lanes, sub = threadIdx.x / p.lanes, step = kThreads / p.lanes;
   const int col = (blockIdx.x * p.lanes + at) * 8;
   const bool mine = col < p.cols;
-  const int64_t first = static_cast<int64_t>(blockIdx.y) * p.chunk;
-  const int64_t end = first + p.chunk < p.M ? first + p.chunk : p.M;
-  float sum[kSums] = {};
+  f32x2 sum[kSums / 2] = {};
   griddep_wait();
   if (mine) {
-    for (int64_t r0 = first + sub; r0 < end; r0 += kRowsAhead * step) {
+    // the row groups take turns, so that the blocks at work together read one front of the rows
+    const int64_t turn = static_cast<int64_t>(gridDim.y) * kRowsAhead * step;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * kRowsAhead * step + sub; r0 < p.M; r0 += turn) {
       uint4 qd[kRowsAhead], qz[kRowsAhead], qu[kRowsAhead];
 #pragma unroll
       for (int k = 0; k < kRowsAhead; ++k) {
         const int64_t r = r0 + k * step;
-        if (r < end) {
+        if (r < p.M) {
           qd[k] = __ldcs(reinterpret_cast<const uint4*>(p.dy + r * p.ld_dy + col));
           if (ACT != TDX_ACT_NONE) qz[k] = __ldcs(reinterpret_cast<const uint4*>(p.z + r * p.ld_z + col));
           if (kGated) qu[k] = __ldcs(reinterpret_cast<const uint4*>(p.z + r * p.ld_z + p.cols + col));
@@ -83,17 +94,16 @@ __global__ void __launch_bounds__(kThreads) tdx_linear_act_bwd_kernel(const __gr
 #pragma unroll
       for (int k = 0; k < kRowsAhead; ++k) {
         const int64_t r = r0 + k * step;
-        if (r < end) {
-          float d[8], z[8], u[8];
+        if (r < p.M) {
+          f32x2 d[4], z[4], u[4];
           unpack(qd[k], d, bf16{});
           if (ACT != TDX_ACT_NONE) unpack(qz[k], z, bf16{});
           if (kGated) unpack(qu[k], u, bf16{});
-          act_backward<ACT>(d, z, u);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[i] = __fadd_rn(sum[i], d[i]);   // of dz as computed: same bits with and without dz
-          if (kGated) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum[kSums - 8 + i] = __fadd_rn(sum[kSums - 8 + i], u[i]);
+          for (int i = 0; i < 4; ++i) {
+            act_backward<ACT>(d[i], z[i], u[i]);
+            sum[i] = add2(sum[i], d[i]);
+            if (kGated) sum[kSums / 2 - 4 + i] = add2(sum[kSums / 2 - 4 + i], u[i]);
           }
           if (p.dz != nullptr) {
             store_vec(p.dz + r * p.ld_z + col, d);
@@ -105,7 +115,10 @@ __global__ void __launch_bounds__(kThreads) tdx_linear_act_bwd_kernel(const __gr
   }
   if (p.part == nullptr) return;
 #pragma unroll
-  for (int i = 0; i < kSums; ++i) sm[threadIdx.x][i] = sum[i];
+  for (int i = 0; i < kSums / 2; ++i) {
+    sm[threadIdx.x][2 * i] = first(sum[i]);
+    sm[threadIdx.x][2 * i + 1] = second(sum[i]);
+  }
   __syncthreads();
   const int64_t row = static_cast<int64_t>(blockIdx.y) * (kGated ? 2 : 1) * p.cols;
   for (int i = threadIdx.x; i < p.lanes * kSums; i += kThreads) {
@@ -125,15 +138,10 @@ int lanes_of(int cols) {
 }
 int col_blocks(int cols) { return (cols + lanes_of(cols) * 8 - 1) / (lanes_of(cols) * 8); }
 
-// Rows of a chunk: as many chunks as kMostBlocks allows, but no shorter than every thread's rows in flight
-int chunk_rows(int M, int cols) {
-  const int chunks = std::max(1, kMostBlocks / col_blocks(cols));
-  const int least = kThreads / lanes_of(cols) * kRowsAhead;
-  return std::max(static_cast<int>((static_cast<int64_t>(M) + chunks - 1) / chunks), least);
-}
-int chunks_of(int M, int cols) {
-  const int rows = chunk_rows(M, cols);
-  return std::max(1, static_cast<int>((static_cast<int64_t>(M) + rows - 1) / rows));
+// Row groups: as many as kMostBlocks allows, but none without rows for every thread's loads
+int groups_of(int M, int cols) {
+  const int64_t turn = kThreads / lanes_of(cols) * kRowsAhead;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMostBlocks / col_blocks(cols), (M + turn - 1) / turn)));
 }
 
 tdx_status launch_act(tdx_activation act, const ActBwdParams& p, dim3 grid, cudaStream_t st) {
@@ -177,7 +185,7 @@ tdx_status tdx_linear_act_bwd_workspace_size(int M, int N, tdx_dtype dtype, cons
   const tdx_linear_opts o = opts ? *opts : linear_defaults();
   const tdx_status s = check_sizes(M, N, dtype, o);
   if (s != TDX_OK) return s;
-  *bytes = static_cast<size_t>(chunks_of(M, o.act == TDX_ACT_SWIGLU ? N / 2 : N)) * N * sizeof(float);
+  *bytes = static_cast<size_t>(groups_of(M, o.act == TDX_ACT_SWIGLU ? N / 2 : N)) * N * sizeof(float);
   return TDX_OK;
 }
 
@@ -201,18 +209,17 @@ tdx_status tdx_linear_act_bwd(const void* dy, const void* z, void* dz, float* db
   if (dbias != nullptr && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need))
     return TDX_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int chunks = chunks_of(M, p.cols);
+  const int groups = groups_of(M, p.cols);
   if (M == 0 && dbias == nullptr) return TDX_OK;
   p.dy = static_cast<const bf16*>(dy);
   p.z = static_cast<const bf16*>(z);
   p.dz = static_cast<bf16*>(dz);
   p.M = M;
-  p.chunk = chunk_rows(M, p.cols);
   p.lanes = lanes_of(p.cols);
-  if (dbias != nullptr) p.part = chunks > 1 ? static_cast<float*>(workspace) : dbias;
-  s = launch_act(o.act, p, dim3(static_cast<unsigned>(col_blocks(p.cols)), static_cast<unsigned>(chunks), 1), st);
-  if (s != TDX_OK || dbias == nullptr || chunks == 1) return s;
-  return launch_sum_parts(static_cast<const float*>(workspace), dbias, chunks, N, st);
+  if (dbias != nullptr) p.part = groups > 1 ? static_cast<float*>(workspace) : dbias;
+  s = launch_act(o.act, p, dim3(static_cast<unsigned>(col_blocks(p.cols)), static_cast<unsigned>(groups), 1), st);
+  if (s != TDX_OK || dbias == nullptr || groups == 1) return s;
+  return launch_sum_parts(static_cast<const float*>(workspace), dbias, groups, N, st);
 }
 
 }  // extern "C"
