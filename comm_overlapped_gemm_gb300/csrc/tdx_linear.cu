@@ -115,7 +115,7 @@ tdx_status run(Form form, Group group, bool fp8, LinParams& p, const Operand& a,
   p.wide = aligned(p.out, 32) && p.ld_out * out % 32 == 0 && p.out_step * out % 32 == 0;
   p.wide_z = aligned(p.z, 32) && p.ld_z % 16 == 0 && (!p.gated || p.cols % 16 == 0);
   // a warp's columns of a tile (half of them) are whole 128-byte rows; strides as tensor maps take them
-  p.tma_out = p.out_type != TDX_FP8_E4M3 && !p.accumulate && width / 2 * out >= 128 && p.ld_out * out < kMostBytes &&
+  p.tma_out = p.out_type != TDX_FP8_E4M3 && width / 2 * out >= 128 && p.ld_out * out < kMostBytes &&
               p.out_step * out < kMostBytes;
   p.plain = p.bias == nullptr && p.z == nullptr && p.act == TDX_ACT_NONE;
   if (p.tma_out) {

@@ -318,12 +318,19 @@ __device__ __forceinline__ void st_shared_v4(uint8_t* row, int unit, int lane, u
   *reinterpret_cast<uint4*>(row + ((unit ^ (lane & 7)) * 16)) = q;
 }
 
-// TMA store of a staged box (coordinates innermost first), in this thread's bulk group
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(z), "r"(src)
-               : "memory");
+// TMA store of a staged box (coordinates innermost first), or its addition to fp32 values as they are (rounded to
+// nearest, by L2: nothing is read back here), in this thread's bulk group
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z, bool add) {
+  if (add)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
 }
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -335,19 +342,19 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-// A warp's columns [begin, last) of a tile that are scaled, rounded and stored, perhaps with a residual added, and
-// nothing else, in boxes of 128-byte rows. 32 columns at a time (the accumulators behind `last` are read, not stored), values in
+// A warp's columns [begin, last) of a tile that are scaled, rounded and stored, perhaps with a row added (the residual,
+// or the output as it is), and nothing else, in boxes of 128-byte rows. 32 columns at a time (the accumulators behind `last` are read, not stored), values in
 // pairs, the next columns' residual on its way. The general loop takes four times the instructions: 8192 x 512 x 8192
 // 68 us with it, 57 with this one.
 template <bool F32, bool RES>
-__device__ __forceinline__ void lin_plain(const LinParams& p, const LinRow& lr, uint32_t d, bool none, bool row_ok, int n0,
-                                          int begin, int last, uint8_t* stage, int warp_row, int z) {
+__device__ __forceinline__ void lin_plain(const LinParams& p, float row_scale, const bf16* add, uint32_t d, bool none,
+                                          bool row_ok, int n0, int begin, int last, uint8_t* stage, int warp_row, int z) {
   const int lane = threadIdx.x & 31;
   uint8_t* stage_row = stage + lane * 128;
-  const f32x2 scale = pair(lr.scale, lr.scale);
+  const f32x2 scale = pair(row_scale, row_scale);
   uint4 res[4];
   auto fetch = [&](int c) {
-    const uint4* at = reinterpret_cast<const uint4*>(p.residual + lr.res + n0 + c);
+    const uint4* at = reinterpret_cast<const uint4*>(add + n0 + c);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (row_ok && c + 8 * i < last) res[i] = at[i];
@@ -398,7 +405,7 @@ __device__ __forceinline__ void lin_plain(const LinParams& p, const LinRow& lr, 
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) {
-        tma_store_3d(&p.tm_c, smem_u32(stage), n0 + c - in_box, warp_row, z);
+        tma_store_3d(&p.tm_c, smem_u32(stage), n0 + c - in_box, warp_row, z, F32 && p.accumulate);
         bulk_commit();
       }
     }
@@ -734,13 +741,13 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
       uint8_t* stage_row = staging + (warp - kEpiWarp0) * kStoreBytes + lane * 128;
       const int box_cols = p.out_type == TDX_BF16 ? 64 : 32, z = GROUP == kSums ? t.e : 0;
       uint8_t* stage = staging + (warp - kEpiWarp0) * kStoreBytes;
-      if (box && p.plain && p.out_type == TDX_FP32 && !(LinSteps<FORM>::kResidual && p.residual != nullptr)) {
-        lin_plain<true, false>(p, lr, d, none, row_ok, n0, first, last, stage, warp_row, z);
+      const bf16* add = LinSteps<FORM>::kResidual && p.residual != nullptr ? p.residual + lr.res : nullptr;
+      if (LinSteps<FORM>::kAccumulate && p.accumulate) add = static_cast<const bf16*>(p.out) + lr.out;
+      if (box && p.plain && p.out_type == TDX_FP32 && (LinSteps<FORM>::kAccumulate || add == nullptr)) {
+        lin_plain<true, false>(p, lr.scale, nullptr, d, none, row_ok, n0, first, last, stage, warp_row, z);
       } else if (box && p.plain && p.out_type == TDX_BF16) {
-        if (LinSteps<FORM>::kResidual && p.residual != nullptr)
-          lin_plain<false, true>(p, lr, d, none, row_ok, n0, first, last, stage, warp_row, z);
-        else
-          lin_plain<false, false>(p, lr, d, none, row_ok, n0, first, last, stage, warp_row, z);
+        if (add != nullptr) lin_plain<false, true>(p, lr.scale, add, d, none, row_ok, n0, first, last, stage, warp_row, z);
+        else lin_plain<false, false>(p, lr.scale, add, d, none, row_ok, n0, first, last, stage, warp_row, z);
       } else
       // a rolled loop over 16 columns: unrolled over the tile its code came from L2 anew with every tile
 #pragma unroll 1
@@ -784,7 +791,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(&p.tm_c, smem_u32(stage), col - in_box, warp_row, z);
+            tma_store_3d(&p.tm_c, smem_u32(stage), col - in_box, warp_row, z, LinSteps<FORM>::kAccumulate && p.accumulate);
             bulk_commit();
           }
         }

@@ -49,7 +49,7 @@ struct LinParams {
   void* out;
   int64_t ld_out, ld_res, ld_z;
   int64_t out_step;         // kSums: elements between two experts' outputs
-  int tma_out;              // output through tm_c (bf16 or fp32, not added to, whole 128-byte columns per warp)
+  int tma_out;              // output through tm_c (bf16 or fp32; whole 128-byte columns per warp)
   int wide, wide_z;         // output and z in 32-byte stores: 32-byte aligned rows
   int plain;                // no bias, z nor activation: the short epilogue where tma_out is set
   int overlap;
