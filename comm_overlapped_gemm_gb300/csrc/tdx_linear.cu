@@ -40,24 +40,32 @@ bool map_of(CUtensorMap* m, const Operand& o, bool fp8, int rank, int box_rows) 
   return encode_map(m, o.p, static_cast<int>(elt), rank, dims, strides, box);
 }
 
-// How a product of about `tiles256` / `tiles1` pair and single tiles with `nkb` K slices runs
+// How a product of about `tiles256` pair or `tiles1` single tiles of `nkb` K slices runs: in pairs, or on single
+// CTAs, a tile's K slices over clusters of `split`
 struct Shape {
   bool pair;
   int split;
 };
 
-// Microseconds of one K slice (128 bytes of K) of a pair's 256 x 256 and of a single CTA's tile, and of
-// a tile's start and end
-constexpr float kPairSlice = 0.29f, kSingleSlice = 0.17f, kTileCost = 2.0f, kFoldCost = 2.0f;
+// Microseconds, as measured over 1 .. 4096 rows, 512 .. 8192 of K and of N: a launch's fixed part; one K slice (128
+// bytes of K) of a pair's and of a single CTA's tile; a persistent kernel's last epilogue; the addition of a tile's
+// partials, once and for each 128 rows of each CTA; what a second wave of clusters adds.
+constexpr float kLaunch = 5.0f, kPairSlice = 0.30f, kSingleSlice = 0.27f, kSingleSliceE4m3 = 0.33f;
+constexpr float kPairEnd = 1.5f, kSingleEnd = 1.0f, kFold = 2.2f, kFoldRows = 1.8f, kFoldRowsCta = 0.5f, kWave = 3.0f;
 
-Shape choose(int64_t tiles256, int64_t tiles1, int64_t most1, int nkb) {
+Shape choose(bool fp8, int64_t tiles256, int64_t tiles1, int64_t most1, int nkb, float rows) {
   const int sms = sm_count() > 0 ? sm_count() : kRefSMs;
+  auto waves = [](int64_t tiles, int at_once) { return static_cast<float>((tiles + at_once - 1) / at_once); };
   Shape best = {true, 1};
-  float t = static_cast<float>((tiles256 + sms / 2 - 1) / (sms / 2)) * (nkb * kPairSlice + kTileCost);
+  float t = kLaunch + waves(tiles256, sms / 2) * nkb * kPairSlice + kPairEnd;
+  const float slice = fp8 ? kSingleSliceE4m3 : kSingleSlice;
   for (int s = 1; s <= 8; s *= 2) {
-    if (s > 1 && (s > nkb || most1 * s > 2 * sms)) break;
-    const float one = static_cast<float>((tiles1 * s + sms - 1) / sms) *
-                      ((nkb + s - 1) / s * kSingleSlice + kTileCost + (s > 1 ? kFoldCost : 0.0f));
+    if (s > 1 && (s > nkb || most1 * s > 4 * sms)) break;
+    float one = kLaunch + waves(tiles1, sms) * nkb * slice + kSingleEnd;
+    if (s > 1) {
+      const float w = waves(tiles1, lin_clusters(s));
+      one = kLaunch + w * ((nkb + s - 1) / s * slice + kFold + rows / 128.0f * (kFoldRows + s * kFoldRowsCta)) + (w - 1) * kWave;
+    }
     if (one < t) {
       t = one;
       best = {false, s};
@@ -85,7 +93,6 @@ tdx_status run(Form form, Group group, bool fp8, LinParams& p, const Operand& a,
     const int64_t runs = std::min(E, rows);
     most256 = (rows + runs * 255) / 256 * n256;
     most1 = (rows + runs * 127) / 128 * n1;
-    t256 = std::min((rows + runs * 128) / 256 + 1, most256) * 1;
     t256 = std::max<int64_t>(std::min((rows / 256 + (runs + 1) / 2) * n256, most256), 1);
     t1 = std::max<int64_t>(std::min((rows / 128 + (rows > runs * 64 ? (runs + 1) / 2 : runs)) * n1, most1), 1);
   } else {
@@ -94,7 +101,8 @@ tdx_status run(Form form, Group group, bool fp8, LinParams& p, const Operand& a,
     if (group == kSums) k = (k + E - 1) / E;
   }
   const int nkb = static_cast<int>((k + bk - 1) / bk);
-  const Shape shape = choose(t256, t1, most1, nkb);
+  const int64_t tile_rows = group == kRows ? (rows + std::min(E, rows) - 1) / std::min(E, rows) : rows;
+  const Shape shape = choose(fp8, t256, t1, most1, nkb, static_cast<float>(std::min<int64_t>(tile_rows, 128)));
   const int64_t most = shape.pair ? most256 : most1;
   if (most + kMoeMaxExperts * std::max(n1, n256) >= INT64_C(0x7FFFFFFF)) return TDX_ERR_UNSUPPORTED;
   const int bn = lin_block_n(fp8, shape.pair);
@@ -110,7 +118,8 @@ tdx_status run(Form form, Group group, bool fp8, LinParams& p, const Operand& a,
   p.keep_b = group == kRows ? (rows > std::min(E, rows) * tm ? 1 : 0) : (p.tiles_m > 1 ? 1 : 0);
   const int b_rows = form == NT ? 128 : bk;
   if (!map_of(&p.tm_a, a, fp8, 2, form == TN ? bk : kBM) || !map_of(&p.tm_b, b, fp8, 3, b_rows)) return TDX_ERR_CUDA;
-  if (form != TN && !map_of(&p.tm_few, a, fp8, 2, kFewRows)) return TDX_ERR_CUDA;
+  p.few_rows = std::min(kFewRows, p.M);
+  if (form != TN && !map_of(&p.tm_few, a, fp8, 2, p.few_rows)) return TDX_ERR_CUDA;
   const int64_t out = static_cast<int64_t>(bytes_of(p.out_type));
   p.wide = aligned(p.out, 32) && p.ld_out * out % 32 == 0 && p.out_step * out % 32 == 0;
   p.wide_z = aligned(p.z, 32) && p.ld_z % 16 == 0 && (!p.gated || p.cols % 16 == 0);

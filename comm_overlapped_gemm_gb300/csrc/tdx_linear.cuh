@@ -480,34 +480,41 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
       uint32_t phase = 0;
       bool stop = false;
       const uint64_t keep_a = policy_of(p.keep_a), keep_b = policy_of(p.keep_b);
+      const uint32_t leader_full0 = PAIR ? mapa_shared(full0, 0) : full0;
+      const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
       for (int it = cid; it < items && !stop; it += ncl) {
         const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, it, crank);
-        // the tile's first column of each half of B (SWIGLU: gate columns, then the other half's)
-        const int n0 = t.nt * (p.gated ? BN / 2 : BN);
-        // A tile of few rows loads only them, in boxes of kFewRows: the rows that a box fills with zeros past
-        // the end of A cost as much as real ones (1 x 8192 x 8192: streaming B alone 23 us, with boxes of 8 or 16
-        // rows of A 23, of 64 rows 31, of 128 rows 33). The accumulators of the rows behind are never read.
-        const int few = !PAIR && !C::A_MN && t.mend - t.m0 <= 4 * kFewRows ? (t.mend - t.m0 + kFewRows - 1) / kFewRows : 0;
-        const uint32_t bytes = few > 0 ? few * kFewRows * 128 + C::B_BYTES : C::STAGE_BYTES;
+        // What stays the same over the tile's slices: this thread's pace is what small tiles wait for (a slice took
+        // it 296 cycles, and 568 with a loop over boxes of few rows).
+        const int n0 = t.nt * (LinSteps<FORM>::kForward && p.gated ? BN / 2 : BN);
+        int n[C::B_BOXES];   // first columns of the boxes of B (SWIGLU: gate columns, then the other half's)
+#pragma unroll
+        for (int j = 0; j < C::B_BOXES; ++j) {
+          const int c = (PAIR ? crank * C::N_CTA : 0) + j * (C::B_MN ? C::BOX_N : 128);
+          n[j] = LinSteps<FORM>::kForward && p.gated && c >= BN / 2 ? p.cols + n0 + c - BN / 2 : n0 + c;
+        }
+        const int z = GROUP == kRows ? t.e : 0;
+        // A tile of few rows loads only them: rows that a box fills with zeros past the end of A cost as much as
+        // real ones (1 x 8192 x 8192: streaming B alone 23 us, with boxes of 8 or 16 rows of A 23, of 64 rows 31, of
+        // 128 rows 33). The accumulators of the rows behind are never read.
+        const bool few = !PAIR && !C::A_MN && t.mend - t.m0 <= p.few_rows;
+        const CUtensorMap* map_a = few ? &p.tm_few : &p.tm_a;
+        const uint32_t bytes = few ? p.few_rows * 128 + C::B_BYTES : C::STAGE_BYTES;
+        int k = t.k0 + t.kb0 * C::BK;
         // One slice; a tail slice is counted on this CTA's own tail barrier. Two instances of the code: with the
         // choice made per load in one loop, the loop and not the tensor cores set the pace (one run of 2048 rows, 2048 x
         // 57344: 379 us against 272).
-        auto issue = [&](int kb, auto is_tail) {
+        auto issue = [&](auto is_tail) {
           constexpr bool kTail = decltype(is_tail)::value;
           if (!lin_wait(p.status, empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
             stop = true;
             return;
           }
           const uint32_t own = (kTail ? tail0 : full0) + 8 * stage;
-          uint32_t bar = own;
-          if constexpr (!PAIR || kTail) {
-            mbar_arrive_expect_tx(own, bytes);
-          } else {
-            bar = mapa_shared(own, 0);   // both CTAs' slices count on the leader's barrier
-            if (leader) mbar_arrive_expect_tx(own, 2 * C::STAGE_BYTES);
-          }
-          const int k = t.k0 + kb * C::BK;
-          const uint32_t a = smem_u32(sA + stage * C::A_BYTES), b = smem_u32(sB + stage * C::B_BYTES);
+          const uint32_t bar = PAIR && !kTail ? leader_full0 + 8 * stage : own;   // a pair's slices count on the leader's
+          if constexpr (!PAIR || kTail) mbar_arrive_expect_tx(own, bytes);
+          else if (leader) mbar_arrive_expect_tx(own, 2 * C::STAGE_BYTES);
+          const uint32_t a = a0 + stage * C::A_BYTES, b = b0 + stage * C::B_BYTES;
           if constexpr (C::A_MN) {
 #pragma unroll
             for (int j = 0; j < C::A_BOXES; ++j) {
@@ -518,21 +525,17 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
             }
           } else if constexpr (PAIR) {
             tma_load_2d_pair_hint(a, &p.tm_a, bar, k, t.m0, keep_a);
-          } else if (few == 0) {
-            tma_load_2d_hint(a, &p.tm_a, bar, k, t.m0, keep_a);
           } else {
-            for (int j = 0; j < few; ++j)
-              tma_load_2d_hint(a + j * kFewRows * 128, &p.tm_few, bar, k, t.m0 + j * kFewRows, keep_a);
+            tma_load_2d_hint(a, map_a, bar, k, t.m0, keep_a);
           }
 #pragma unroll
           for (int j = 0; j < C::B_BOXES; ++j) {
             const uint32_t dst = b + j * C::B_BOX_STEP;
-            const int c = (PAIR ? crank * C::N_CTA : 0) + j * (C::B_MN ? C::BOX_N : 128);
-            const int n = LinSteps<FORM>::kForward && p.gated && c >= BN / 2 ? p.cols + n0 + c - BN / 2 : n0 + c;
-            const int x = C::B_MN ? n : k, y = C::B_MN ? k : n, z = GROUP == kRows ? t.e : 0;
+            const int x = C::B_MN ? n[j] : k, y = C::B_MN ? k : n[j];
             if constexpr (PAIR && !kTail) tma_load_3d_pair_hint(dst, &p.tm_b, bar, x, y, z, keep_b);
             else tma_load_3d_hint(dst, &p.tm_b, bar, x, y, z, keep_b);
           }
+          k += C::BK;
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -540,9 +543,9 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
         };
         const bool tail = GROUP == kSums && t.kb1 > t.kb0 && t.kb1 * C::BK > t.klen;
         const int whole = tail ? t.kb1 - 1 : t.kb1;
-        for (int kb = t.kb0; kb < whole && !stop; ++kb) issue(kb, std::false_type{});
+        for (int kb = t.kb0; kb < whole && !stop; ++kb) issue(std::false_type{});
         if constexpr (GROUP == kSums) {
-          if (tail && !stop) issue(whole, std::true_type{});
+          if (tail && !stop) issue(std::true_type{});
         }
       }
     }

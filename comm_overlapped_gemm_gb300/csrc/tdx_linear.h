@@ -12,7 +12,7 @@ enum Form { NN, NT, TN };                 // see tdx_linear.cuh
 enum Group { kFlat, kRows, kSums };
 constexpr uint64_t kLinTimeoutNs = 4000000000ull;
 constexpr int kLinSegment = 14;   // K slices summed on the tensor cores alone, for fp32 results
-constexpr int kFewRows = 16;   // rows of the small boxes of A
+constexpr int kFewRows = 16;   // most rows of the small boxes of A
 
 // Tile columns: pairs 256. Single CTAs 128, and 256 for e4m3, whose 128-column boxes would not split
 // a 128-column tile into gate and up halves.
@@ -34,6 +34,7 @@ struct LinParams {
   int E;
   const int32_t* offsets;
   int tiles_m, tiles_n, items, group_n;
+  int few_rows;             // rows of tm_few's boxes: kFewRows, or all rows of a smaller A
   int split;                // CTAs that share a tile's K slices (single CTAs)
   int keep_a, keep_b;       // L2 policies of the operands' loads (policy_of)
   int gated;                // act == TDX_ACT_SWIGLU
@@ -61,5 +62,8 @@ struct LinParams {
 using LinLaunch = tdx_status(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream);
 LinLaunch launch_linear_nn, launch_linear_nt, launch_linear_tn, launch_linear_e4m3;
 LinLaunch launch_linear_nn_long, launch_linear_nt_long, launch_linear_tn_long, launch_linear_e4m3_long;
+
+// Clusters of `split` single CTAs that are resident together on the current device (2, 4 or 8)
+int lin_clusters(int split);
 
 }  // namespace tdx

@@ -374,6 +374,23 @@ def test_grouped_e4m3(act):
         close(C, y, slack, BF)
 
 
+def test_grouped_bwd_no_rows():
+    """Experts without any row: their gradients are 0, and dX, of no rows, is left alone."""
+    one = torch.ones(8, 128, dtype=BF, device="cuda")
+    B = torch.ones(3, 64, 128, dtype=BF, device="cuda")
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for rows in (0, 8):   # no rows at all, and 8 rows of no expert
+        dB = torch.full((3, 64, 128), 3.0, device="cuda")
+        dX = torch.full((8, 64), 3.0, dtype=BF, device="cuda")
+        X = torch.full((8, 64), float("nan"), dtype=BF, device="cuda")
+        tdx.check(tdx.tdx_grouped_gemm_bwd(one, X, off, B, dX, dB, rows, 64, 128, 3, tdx.TDX_BF16,
+                                           tdx.make_linear_opts(dw_dtype=tdx.TDX_FP32)))
+        assert (dB == 0).all() and (dX == 3.0).all()
+        Y = torch.full((8, 128), 3.0, dtype=BF, device="cuda")
+        tdx.check(tdx.tdx_grouped_gemm(X, off, B, None, None, Y, None, rows, 64, 128, 3, tdx.TDX_BF16))
+        assert (Y == 3.0).all()
+
+
 def test_grouped_offsets_out_of_order():
     """Entries outside [0, R] are taken into it, one below its predecessor is raised to it."""
     g = gen(9)
@@ -394,13 +411,13 @@ def test_grouped_offsets_out_of_order():
 @pytest.mark.parametrize("M,N", [(8, 128), (100, 272), (2048, 2304)])
 def test_fp32_results_of_long_sums(M, N):
     """The tensor cores truncate each of a sum's additions, which for terms of one sign drifts with K. fp32 results
-    add segments of 16 slices (1024 of K in bf16: 64 additions within 2^-22 each, 80 with the margin above) in
-    fp32, K / 1024 additions within 2^-24 each: whatever K, the error stays below that of the segments' own."""
+    add segments of 14 slices (896 of K in bf16: 56 additions within 2^-22 each, 80 with a margin as above) in
+    fp32, K / 896 additions within 2^-24 each: whatever K, the error stays below that of the segments' own."""
     g = gen(M)
     K = 32768
     A = (torch.rand(M, K, generator=g) + 0.5).to(BF).cuda()
     B = (torch.rand(K, N, generator=g) + 0.5).to(BF).cuda()
-    lim = 80 * 2.0 ** -22 + (K / 1024 + 8) * 2.0 ** -24
+    lim = 80 * 2.0 ** -22 + (K / 896 + 8) * 2.0 ** -24
     want = A.double() @ B.double()
     C, _ = run_linear(A, B, out=F32)
     assert float(((C.double() - want) / want).abs().max()) <= lim
