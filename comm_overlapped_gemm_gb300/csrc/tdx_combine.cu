@@ -41,8 +41,8 @@ __global__ void __launch_bounds__(kThreads) tdx_moe_combine_kernel(const __grid_
     float g[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      row[j] = j0 + j < p.topk ? __ldg(dest + j0 + j) : -1;
-      g[j] = gates != nullptr && j0 + j < p.topk ? __ldg(gates + j0 + j) : 1.0f;
+      row[j] = j0 + j < p.topk ? *(dest + j0 + j) : -1;
+      g[j] = gates != nullptr && j0 + j < p.topk ? *(gates + j0 + j) : 1.0f;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -75,9 +75,9 @@ __global__ void __launch_bounds__(kBwdThreads) tdx_moe_combine_bwd_kernel(const 
   float g[K], dot[K];
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    row[j] = j < p.topk ? __ldg(p.dest + t * p.topk + j) : -1;
+    row[j] = j < p.topk ? *(p.dest + t * p.topk + j) : -1;
     if (row[j] >= p.R) row[j] = -1;
-    g[j] = p.gates != nullptr && j < p.topk ? __ldg(p.gates + t * p.topk + j) : 1.0f;
+    g[j] = p.gates != nullptr && j < p.topk ? *(p.gates + t * p.topk + j) : 1.0f;
     dot[j] = 0.0f;
   }
   const T* dout = static_cast<const T*>(p.dout) + t * p.ld_out;

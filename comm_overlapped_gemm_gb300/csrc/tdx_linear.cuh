@@ -166,7 +166,7 @@ __device__ __forceinline__ void lin_table(const int32_t* offsets, int E, int row
 #pragma unroll
   for (int i = 0; i < (kMoeMaxExperts + 32) / 32; ++i) {
     const int e = i * 32 + lane;
-    v[i] = e <= E ? min(max(__ldg(offsets + e), 0), rows) : 0;
+    v[i] = e <= E ? min(max(offsets[e], 0), rows) : 0;
   }
   int last = 0, tiles = 0;
 #pragma unroll

@@ -48,6 +48,9 @@ __device__ __forceinline__ void act_backward(f32x2& dy, f32x2 x, f32x2& u) {
     };
     dy = mul2(dy, pair(one(first(x)), one(second(x))));
   } else if (ACT == TDX_ACT_GELU_TANH) {
+    // past 16 the derivative is 0 or 1, and x^2 would overflow for values of a mask; a NaN stays
+    auto near = [](float v) { return fabsf(v) > 16.0f ? copysignf(16.0f, v) : v; };
+    x = pair(near(first(x)), near(second(x)));
     const f32x2 square = mul2(x, x);
     const f32x2 z = mul2(x, fma2(both(-kLog2e * kGelu2 * kGeluCube), square, both(-kLog2e * kGelu2)));
     const f32x2 s = sigmoid2(z, &rest);

@@ -104,7 +104,7 @@ def run_linear(A, B, bias=None, res=None, rs=None, out=None, act="none", alpha=1
 
 SIZES = [(1, 8, 8), (1, 64, 128), (1, 4096, 1024), (2, 1000, 136), (16, 8192, 1024), (63, 72, 8), (127, 128, 120),
          (128, 512, 128), (129, 520, 264), (200, 64, 2048), (255, 1024, 1000), (300, 4096, 264), (1000, 264, 1000),
-         (1999, 520, 2040), (2048, 1024, 4096), (4097, 256, 1288), (130, 8, 10000)]
+         (1999, 520, 2040), (2048, 1024, 4096), (4097, 256, 1288), (130, 8, 10000), (1, 72, 100000)]
 
 
 # ---------------------------------------------------------------------------------- linear layer
@@ -180,6 +180,82 @@ def test_linear_e4m3_integers():
         same(C, f64(A) @ f64(B), F32)
 
 
+@pytest.mark.parametrize("M,K,N", [(3, 64, 64), (200, 72, 528), (2304, 128, 2064)])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_linear_rows_off_32_byte_boundaries(M, K, N, out):
+    """Buffers and strides that are multiples of 16 bytes and no more; rows and columns around them untouched."""
+    g = gen(M)
+    e = 8 if out == BF else 4
+    A, B, bias = ints(g, M, K), ints(g, K, N), ints(g, N)
+    buf = torch.full((M * (N + e) + e,), 777.0, device="cuda").to(out)
+    C = buf[e:].view(M, N + e)
+    zbuf = torch.full((M * (N + 8) + 8,), 777.0, device="cuda").to(BF)
+    Z = zbuf[8:].view(M, N + 8)
+    for z in (None, Z):
+        o = tdx.make_linear_opts(out_dtype=code(out), ld_c=N + e, ld_z=N + 8)
+        tdx.check(tdx.tdx_linear(A, B, bias, None, None, C, z, M, K, N, tdx.TDX_BF16, o))
+        want = f64(A) @ f64(B) + f64(bias)
+        same(C[:, :N], want, out)
+        assert (C[:, N:] == C.new_tensor(777.0)).all() and (buf[:e] == buf.new_tensor(777.0)).all()
+    same(Z[:, :N], want, BF)
+    assert (Z[:, N:] == Z.new_tensor(777.0)).all()
+    # gate and up halves, 16-byte steps apart
+    h = N // 2
+    Y = buf[e:e + M * (h + e)].view(M, h + e)
+    buf.fill_(777.0)
+    o = tdx.make_linear_opts(out_dtype=code(out), act=tdx.TDX_ACT_SWIGLU, ld_c=h + e, ld_z=N + 8)
+    tdx.check(tdx.tdx_linear(A, B, bias, None, None, Y, Z, M, K, N, tdx.TDX_BF16, o))
+    same(Z[:, :N], want, BF)
+    y = P.act("swiglu", want)
+    # where exp(-g) passes fp32's range (2^128) the sigmoid, then below 2^-128, is taken as 0: off by |g| 2^-128 |u|
+    tiny = 2.0 ** -127 * np.abs(want[:, :h] * want[:, h:])
+    close(Y[:, :h], y, 2.0 ** -21 * (4 + np.abs(want[:, :h])) * np.abs(y) + tiny, out)
+    assert (Y[:, h:] == Y.new_tensor(777.0)).all()
+
+
+def test_linear_e4m3_to_e4m3():
+    """The e4m3 product's gated result as the next product's e4m3 input. Codes lie up to half a step (2^-4) off."""
+    for M, K, N in [(1, 512, 256), (300, 272, 1056), (1100, 512, 2048)]:
+        g = gen(M)
+        A, B = rand(g, M, K, scale=30.0, dtype=E4), rand(g, K, N, scale=30.0, dtype=E4)
+        C, _ = run_linear(A, B, out=E4, act="swiglu", alpha=2.0 ** -14, out_scale=0.03125)
+        v, mag = P.product(f64(A), f64(B))
+        v, dv, h = v * 2.0 ** -14, acc_slack(K, mag * 2.0 ** -14), N // 2
+        y = P.act("swiglu", v)
+        slack = 1.1 * dv[:, :h] * (np.abs(v[:, h:]) + dv[:, h:]) + np.abs(P.act("silu", v[:, :h])) * dv[:, h:] + \
+            2.0 ** -21 * (4 + np.abs(v[:, :h])) * np.abs(y)
+        close(C, np.clip(y * 32, -448, 448), slack * 32, E4)
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu", "swiglu"])
+def test_activations_of_a_masks_lowest_value(act):
+    """Values at the ends of the type: the gate is 0 or the value itself, its gradient 0 or dy."""
+    low, high = float(torch.finfo(BF).min), float(torch.finfo(BF).max)
+    x = [low, -1e30, -1e19, -200.0, -30.0, 0.0, 30.0, 200.0, 1e19, 1e30, high]
+    n = 16
+    gate = torch.tensor(x + [0.0] * (n - len(x)), device="cuda").to(BF)
+    up = torch.ones(n, dtype=BF, device="cuda")
+    bias = torch.cat([gate, up]) if act == "swiglu" else gate
+    N = bias.numel()
+    A, B = torch.zeros(3, 8, dtype=BF, device="cuda"), torch.zeros(8, N, dtype=BF, device="cuda")
+    want = torch.where(gate > 0, gate, torch.zeros_like(gate)).double().cpu().numpy()
+    for out in (BF, F32):
+        C, _ = run_linear(A, B, bias, out=out, act=act)
+        # from |x| = 30 on what is left of the gate is below 30 * exp(-30) = 3e-12
+        assert (np.abs(f64(C) - want) <= 2.0 ** -8 * np.abs(want) + 3e-12).all()
+    z, dy = bias.expand(3, N).contiguous(), torch.full((3, n), 2.0, dtype=BF, device="cuda")
+    dz = torch.empty_like(z)
+    tdx.check(tdx.tdx_linear_act_bwd(dy, z, dz, None, None, 3, N, 0, tdx.make_linear_opts(act=act_code(act))))
+    got = f64(dz)[:, :n]
+    slope = np.where(f64(gate) > 0, 2.0, 0.0)
+    at0 = np.array([v == 0.0 for v in x] + [True] * (n - len(x)))
+    slope[at0] = 0.0 if act == "relu" else 1.0
+    assert (np.abs(got - slope) <= 1e-9).all()
+    if act != "swiglu":   # the same gradient in place of dy
+        tdx.check(tdx.tdx_linear_act_bwd(dy, z, dy, None, None, 3, N, 0, tdx.make_linear_opts(act=act_code(act))))
+        assert torch.equal(dy, dz)
+
+
 def test_linear_residual_in_place_and_inf():
     g = gen(5)
     for M, N in [(3, 64), (700, 2048)]:
@@ -190,8 +266,8 @@ def test_linear_residual_in_place_and_inf():
         # an infinity and a NaN stay in their own row
         A[1, 5], A[2, 7] = float("inf"), float("nan")
         C2, _ = run_linear(A, B, out=F32)
-        want = f64(A) @ f64(B)
         with np.errstate(invalid="ignore"):
+            want = f64(A) @ f64(B)
             assert np.array_equal(np.isnan(f64(C2)), np.isnan(want))
         keep = [i for i in range(M) if i not in (1, 2)]
         same(C2[keep], want[keep], F32)
