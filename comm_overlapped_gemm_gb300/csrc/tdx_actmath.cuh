@@ -78,4 +78,16 @@ __device__ __forceinline__ void act_forward(tdx_activation act, bool exact, floa
   }
 }
 
+// The approximate forms of two values: RELU, GELU_TANH and SILU (the gate of SWIGLU)
+__device__ __forceinline__ f32x2 act_pair(tdx_activation act, f32x2 v) {
+  if (act == TDX_ACT_RELU) return pair(first(v) < 0.0f ? 0.0f : first(v), second(v) < 0.0f ? 0.0f : second(v));
+  f32x2 z = pair(-kLog2e, -kLog2e);
+  if (act == TDX_ACT_GELU_TANH)
+    z = fma2(mul2(v, v), pair(-kLog2e * kGelu2 * kGeluCube, -kLog2e * kGelu2 * kGeluCube), pair(-kLog2e * kGelu2, -kLog2e * kGelu2));
+  z = mul2(z, v);
+  const f32x2 part = pair(kPart, kPart);
+  const f32x2 d = fma2(pair(power_of_2(first(z)), power_of_2(second(z))), part, part);
+  return mul2(mul2(v, part), pair(reciprocal(first(d)), reciprocal(second(d))));
+}
+
 }  // namespace tdx

@@ -126,7 +126,9 @@ tdx_status run(Form form, Group group, bool fp8, LinParams& p, const Operand& a,
   // a warp's columns of a tile (half of them) are whole 128-byte rows; strides as tensor maps take them
   p.tma_out = p.out_type != TDX_FP8_E4M3 && width / 2 * out >= 128 && p.ld_out * out < kMostBytes &&
               p.out_step * out < kMostBytes;
-  p.plain = p.bias == nullptr && p.z == nullptr && p.act == TDX_ACT_NONE;
+  const bool bare = p.bias == nullptr && p.z == nullptr && p.act == TDX_ACT_NONE;
+  const bool approximate = p.act == TDX_ACT_RELU || p.act == TDX_ACT_GELU_TANH || p.act == TDX_ACT_SILU;
+  p.steps = bare ? 0 : p.out_type != TDX_BF16 ? -1 : p.gated ? 2 : approximate ? 1 : -1;
   if (p.tma_out) {
     const uint64_t dims[3] = {static_cast<uint64_t>(p.cols), static_cast<uint64_t>(p.M),
                               static_cast<uint64_t>(group == kSums ? p.E : 1)};

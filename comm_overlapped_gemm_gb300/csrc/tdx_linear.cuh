@@ -342,16 +342,46 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-// A warp's columns [begin, last) of a tile that are scaled, rounded and stored, perhaps with a row added (the residual,
-// or the output as it is), and nothing else, in boxes of 128-byte rows. 32 columns at a time (the accumulators behind `last` are read, not stored), values in
-// pairs, the next columns' residual on its way. The general loop takes four times the instructions: 8192 x 512 x 8192
-// 68 us with it, 57 with this one.
-template <bool F32, bool RES>
-__device__ __forceinline__ void lin_plain(const LinParams& p, float row_scale, const bf16* add, uint32_t d, bool none,
-                                          bool row_ok, int n0, int begin, int last, uint8_t* stage, int warp_row, int z) {
+// 32 columns' values of a row plus the bias of their columns, and to z where it is kept; `n` of the columns exist
+__device__ __forceinline__ void lin_bias_z(const LinParams& p, const LinRow& lr, int col, int n, bool row_ok, f32x2 (&v)[16]) {
+  if (p.bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (8 * i >= n) break;
+      f32x2 w[4];
+      unpack(*reinterpret_cast<const uint4*>(p.bias + col + 8 * i), w, bf16{});
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[4 * i + k] = add2(v[4 * i + k], w[k]);
+    }
+  }
+  if (p.z != nullptr && row_ok) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (16 * i >= n) break;
+      float f[16];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        f[2 * k] = first(v[8 * i + k]);
+        f[2 * k + 1] = second(v[8 * i + k]);
+      }
+      store_bf16(p.z + lr.z + col + 16 * i, f, 16 * i + 8 < n, p.wide_z);
+    }
+  }
+}
+
+// The short epilogues, over a warp's columns [begin, last) of a tile that go out in boxes of 128-byte rows: 32
+// columns at a time (the accumulators behind `last` are read, not stored), values in pairs. STEPS 0: scaled, perhaps with a
+// row added (RES: the residual, or the output as it is, on its way ahead of its use), rounded; 1: bias, z and an
+// approximate activation too; 2: SWIGLU, whose other half lies `other` columns on. The general loop takes some four
+// times the instructions: 8192 x 512 x 8192 68 us with it, 57 with STEPS 0; 8192 x 1024 x 8192 with bias and GELU_TANH 125
+// and 103 with 1, with SWIGLU 95 and 86 with 2.
+template <bool F32, bool RES, int STEPS>
+__device__ __forceinline__ void lin_short(const LinParams& p, const LinRow& lr, const bf16* add, uint32_t d, bool none,
+                                          bool row_ok, int n0, int begin, int last, uint8_t* stage, int warp_row, int z,
+                                          int other) {
   const int lane = threadIdx.x & 31;
   uint8_t* stage_row = stage + lane * 128;
-  const f32x2 scale = pair(row_scale, row_scale);
+  const f32x2 scale = pair(lr.scale, lr.scale);
   uint4 res[4];
   auto fetch = [&](int c) {
     const uint4* at = reinterpret_cast<const uint4*>(add + n0 + c);
@@ -359,19 +389,26 @@ __device__ __forceinline__ void lin_plain(const LinParams& p, float row_scale, c
     for (int i = 0; i < 4; ++i)
       if (row_ok && c + 8 * i < last) res[i] = at[i];
   };
-  if (RES) fetch(begin);
-#pragma unroll 1
-  for (int c = begin; c < last; c += 32) {
-    uint32_t r[32];
-    f32x2 v[16];
-    __syncwarp();
+  auto load = [&](uint32_t at, uint32_t (&r)[32]) {
     if (none) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) r[i] = 0u;
     } else {
-      tmem_ld_32x32b_x32(d + c, r);
-      tmem_ld_wait(r);
+      tmem_ld_32x32b_x32(at, r);
     }
+  };
+  if (RES) fetch(begin);
+#pragma unroll 1
+  for (int c = begin; c < last; c += 32) {
+    uint32_t r[32], q[32];
+    f32x2 v[16];
+    __syncwarp();
+    load(d + c, r);
+    if (STEPS == 2) {
+      load(d + other + c, q);
+      tmem_ld_wait(q);
+    }
+    tmem_ld_wait(r);
     const int in_box = F32 ? 0 : c & 32;
     if (in_box == 0) {
       if (lane == 0) bulk_wait_read_all();   // the staging's last store has been read
@@ -379,6 +416,19 @@ __device__ __forceinline__ void lin_plain(const LinParams& p, float row_scale, c
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = mul2(pair(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), scale);
+    if (STEPS > 0) {
+      lin_bias_z(p, lr, n0 + c, last - c, row_ok, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = act_pair(STEPS == 2 ? TDX_ACT_SILU : p.act, v[i]);
+    }
+    if (STEPS == 2) {
+      f32x2 u[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) u[i] = mul2(pair(__uint_as_float(q[2 * i]), __uint_as_float(q[2 * i + 1])), scale);
+      lin_bias_z(p, lr, p.cols + n0 + c, last - c, row_ok, u);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = mul2(v[i], u[i]);
+    }
     if (RES) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -392,14 +442,14 @@ __device__ __forceinline__ void lin_plain(const LinParams& p, float row_scale, c
     // 16-byte units of a row, permuted as the 128-byte swizzle has them
 #pragma unroll
     for (int i = 0; i < 16; i += F32 ? 2 : 4) {
-      uint4 q;
+      uint4 w;
       if (F32)
-        q = make_uint4(__float_as_uint(first(v[i])), __float_as_uint(second(v[i])), __float_as_uint(first(v[i + 1])),
+        w = make_uint4(__float_as_uint(first(v[i])), __float_as_uint(second(v[i])), __float_as_uint(first(v[i + 1])),
                        __float_as_uint(second(v[i + 1])));
       else
-        q = make_uint4(pack_bf16(first(v[i]), second(v[i])), pack_bf16(first(v[i + 1]), second(v[i + 1])),
+        w = make_uint4(pack_bf16(first(v[i]), second(v[i])), pack_bf16(first(v[i + 1]), second(v[i + 1])),
                        pack_bf16(first(v[i + 2]), second(v[i + 2])), pack_bf16(first(v[i + 3]), second(v[i + 3])));
-      st_shared_v4(stage_row, F32 ? i / 2 : in_box / 8 + i / 4, lane, q);
+      st_shared_v4(stage_row, F32 ? i / 2 : in_box / 8 + i / 4, lane, w);
     }
     if (F32 || in_box == 32 || c + 32 >= last) {
       fence_proxy_async_shared();
@@ -746,11 +796,20 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
       uint8_t* stage = staging + (warp - kEpiWarp0) * kStoreBytes;
       const bf16* add = LinSteps<FORM>::kResidual && p.residual != nullptr ? p.residual + lr.res : nullptr;
       if (LinSteps<FORM>::kAccumulate && p.accumulate) add = static_cast<const bf16*>(p.out) + lr.out;
-      if (box && p.plain && p.out_type == TDX_FP32 && (LinSteps<FORM>::kAccumulate || add == nullptr)) {
-        lin_plain<true, false>(p, lr.scale, nullptr, d, none, row_ok, n0, first, last, stage, warp_row, z);
-      } else if (box && p.plain && p.out_type == TDX_BF16) {
-        if (add != nullptr) lin_plain<false, true>(p, lr.scale, add, d, none, row_ok, n0, first, last, stage, warp_row, z);
-        else lin_plain<false, false>(p, lr.scale, add, d, none, row_ok, n0, first, last, stage, warp_row, z);
+      auto run = [&](auto f32, auto res, auto steps) {
+        lin_short<decltype(f32)::value, decltype(res)::value, decltype(steps)::value>(
+            p, lr, add, d, none, row_ok, n0, first, last, stage, warp_row, z, BN / 2);
+      };
+      using S0 = std::integral_constant<int, 0>;
+      if (box && p.steps == 0 && p.out_type == TDX_FP32 && (LinSteps<FORM>::kAccumulate || add == nullptr)) {
+        run(std::true_type{}, std::false_type{}, S0{});
+      } else if (box && p.steps == 0 && p.out_type == TDX_BF16) {
+        if (add != nullptr) run(std::false_type{}, std::true_type{}, S0{});
+        else run(std::false_type{}, std::false_type{}, S0{});
+      } else if (LinSteps<FORM>::kForward && !LONG && box && p.steps == 1 && add == nullptr) {
+        run(std::false_type{}, std::false_type{}, std::integral_constant<int, LinSteps<FORM>::kForward ? 1 : 0>{});
+      } else if (LinSteps<FORM>::kForward && !LONG && box && p.steps == 2 && add == nullptr) {
+        run(std::false_type{}, std::false_type{}, std::integral_constant<int, LinSteps<FORM>::kForward ? 2 : 0>{});
       } else
       // a rolled loop over 16 columns: unrolled over the tile its code came from L2 anew with every tile
 #pragma unroll 1

@@ -52,7 +52,7 @@ struct LinParams {
   int64_t out_step;         // kSums: elements between two experts' outputs
   int tma_out;              // output through tm_c (bf16 or fp32; whole 128-byte columns per warp)
   int wide, wide_z;         // output and z in 32-byte stores: 32-byte aligned rows
-  int plain;                // no bias, z nor activation: the short epilogue where tma_out is set
+  int steps;                // a short epilogue's (lin_short) where tma_out is set: 0, 1, 2, or -1 for none
   int overlap;
   uint32_t* status;
 };
