@@ -13,8 +13,9 @@
 // Roles (12 warps, one CTA per SM, persistent over tiles):
 //   warp 0 lane 0  TMA loads of 128-byte K slices into a ring of shared-memory slots
 //   warp 1 lane 0  tcgen05.mma into one of two accumulators; commits free slots, hand over accumulators
-//   warp 2         kSums: a run's last slice also holds rows of the next run; they are cleared in shared
-//                  memory, in both operands (0 times a foreign infinity would still be a NaN)
+//   warp 2         kSums: a run's last slice also holds rows of the next run (the tail); they are cleared in
+//                  shared memory, in both operands (0 times a foreign infinity would still be a NaN), in a slot
+//                  of its own that is loaded early in the tile: with tails in the ring every tile waited 1.4 us
 //   warps 4-11     epilogue: Tensor Memory -> registers -> output, while the next tile is multiplied
 //
 // Pairs (kPair): two CTAs run one 2-SM MMA stream on a 256 x 256 tile, each staging its 128 rows of A
@@ -36,6 +37,7 @@ namespace tdx {
 
 constexpr int kLinStages = 6;
 constexpr int kStoreBytes = 4096;   // an epilogue warp's staging: 32 rows of 128 bytes
+constexpr int kTailAfter = 8;       // whole slices of a tile that are loaded in front of its tail
 
 
 template <bool FP8, Form FORM, Group GROUP, bool PAIR>
@@ -57,21 +59,23 @@ struct LinCfg {
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int TM = PAIR ? 2 * kBM : kBM;      // rows of a tile
   static constexpr int TMEM_COLS = 2 * BN;
-  static constexpr int TABLE = GROUP == kFlat ? 0 : 2 * (kMoeMaxExperts + 1) + 2;   // ints
+  // run ends and, for kRows, tiles in front of each run
+  static constexpr int TABLE = GROUP == kFlat ? 0 : (GROUP == kRows ? 2 : 1) * (kMoeMaxExperts + 1) + 3;   // ints
   // staging for the output's TMA stores, but for the e4m3 kernel of single CTAs, whose slots are larger
   static constexpr int STORE = STAGE_BYTES > 32768 ? 0 : kNumEpiWarps * kStoreBytes;
-  static constexpr int OTHER = 1024 + STORE + 64 + TABLE * 4 + (3 * kLinStages + 5) * 8;
+  static constexpr int OTHER = STORE + 64 + TABLE * 4 + (2 * kLinStages + 8) * 8;
   static constexpr int FIT = (227 * 1024 - OTHER) / STAGE_BYTES;
-  static constexpr int STAGES = FIT < kLinStages ? FIT : kLinStages;
-  static constexpr int NUM_BARS = 3 * STAGES + 5;      // full, empty, tail per slot; accumulators; drain
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + STORE + NUM_BARS * 8 + 64 + TABLE * 4;
+  static constexpr int SLOTS = FIT < kLinStages ? FIT : kLinStages;
+  static constexpr int STAGES = GROUP == kSums ? SLOTS - 1 : SLOTS;   // of the ring; kSums: one slot is the tails'
+  static constexpr int NUM_BARS = 2 * STAGES + 8;      // full and empty per slot; accumulators; drain; tail
+  static constexpr int SMEM_BYTES = SLOTS * STAGE_BYTES + STORE + NUM_BARS * 8 + 64 + TABLE * 4;
   static constexpr int PART_LD = BN + 4;               // row pitch of a partial: 16 bytes past the banks' period
   static constexpr uint32_t IDESC = (1u << 4) | ((FP8 ? 0u : 1u) << 7) | ((FP8 ? 0u : 1u) << 10) |
                                     ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
                                     (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
   static_assert(!FP8 || FORM == NN, "e4m3 operands: the forward product only");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-  static_assert(PAIR || kBM * PART_LD * 4 <= STAGES * STAGE_BYTES, "a partial fits the ring");
+  static_assert(PAIR || kBM * PART_LD * 4 <= SLOTS * STAGE_BYTES, "a partial fits the slots");
 };
 
 // ------------------------------------------------------------------------------------ bounded waits
@@ -159,7 +163,7 @@ __device__ __forceinline__ LinTile lin_tile(const LinParams& p, const int* off, 
 }
 
 // One warp: the runs' ends as given, clamped to [0, rows] and never descending, and the count of tiles
-// (of tile_rows rows) in front of each run
+// (of tile_rows rows) in front of each run, where cum is not NULL
 __device__ __forceinline__ void lin_table(const int32_t* offsets, int E, int rows, int tile_rows, int* off, int* cum) {
   const int lane = threadIdx.x & 31;
   int32_t v[(kMoeMaxExperts + 32) / 32];
@@ -191,7 +195,7 @@ __device__ __forceinline__ void lin_table(const int32_t* offsets, int E, int row
     }
     if (e <= E) {
       off[e] = hi;
-      cum[e] = tiles + n;
+      if (cum != nullptr) cum[e] = tiles + n;
     }
     last = __shfl_sync(0xFFFFFFFFu, hi, 31);
     tiles += __shfl_sync(0xFFFFFFFFu, n, 31);
@@ -467,19 +471,20 @@ template <bool FP8, Form FORM, Group GROUP, bool PAIR, bool LONG>
 __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid_constant__ LinParams p) {
   using C = LinCfg<FP8, FORM, GROUP, PAIR>;
   constexpr int BN = C::BN;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];   // checked below: swizzled boxes lie on 1024-byte boundaries
   uint8_t* sA = smem;
-  uint8_t* sB = smem + C::STAGES * C::A_BYTES;
-  uint8_t* staging = smem + C::STAGES * C::STAGE_BYTES;
+  uint8_t* sB = smem + C::SLOTS * C::A_BYTES;
+  uint8_t* staging = smem + C::SLOTS * C::STAGE_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(staging + C::STORE);
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + C::NUM_BARS);   // [0] Tensor Memory base, [1] abort
   int* off = reinterpret_cast<int*>(misc + 16);
-  int* cum = off + kMoeMaxExperts + 1;
+  int* cum = GROUP == kRows ? off + kMoeMaxExperts + 1 : nullptr;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + C::STAGES), tail0 = smem_u32(bars + 2 * C::STAGES);
-  const uint32_t tfull0 = smem_u32(bars + 3 * C::STAGES), tempty0 = smem_u32(bars + 3 * C::STAGES + 2);
-  const uint32_t drain_bar = smem_u32(bars + 3 * C::STAGES + 4);
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + C::STAGES);
+  const uint32_t tfull0 = smem_u32(bars + 2 * C::STAGES), tempty0 = smem_u32(bars + 2 * C::STAGES + 2);
+  const uint32_t drain_bar = smem_u32(bars + 2 * C::STAGES + 4);
+  // the tail's slot: loads landed (leader: and the peer's slot cleared), cleared, multiplied
+  const uint32_t tail_in = smem_u32(bars + 2 * C::STAGES + 5), tail_full = tail_in + 8, tail_empty = tail_in + 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = PAIR ? 2 : p.split;   // CTAs per cluster
   const int crank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -489,8 +494,10 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
-      mbar_init(tail0 + 8 * s, PAIR && leader ? 2 : 1);   // its own loads; the peer's slice cleared
     }
+    mbar_init(tail_in, PAIR && leader ? 2 : 1);
+    mbar_init(tail_full, 1);
+    mbar_init(tail_empty, 1);
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
       mbar_init(tempty0 + 8 * a, PAIR ? 2 * kNumEpiWarps : kNumEpiWarps);
@@ -501,6 +508,10 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
     tma_prefetch_map(&p.tm_a);
     tma_prefetch_map(&p.tm_b);
     if (p.tma_out) tma_prefetch_map(&p.tm_c);
+  }
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0 && p.status != nullptr) *p.status = TDX_ERR_CUDA;
+    return;   // every CTA alike
   }
   if (warp == kMmaWarp) {
     if constexpr (PAIR) {
@@ -527,7 +538,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
   if (warp == kTmaWarp) {
     if (lane == 0) {
       int stage = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, tails = 0;   // parity of the tail slot's use
       bool stop = false;
       const uint64_t keep_a = policy_of(p.keep_a), keep_b = policy_of(p.keep_b);
       const uint32_t leader_full0 = PAIR ? mapa_shared(full0, 0) : full0;
@@ -551,72 +562,83 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
         const CUtensorMap* map_a = few ? &p.tm_few : &p.tm_a;
         const uint32_t bytes = few ? p.few_rows * 128 + C::B_BYTES : C::STAGE_BYTES;
         int k = t.k0 + t.kb0 * C::BK;
-        // One slice; a tail slice is counted on this CTA's own tail barrier. Two instances of the code: with the
-        // choice made per load in one loop, the loop and not the tensor cores set the pace (one run of 2048 rows, 2048 x
-        // 57344: 379 us against 272).
-        auto issue = [&](auto is_tail) {
-          constexpr bool kTail = decltype(is_tail)::value;
-          if (!lin_wait(p.status, empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
-            stop = true;
-            return;
-          }
-          const uint32_t own = (kTail ? tail0 : full0) + 8 * stage;
-          const uint32_t bar = PAIR && !kTail ? leader_full0 + 8 * stage : own;   // a pair's slices count on the leader's
-          if constexpr (!PAIR || kTail) mbar_arrive_expect_tx(own, bytes);
-          else if (leader) mbar_arrive_expect_tx(own, 2 * C::STAGE_BYTES);
-          const uint32_t a = a0 + stage * C::A_BYTES, b = b0 + stage * C::B_BYTES;
+        // The loads of slice kb into a slot. A tail is counted on this CTA's own barrier, a pair's other slices on
+        // the leader's. Two instances of the code: with the choice made per load in one loop, the loop and not the
+        // tensor cores set the pace (one run of 2048 rows, 2048 x 57344: 379 us against 272).
+        auto load = [&](auto is_tail, uint32_t bar, uint32_t a, uint32_t b, int k) {
+          constexpr bool kOwn = !PAIR || decltype(is_tail)::value;
           if constexpr (C::A_MN) {
 #pragma unroll
             for (int j = 0; j < C::A_BOXES; ++j) {
-              if constexpr (PAIR && !kTail)
-                tma_load_2d_pair_hint(a + j * C::BOX_BYTES, &p.tm_a, bar, t.m0 + j * C::BOX_N, k, keep_a);
-              else
-                tma_load_2d_hint(a + j * C::BOX_BYTES, &p.tm_a, bar, t.m0 + j * C::BOX_N, k, keep_a);
+              if constexpr (kOwn) tma_load_2d_hint(a + j * C::BOX_BYTES, &p.tm_a, bar, t.m0 + j * C::BOX_N, k, keep_a);
+              else tma_load_2d_pair_hint(a + j * C::BOX_BYTES, &p.tm_a, bar, t.m0 + j * C::BOX_N, k, keep_a);
             }
-          } else if constexpr (PAIR) {
-            tma_load_2d_pair_hint(a, &p.tm_a, bar, k, t.m0, keep_a);
-          } else {
+          } else if constexpr (kOwn) {
             tma_load_2d_hint(a, map_a, bar, k, t.m0, keep_a);
+          } else {
+            tma_load_2d_pair_hint(a, &p.tm_a, bar, k, t.m0, keep_a);
           }
 #pragma unroll
           for (int j = 0; j < C::B_BOXES; ++j) {
             const uint32_t dst = b + j * C::B_BOX_STEP;
             const int x = C::B_MN ? n[j] : k, y = C::B_MN ? k : n[j];
-            if constexpr (PAIR && !kTail) tma_load_3d_pair_hint(dst, &p.tm_b, bar, x, y, z, keep_b);
-            else tma_load_3d_hint(dst, &p.tm_b, bar, x, y, z, keep_b);
-          }
-          k += C::BK;
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
+            if constexpr (kOwn) tma_load_3d_hint(dst, &p.tm_b, bar, x, y, z, keep_b);
+            else tma_load_3d_pair_hint(dst, &p.tm_b, bar, x, y, z, keep_b);
           }
         };
         const bool tail = GROUP == kSums && t.kb1 > t.kb0 && t.kb1 * C::BK > t.klen;
         const int whole = tail ? t.kb1 - 1 : t.kb1;
-        for (int kb = t.kb0; kb < whole && !stop; ++kb) issue(std::false_type{});
+        // whole slices to the ring up to slice `to`
+        int kb = t.kb0;
+        auto ring = [&](int to) {
+          for (; kb < to && !stop; ++kb) {
+            if (!lin_wait(p.status, empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
+              stop = true;
+              return;
+            }
+            if constexpr (!PAIR) mbar_arrive_expect_tx(full0 + 8 * stage, bytes);
+            else if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * C::STAGE_BYTES);
+            load(std::false_type{}, leader_full0 + 8 * stage, a0 + stage * C::A_BYTES, b0 + stage * C::B_BYTES, k);
+            k += C::BK;
+            if (++stage == C::STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        };
         if constexpr (GROUP == kSums) {
-          if (tail && !stop) issue(std::true_type{});
+          if (tail) {
+            // The tail goes to a slot of its own early in the tile, so that it is cleared long before its turn at the
+            // end, but late enough that the last tile's tail has been multiplied.
+            ring(min(whole, t.kb0 + kTailAfter));
+            if (!stop && lin_wait(p.status, tail_empty, tails ^ 1u, abort_flag)) {
+              mbar_arrive_expect_tx(tail_in, C::STAGE_BYTES);
+              load(std::true_type{}, tail_in, a0 + C::STAGES * C::A_BYTES, b0 + C::STAGES * C::B_BYTES, t.k0 + whole * C::BK);
+              tails ^= 1u;
+            } else {
+              stop = true;
+            }
+          }
         }
+        ring(whole);
       }
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0 && leader) {
       int stage = 0, local = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, tails = 0;
       bool stop = false;
+      const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
       for (int it = cid; it < items && !stop; it += ncl, ++local) {
         const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, it, crank);
         int acc = local & 1;
         if (!lin_wait(p.status, tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, abort_flag)) break;
         tc_fence_after();
         uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
-        for (int kb = t.kb0; kb < t.kb1; ++kb) {
-          if (!lin_wait(p.status, full0 + 8 * stage, phase, abort_flag)) {
-            stop = true;
-            break;
-          }
+        // slice kb, once `full` is: into the accumulator, and its slot is free when that is done
+        auto multiply = [&](int kb, uint32_t full, uint32_t parity, uint32_t a, uint32_t b, uint32_t empty) {
+          if (!lin_wait(p.status, full, parity, abort_flag)) return false;
           tc_fence_after();
-          const uint32_t a = smem_u32(sA + stage * C::A_BYTES), b = smem_u32(sB + stage * C::B_BYTES);
           const int in_segment = LONG ? (kb - t.kb0) % kLinSegment : kb - t.kb0;
           if (LONG && in_segment == 0 && kb > t.kb0) {
             // the epilogue takes what is summed so far; on with the other accumulator
@@ -624,10 +646,7 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
             else tc_commit(tfull0 + 8 * acc);
             ++local;
             acc = local & 1;
-            if (!lin_wait(p.status, tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, abort_flag)) {
-              stop = true;
-              break;
-            }
+            if (!lin_wait(p.status, tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, abort_flag)) return false;
             tc_fence_after();
             d = tmem_base + static_cast<uint32_t>(acc * BN);
           }
@@ -646,11 +665,26 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
               else umma_bf16(d, ad, bd, C::IDESC, accum);
             }
           }
-          if constexpr (PAIR) tc_commit_pair_multicast(empty0 + 8 * stage, static_cast<uint16_t>(0x3));
-          else tc_commit(empty0 + 8 * stage);
+          if constexpr (PAIR) tc_commit_pair_multicast(empty, static_cast<uint16_t>(0x3));
+          else tc_commit(empty);
+          return true;
+        };
+        const bool tail = GROUP == kSums && t.kb1 > t.kb0 && t.kb1 * C::BK > t.klen;
+        const int whole = tail ? t.kb1 - 1 : t.kb1;
+        for (int kb = t.kb0; kb < whole; ++kb) {
+          if (!multiply(kb, full0 + 8 * stage, phase, a0 + stage * C::A_BYTES, b0 + stage * C::B_BYTES, empty0 + 8 * stage)) {
+            stop = true;
+            break;
+          }
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
+          }
+        }
+        if constexpr (GROUP == kSums) {
+          if (tail && !stop) {
+            stop = !multiply(whole, tail_full, tails, a0 + C::STAGES * C::A_BYTES, b0 + C::STAGES * C::B_BYTES, tail_empty);
+            tails ^= 1u;
           }
         }
         if (stop) break;
@@ -664,36 +698,33 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
       lin_wait(p.status, drain_bar, 0, &none);
     }
   } else if (GROUP == kSums && warp == kCopyWarp0) {
-    int slot = 0;           // of the next slice
-    uint32_t par = 0;       // parity each slot's tail barrier is waited for next
+    uint32_t tails = 0;
     for (int it = cid; it < items; it += ncl) {
       const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, it, crank);
-      const int n = t.kb1 - t.kb0, valid = t.klen - (t.kb1 - 1) * C::BK;
-      slot = (slot + n) % C::STAGES;
-      if (n == 0 || valid >= C::BK) continue;
-      const int s = slot == 0 ? C::STAGES - 1 : slot - 1;
-      const bool ok = lin_wait(p.status, tail0 + 8 * s, (par >> s) & 1u, abort_flag);
+      const int valid = t.klen - (t.kb1 - 1) * C::BK;
+      if (t.kb1 == t.kb0 || valid >= C::BK) continue;
+      const bool ok = lin_wait(p.status, tail_in, tails, abort_flag);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      par ^= 1u << s;
+      tails ^= 1u;
       // a K row is one 128-byte line of every box (the swizzle permutes 16-byte units inside a line)
       const int units = (C::BK - valid) * 8;
       for (int i = lane; i < units; i += 32) {
         const int at = valid * 128 + i * 16;
 #pragma unroll
         for (int j = 0; j < C::A_BOXES; ++j)
-          *reinterpret_cast<uint4*>(sA + s * C::A_BYTES + j * C::BOX_BYTES + at) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(sA + C::STAGES * C::A_BYTES + j * C::BOX_BYTES + at) = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int j = 0; j < C::B_BOXES; ++j)
-          *reinterpret_cast<uint4*>(sB + s * C::B_BYTES + j * C::BOX_BYTES + at) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(sB + C::STAGES * C::B_BYTES + j * C::BOX_BYTES + at) = make_uint4(0u, 0u, 0u, 0u);
       }
       fence_proxy_async_shared();
       __syncwarp();
-      // the second CTA of a pair tells the leader, whose arrival (after both) releases the slice. (Two
-      // arrivals on every slice's barrier, one of them remote, cost 1 us a slice: 1583 us for 32749 rows of 2048
-      // and 7168 columns over 16 experts.)
+      // The second CTA of a pair tells the leader, whose arrival (after both) releases the slice. (Two arrivals on
+      // every slice's barrier, one of them remote, cost 1 us a slice: 1583 us for 32749 rows of 2048 and 7168
+      // columns over 16 experts.)
       if (lane == 0) {
-        if (leader) mbar_arrive(full0 + 8 * s);
-        else mbar_arrive_cluster(mapa_shared(tail0 + 8 * s, 0));
+        if (leader) mbar_arrive(tail_full);
+        else mbar_arrive_cluster(mapa_shared(tail_in, 0));
       }
     }
   } else if (warp >= kEpiWarp0) {

@@ -358,7 +358,7 @@ GROUPS = [
     ([1, 1, 1, 1, 1, 1, 1, 1], 0, 0, 1024, 256), ([64, 128, 0, 63, 65, 1], 2, 1, 264, 120),
     ([300, 0, 129, 1, 255, 257, 64], 0, 5, 136, 1032), ([2000, 100, 1900], 0, 0, 256, 512),
     ([700, 0, 513, 800, 127, 1, 1500, 256], 7, 9, 512, 2048), ([0, 0], 0, 4, 64, 64),
-    ([3] * 100, 0, 0, 64, 72), ([1, 0] * 256, 0, 0, 64, 64)]
+    ([3] * 100, 0, 0, 64, 72), ([1, 0] * 256, 0, 0, 64, 64), ([130, 1, 65, 0, 64, 63, 600] * 6, 0, 2, 512, 2048)]
 
 
 @pytest.mark.parametrize("counts,first,behind,K,N", GROUPS)
