@@ -26,12 +26,6 @@ struct ActParams {
   float inv_scale;
 };
 
-// i / d as the high half of i * ceil(2^64 / d): exact as long as i * (the product of d and that - 2^64) < 2^64,
-// that is i < 2^37 for d up to 2^27
-uint64_t magic_of(int d) { return d == 1 ? 0 : ~UINT64_C(0) / d + 1; }
-__device__ __forceinline__ int64_t divide(int64_t i, uint64_t magic) {
-  return magic != 0 ? static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(i), magic)) : i;
-}
 // The call's i-th vector: its row (dest not applied) and first column
 template <int N>
 __device__ __forceinline__ int64_t place(const ActParams& p, int64_t i, int* c) {

@@ -68,7 +68,9 @@ __device__ __forceinline__ void act_backward(f32x2& dy, f32x2 x, f32x2& u) {
 
 // Bound by HBM. A warp reads whole lines of a row (several rows where a row is short), a thread keeps the
 // sums of its 8 columns (16 for SWIGLU) in registers over its rows; they are joined in shared memory
-// in a fixed order.
+// in a fixed order. 16381 x 8192 GELU_TANH with dbias 128 us (6.3 TB/s), SWIGLU 111. Blocks with chunks of
+// neighbouring rows, each reading a front of its own, took 136; the next rows' loads in front of the present ones' work
+// 139 to 158 (more rows in flight, fewer hits of open DRAM pages); 4 blocks of 64 registers per SM 140.
 template <int ACT>
 __global__ void __launch_bounds__(kThreads) tdx_linear_act_bwd_kernel(const __grid_constant__ ActBwdParams p) {
   constexpr bool kGated = ACT == TDX_ACT_SWIGLU;

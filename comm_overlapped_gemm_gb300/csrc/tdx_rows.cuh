@@ -147,6 +147,13 @@ __device__ __forceinline__ float lanes_max_abs(float v) {
 __device__ __forceinline__ float warp_sum(float v) { return lanes_sum<32>(v); }
 __device__ __forceinline__ float warp_max(float v) { return lanes_max<32>(v); }
 
+// i / d as the high half of i * ceil(2^64 / d): exact as long as i * (the product of d and that - 2^64) < 2^64,
+// that is i < 2^37 for d up to 2^27
+inline uint64_t magic_of(int d) { return d == 1 ? 0 : ~UINT64_C(0) / d + 1; }
+__device__ __forceinline__ int64_t divide(int64_t i, uint64_t magic) {
+  return magic != 0 ? static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(i), magic)) : i;
+}
+
 // ------------------------------------------------------------------------------------ host side
 // Launch with programmatic dependent launch: the grid may be scheduled before the stream's previous
 // kernel has ended, and every kernel here calls griddep_wait before it touches global memory.

@@ -42,7 +42,9 @@ def inputs(T, H, k, dtype, seed, spare=3, pad=0):
     return R, Z, dest, gates, dout
 
 
-CASES = [(1, 8, 1), (1, 7168, 8), (2, 16, 3), (33, 64, 16), (200, 1000, 8), (1000, 264, 2), (77, 4104, 9), (5, 20000, 4)]
+# the last ones are large enough for several vectors a thread
+CASES = [(1, 8, 1), (1, 7168, 8), (2, 16, 3), (33, 64, 16), (200, 1000, 8), (1000, 264, 2), (77, 4104, 9), (5, 20000, 4), (2501, 1000, 2),
+         (1301, 2056, 4)]
 
 
 @pytest.mark.parametrize("T,H,k", CASES)
