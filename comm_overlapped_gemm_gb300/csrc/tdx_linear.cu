@@ -51,7 +51,7 @@ struct Shape {
 // bytes of K) of a pair's and of a single CTA's tile; a persistent kernel's last epilogue; the addition of a tile's
 // partials, once and for each 128 rows of each CTA; what a second wave of clusters adds.
 constexpr float kLaunch = 5.0f, kPairSlice = 0.30f, kSingleSlice = 0.27f, kSingleSliceE4m3 = 0.33f;
-constexpr float kPairEnd = 1.5f, kSingleEnd = 1.0f, kFold = 2.2f, kFoldRows = 1.8f, kFoldRowsCta = 0.5f, kWave = 3.0f;
+constexpr float kPairEnd = 1.5f, kSingleEnd = 1.0f, kFold = 2.2f, kFoldRows = 1.8f, kFoldRowsCta = 0.7f, kWave = 3.0f;
 
 Shape choose(bool fp8, int64_t tiles256, int64_t tiles1, int64_t most1, int nkb, float rows) {
   const int sms = sm_count() > 0 ? sm_count() : kRefSMs;
@@ -59,7 +59,7 @@ Shape choose(bool fp8, int64_t tiles256, int64_t tiles1, int64_t most1, int nkb,
   Shape best = {true, 1};
   float t = kLaunch + waves(tiles256, sms / 2) * nkb * kPairSlice + kPairEnd;
   const float slice = fp8 ? kSingleSliceE4m3 : kSingleSlice;
-  for (int s = 1; s <= 8; s *= 2) {
+  for (int s = 1; s <= kMostSplit; ++s) {
     if (s > 1 && (s > nkb || most1 * s > 4 * sms)) break;
     float one = kLaunch + waves(tiles1, sms) * nkb * slice + kSingleEnd;
     if (s > 1) {

@@ -12,6 +12,7 @@ enum Form { NN, NT, TN };                 // see tdx_linear.cuh
 enum Group { kFlat, kRows, kSums };
 constexpr uint64_t kLinTimeoutNs = 4000000000ull;
 constexpr int kLinSegment = 14;   // K slices summed on the tensor cores alone, for fp32 results
+constexpr int kMostSplit = 8;    // CTAs of a cluster that share a tile, the portable limit
 constexpr int kFewRows = 16;   // most rows of the small boxes of A
 
 // Tile columns: pairs 256. Single CTAs 128, and 256 for e4m3, whose 128-column boxes would not split
@@ -63,7 +64,7 @@ using LinLaunch = tdx_status(Group g, bool pair, const LinParams& p, int want, c
 LinLaunch launch_linear_nn, launch_linear_nt, launch_linear_tn, launch_linear_e4m3;
 LinLaunch launch_linear_nn_long, launch_linear_nt_long, launch_linear_tn_long, launch_linear_e4m3_long;
 
-// Clusters of `split` single CTAs that are resident together on the current device (2, 4 or 8)
+// Clusters of `split` single CTAs (2 .. kMostSplit) that are resident together on the current device
 int lin_clusters(int split);
 
 }  // namespace tdx

@@ -4,12 +4,11 @@
 namespace tdx {
 
 int lin_clusters(int split) {
-  static std::atomic<int> cache[64][4];
-  const int at = split == 2 ? 1 : split == 4 ? 2 : 3;
-  const int guess = split == 2 ? 72 : split == 4 ? 32 : 14;   // where it cannot be asked
+  static std::atomic<int> cache[64][kMostSplit + 1];
+  const int guess = 16 / split * 8;   // where it cannot be asked: 8 groups of 16 SMs
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return guess;
-  const int known = cache[dev][at].load(std::memory_order_relaxed);
+  const int known = cache[dev][split].load(std::memory_order_relaxed);
   if (known > 0) return known;
   using C = LinCfg<false, NN, kFlat, false>;
   auto* kernel = tdx_linear_kernel<false, NN, kFlat, false, false>;
@@ -28,7 +27,7 @@ int lin_clusters(int split) {
   cfg.numAttrs = 1;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) return guess;
-  cache[dev][at].store(n, std::memory_order_relaxed);
+  cache[dev][split].store(n, std::memory_order_relaxed);
   return n;
 }
 
