@@ -262,3 +262,62 @@ def test_offsets_past_32_bits():
     tdx.check(tdx.tdx_grouped_gemm_bwd(dY, X, off_, W, None, dW, R, K, N, E, 0))
     assert torch.equal(dW[E - 1].double(), (X[100:].double().t() @ dY[100:].double()).to(BF).double())
     assert bool((dW[5] == 0).all()) and bool((dW[E - 2] == 0).all())
+
+
+FIRST_CALLS = """
+import torch
+import comm_overlapped_gemm_gb300 as tdx
+def rn(*s): return torch.randn(*s, device="cuda", dtype=torch.bfloat16)
+A, B, x, W, big = rn(300, 512), rn(512, 1024), rn(1, 8192), rn(8192, 2048), rn(2048, 2048)
+C, y, out, dA, dB = rn(300, 1024), rn(1, 2048), rn(2048, 2048), torch.empty_like(A), torch.empty_like(B)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    tdx.check(tdx.tdx_linear(A, B, None, None, None, C, None, 300, 512, 1024, 0))
+    tdx.check(tdx.tdx_linear_bwd(C, A, B, None, dA, dB, 300, 512, 1024, 0))
+    tdx.check(tdx.tdx_linear(x, W, None, None, None, y, None, 1, 8192, 2048, 0))      # clusters
+    tdx.check(tdx.tdx_linear(big, big, None, None, None, out, None, 2048, 2048, 2048, 0))   # pairs
+g.replay()
+torch.cuda.synchronize()
+for got, want in ((C, A.double() @ B.double()), (dA, C.double() @ B.double().t()), (dB, A.double().t() @ C.double()),
+                  (y, x.double() @ W.double()), (out, big.double() @ big.double())):
+    assert float((got.double() - want).norm() / want.norm()) <= 2.0 ** -8
+"""
+
+
+def test_first_calls_of_a_process_under_capture():
+    """Kernels' limits and the clusters that fit are asked for at the first call, which may be a captured one."""
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_two_threads():
+    import threading
+    blocks = [Dense(300, 256, 1024, seed=7), Dense(170, 512, 512, seed=8)]
+    want = []
+    for b in blocks:
+        b.run()
+        want.append([t.clone() for t in b.results()])
+        b.wipe()
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(b):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    b.run()
+        except Exception as e:   # noqa: BLE001  (reported below, in the test's own thread)
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(b,)) for b in blocks]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad
+    for b, w in zip(blocks, want):
+        assert all(torch.equal(x, y) for x, y in zip(b.results(), w))
