@@ -545,8 +545,8 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
       const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
       for (int it = cid; it < items && !stop; it += ncl) {
         const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, it, crank);
-        // What stays the same over the tile's slices: this thread's pace is what small tiles wait for (a slice took
-        // it 296 cycles, and 568 with a loop over boxes of few rows).
+        // What stays the same over the tile's slices: this thread's pace is what small tiles wait for (a slice takes
+        // it 240 cycles; with this inside 296, with a loop over boxes of few rows 568).
         const int n0 = t.nt * (LinSteps<FORM>::kForward && p.gated ? BN / 2 : BN);
         int n[C::B_BOXES];   // first columns of the boxes of B (SWIGLU: gate columns, then the other half's)
 #pragma unroll
