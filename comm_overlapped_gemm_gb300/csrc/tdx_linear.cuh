@@ -754,7 +754,10 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
         const int segments = (t.kb1 - t.kb0 + kLinSegment - 1) / kLinSegment;
         if (segments > 1) {
           float sum[BN / 2];
-          const int base = p.gated ? half * (BN / 4) : half * (BN / 2), skip = p.gated ? BN / 4 : 0;
+          // The columns that this warp reads again below, as its own stores alone are ordered before its loads: of a
+          // gated tile a quarter of the gates and the same of the other half; of a cluster's partial its half.
+          const bool apart = p.gated && (PAIR || S == 1);
+          const int base = apart ? half * (BN / 4) : half * (BN / 2), skip = apart ? BN / 4 : 0;
 #pragma unroll 1
           for (int g = 0; g < segments && ok; ++g, local += g < segments) {
             ok = __all_sync(0xFFFFFFFFu, lin_wait(p.status, tfull0 + 8 * (local & 1), (local >> 1) & 1, abort_flag));
