@@ -252,7 +252,8 @@ tdx_status tdx_moe_combine(const void* Z, const int32_t* dest, const float* gate
   CombineParams p;
   const tdx_status s = combine_params(R, T, H, topk, dtype, o.out_dtype, o, &p);
   if (s != TDX_OK) return s;
-  if (Z == nullptr || dest == nullptr || out == nullptr) return TDX_ERR_INVALID_ARG;
+  // tensors of no rows (Z: R = 0, the others: T = 0) have no address
+  if ((R > 0 && Z == nullptr) || (T > 0 && (dest == nullptr || out == nullptr))) return TDX_ERR_INVALID_ARG;
   if (!aligned(Z, 16) || !aligned(out, 16) || !aligned(dest, 4) || !aligned(gates, 4)) return TDX_ERR_ALIGNMENT;
   if (T == 0) return TDX_OK;
   p.z = Z;
@@ -271,7 +272,9 @@ tdx_status tdx_moe_combine_bwd(const void* dout, const void* Z, const int32_t* d
   CombineParams p;
   const tdx_status s = combine_params(R, T, H, topk, dtype, dtype, o, &p);
   if (s != TDX_OK) return s;
-  if (dout == nullptr || dest == nullptr || (dZ == nullptr && dgates == nullptr) || (dgates != nullptr && Z == nullptr))
+  // tensors of no rows (Z and dZ: R = 0, the others: T = 0) have no address
+  if (T > 0 && (dout == nullptr || dest == nullptr || (R > 0 && dZ == nullptr && dgates == nullptr) ||
+                (R > 0 && dgates != nullptr && Z == nullptr)))
     return TDX_ERR_INVALID_ARG;
   if (!aligned(dout, 16) || !aligned(Z, 16) || !aligned(dZ, 16) || !aligned(dest, 4) || !aligned(gates, 4) ||
       !aligned(dgates, 4))

@@ -154,7 +154,8 @@ tdx_status forward(const void* A, const int32_t* offsets, const void* B, const v
                    tdx_dtype dtype, const tdx_linear_opts* opts, void* stream) {
   const tdx_linear_opts o = opts ? *opts : linear_defaults();
   if (M < 0 || K <= 0 || N <= 0 || !known(dtype) || !known(o.out_dtype) || !act_known(o.act)) return TDX_ERR_INVALID_ARG;
-  if (A == nullptr || B == nullptr || C == nullptr || !std::isfinite(o.alpha) || !usable_scale(o.out_scale))
+  // tensors of M = 0 rows have no address
+  if (B == nullptr || (M > 0 && (A == nullptr || C == nullptr)) || !std::isfinite(o.alpha) || !usable_scale(o.out_scale))
     return TDX_ERR_INVALID_ARG;
   const bool gated = o.act == TDX_ACT_SWIGLU, fp8 = dtype == TDX_FP8_E4M3;
   if (gated && N % 2 != 0) return TDX_ERR_INVALID_ARG;
@@ -204,9 +205,12 @@ tdx_status backward(const void* dz, const void* A, const int32_t* offsets, const
   const tdx_linear_opts o = opts ? *opts : linear_defaults();
   if (M < 0 || K <= 0 || N <= 0 || !known(dtype) || !known(o.out_dtype) || !known(o.dw_dtype) || !act_known(o.act))
     return TDX_ERR_INVALID_ARG;
-  if (dz == nullptr || (dA == nullptr && dB == nullptr) || (dA != nullptr && B == nullptr) ||
-      (dB != nullptr && A == nullptr) || (dres != nullptr && dA == nullptr) || o.act != TDX_ACT_NONE ||
-      !std::isfinite(o.alpha) || o.accumulate < 0 || o.accumulate > 1)
+  if ((dA != nullptr && B == nullptr) || o.act != TDX_ACT_NONE || !std::isfinite(o.alpha) || o.accumulate < 0 ||
+      o.accumulate > 1)
+    return TDX_ERR_INVALID_ARG;
+  // tensors of M = 0 rows have no address
+  if (M > 0 && (dz == nullptr || (dA == nullptr && dB == nullptr) || (dB != nullptr && A == nullptr) ||
+                (dres != nullptr && dA == nullptr)))
     return TDX_ERR_INVALID_ARG;
   if (dtype != TDX_BF16 || o.out_dtype == TDX_FP8_E4M3 || o.dw_dtype == TDX_FP8_E4M3 || M > kMostSize ||
       K > kMostSize || N > kMostSize)
@@ -258,7 +262,10 @@ tdx_status backward(const void* dz, const void* A, const int32_t* offsets, const
     q.out_type = o.dw_dtype;
     q.accumulate = o.accumulate;
     q.overlap = both ? kOverlapSecond : kOverlapNone;
-    return run(TN, E > 0 ? kSums : kFlat, false, q, {A, M, K, ld_a, 0, 1}, {dz, M, N, ld_z, 0, 1}, st);
+    // without rows nothing is loaded; the maps want an address all the same
+    const void* rows_a = M > 0 ? A : dB;
+    const void* rows_z = M > 0 ? dz : dB;
+    return run(TN, E > 0 ? kSums : kFlat, false, q, {rows_a, M, K, ld_a, 0, 1}, {rows_z, M, N, ld_z, 0, 1}, st);
   }
   return TDX_OK;
 }

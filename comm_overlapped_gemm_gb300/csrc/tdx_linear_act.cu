@@ -202,7 +202,8 @@ tdx_status tdx_linear_act_bwd(const void* dy, const void* z, void* dz, float* db
   tdx_status s = tdx_linear_act_bwd_workspace_size(M, N, dtype, &o, &need);
   if (s != TDX_OK) return s;
   const bool gated = o.act == TDX_ACT_SWIGLU;
-  if (dy == nullptr || (dz == nullptr && dbias == nullptr) || (o.act != TDX_ACT_NONE && z == nullptr))
+  // tensors of M = 0 rows have no address
+  if (M > 0 && (dy == nullptr || (dz == nullptr && dbias == nullptr) || (o.act != TDX_ACT_NONE && z == nullptr)))
     return TDX_ERR_INVALID_ARG;
   ActBwdParams p;
   std::memset(&p, 0, sizeof(p));

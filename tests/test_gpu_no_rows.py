@@ -1,0 +1,69 @@
+"""GPU tests of calls whose row tensors are empty: what the formulas leave is zeroed, nothing else is written."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import comm_overlapped_gemm_gb300 as tdx
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def empty(*shape, dtype=BF):
+    t = torch.empty(*shape, dtype=dtype, device="cuda")
+    assert t.data_ptr() == 0
+    return t
+
+
+def full(*shape, dtype=F32):
+    return torch.full(shape, 3.0, dtype=dtype, device="cuda")
+
+
+@pytest.mark.parametrize("dw", [F32, BF])
+@pytest.mark.parametrize("acc", [0, 1])
+@pytest.mark.parametrize("K,N", [(64, 128), (2048, 4096)])
+def test_weight_gradients(dw, acc, K, N):
+    o = tdx.make_linear_opts(dw_dtype=tdx.TDX_FP32 if dw == F32 else tdx.TDX_BF16, accumulate=acc)
+    want = 3.0 if acc else 0.0
+    dB, B = full(K, N, dtype=dw), full(K, N, dtype=BF)
+    tdx.check(tdx.tdx_linear_bwd(empty(0, N), empty(0, K), B, empty(0, K), empty(0, K), dB, 0, K, N, 0, o))
+    assert bool((dB == want).all())
+    dB, B, off = full(3, K, N, dtype=dw), full(3, K, N, dtype=BF), torch.zeros(4, dtype=torch.int32, device="cuda")
+    tdx.check(tdx.tdx_grouped_gemm_bwd(empty(0, N), empty(0, K), off, B, empty(0, K), dB, 0, K, N, 3, 0, o))
+    assert bool((dB == want).all())
+
+
+@pytest.mark.parametrize("act", range(6))
+def test_bias_gradient(act):
+    cols = 64 if act == 5 else 128
+    o, db = tdx.make_linear_opts(act=act), full(128)
+    ws = torch.empty(tdx.tdx_linear_act_bwd_workspace_size(0, 128, 0, o), dtype=torch.uint8, device="cuda")
+    tdx.check(tdx.tdx_linear_act_bwd(empty(0, cols), empty(0, 128), empty(0, 128), db, ws, 0, 128, 0, o))
+    assert bool((db == 0).all())
+
+
+def test_forward_products():
+    B = full(2, 64, 128, dtype=BF)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    tdx.check(tdx.tdx_linear(empty(0, 64), B, None, empty(0, 128), empty(0, dtype=F32), empty(0, 128), empty(0, 128), 0,
+                             64, 128, 0))
+    tdx.check(tdx.tdx_grouped_gemm(empty(0, 64), off, B, empty(0, dtype=F32), None, empty(0, 128), None, 0, 64, 128, 2, 0))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_combine(dtype):
+    code = tdx.TDX_BF16 if dtype == BF else tdx.TDX_FP32
+    T, H, k = 5, 64, 2
+    dest, gates = torch.zeros(T, k, dtype=torch.int32, device="cuda"), full(T, k)
+    out, dg, Z = full(T, H, dtype=BF), full(T, k), empty(0, H, dtype=dtype)
+    tdx.check(tdx.tdx_moe_combine(Z, dest, gates, out, 0, T, H, k, code))
+    assert bool((out == 0).all())
+    dout = full(T, H, dtype=dtype)
+    tdx.check(tdx.tdx_moe_combine_bwd(dout, Z, dest, gates, empty(0, H, dtype=dtype), dg, 0, T, H, k, code))
+    assert bool((dg == 0).all())
+    none, Z = torch.empty(0, k, dtype=torch.int32, device="cuda"), full(4, H, dtype=dtype)
+    tdx.check(tdx.tdx_moe_combine(Z, none, empty(0, k, dtype=F32), empty(0, H), 4, 0, H, k, code))
+    tdx.check(tdx.tdx_moe_combine_bwd(empty(0, H, dtype=dtype), Z, none, None, Z, empty(0, k, dtype=F32), 4, 0, H, k, code))
+    assert bool((Z == 3).all())
