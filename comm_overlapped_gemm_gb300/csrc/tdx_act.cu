@@ -232,8 +232,10 @@ tdx_status tdx_swiglu(const void* y, void* out, const float* row_scale, const in
   ActParams p;
   const tdx_status s = act_params(R, I, dtype, o.out_dtype, o, &p);
   if (s != TDX_OK) return s;
-  if (y == nullptr || out == nullptr || !usable_scale(o.out_scale) || o.topk < 0) return TDX_ERR_INVALID_ARG;
-  if ((o.topk > 0) != (dest != nullptr) || (o.topk > 0 && (R % o.topk != 0 || row_scale == nullptr)))
+  if (!usable_scale(o.out_scale) || o.topk < 0 || (o.topk > 0 && R % o.topk != 0)) return TDX_ERR_INVALID_ARG;
+  // tensors of R = 0 rows have no address
+  if (R > 0 && (y == nullptr || out == nullptr || (o.topk > 0) != (dest != nullptr) ||
+                (o.topk > 0 && row_scale == nullptr)))
     return TDX_ERR_INVALID_ARG;
   if (!aligned(y, 16) || !aligned(out, 16) || !aligned(row_scale, 4) || !aligned(dest, 4)) return TDX_ERR_ALIGNMENT;
   if (R == 0) return TDX_OK;
@@ -253,7 +255,8 @@ tdx_status tdx_swiglu_bwd(const void* y, const void* dout, void* dy, int R, int 
   ActParams p;
   const tdx_status s = act_params(R, I, dtype, dtype, o, &p);
   if (s != TDX_OK) return s;
-  if (y == nullptr || dout == nullptr || dy == nullptr) return TDX_ERR_INVALID_ARG;
+  // tensors of R = 0 rows have no address
+  if (R > 0 && (y == nullptr || dout == nullptr || dy == nullptr)) return TDX_ERR_INVALID_ARG;
   if (!aligned(y, 16) || !aligned(dout, 16) || !aligned(dy, 16)) return TDX_ERR_ALIGNMENT;
   if (R == 0) return TDX_OK;
   p.y = y;

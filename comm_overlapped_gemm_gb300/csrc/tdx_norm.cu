@@ -680,7 +680,8 @@ tdx_status tdx_rmsnorm(const void* x, const void* residual, const void* weight, 
   const tdx_norm_opts o = opts ? *opts : norm_defaults();
   tdx_status s = check_sizes(T, H, dtype);
   if (s != TDX_OK) return s;
-  if (x == nullptr || weight == nullptr || y == nullptr || (h_out != nullptr && residual == nullptr))
+  // tensors of T = 0 rows have no address
+  if (weight == nullptr || (T > 0 && (x == nullptr || y == nullptr || (h_out != nullptr && residual == nullptr))))
     return TDX_ERR_INVALID_ARG;
   if (!known(o.out_dtype) || !(o.eps >= 0.0f) || !std::isfinite(o.eps) || !usable_scale(o.out_scale))
     return TDX_ERR_INVALID_ARG;
@@ -729,7 +730,9 @@ tdx_status tdx_rmsnorm_bwd(const void* dy, const void* h, const void* weight, co
   size_t need = 0;
   tdx_status s = tdx_rmsnorm_bwd_workspace_size(T, H, dtype, &need);
   if (s != TDX_OK) return s;
-  if (dy == nullptr || h == nullptr || weight == nullptr || rstd == nullptr || dx == nullptr || dweight == nullptr)
+  // tensors of T = 0 rows have no address
+  if (weight == nullptr || dweight == nullptr ||
+      (T > 0 && (dy == nullptr || h == nullptr || rstd == nullptr || dx == nullptr)))
     return TDX_ERR_INVALID_ARG;
   NormBwdParams p;
   std::memset(&p, 0, sizeof(p));

@@ -942,7 +942,8 @@ tdx_status tdx_moe_route(const void* logits, const float* bias, int32_t* topk_id
   RouteParams p;
   const tdx_status s = route_params(T, E, topk, dtype, o, &p);
   if (s != TDX_OK) return s;
-  if (logits == nullptr || topk_idx == nullptr || gates == nullptr) return TDX_ERR_INVALID_ARG;
+  // tensors of T = 0 rows have no address
+  if (T > 0 && (logits == nullptr || topk_idx == nullptr || gates == nullptr)) return TDX_ERR_INVALID_ARG;
   if (static_cast<int64_t>(topk) > static_cast<int64_t>(o.topk_group) * (E / o.n_group)) return TDX_ERR_INVALID_ARG;
   if (!aligned(logits, static_cast<unsigned>(bytes_of(dtype))) || !aligned(bias, 4) || !aligned(topk_idx, 4) ||
       !aligned(gates, 4) || !aligned(counts, 4))
@@ -963,7 +964,9 @@ tdx_status tdx_moe_route_bwd(const void* logits, const int32_t* topk_idx, const 
   RouteParams p;
   const tdx_status s = route_params(T, E, topk, dtype, o, &p);
   if (s != TDX_OK) return s;
-  if (logits == nullptr || topk_idx == nullptr || dgates == nullptr || dlogits == nullptr) return TDX_ERR_INVALID_ARG;
+  // tensors of T = 0 rows have no address
+  if (T > 0 && (logits == nullptr || topk_idx == nullptr || dgates == nullptr || dlogits == nullptr))
+    return TDX_ERR_INVALID_ARG;
   const unsigned elt = static_cast<unsigned>(bytes_of(dtype));
   if (!aligned(logits, elt) || !aligned(dlogits, elt) || !aligned(topk_idx, 4) || !aligned(dgates, 4))
     return TDX_ERR_ALIGNMENT;

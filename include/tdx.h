@@ -332,10 +332,10 @@ tdx_status tdx_moe_combine_plan_info(int W, int T, int F, int H, int E, int topk
  * e4m3 codes are those of the value times its scale's fp32 reciprocal, not of an exact quotient: a
  * value within the arithmetic's own rounding of the middle between two codes may take either.
  * Except tdx_rmsnorm_bwd they need no workspace, and they record nothing in a device status word: ids
- * and indexes read on the device are bounds-checked there. Rows of 0 elements are invalid; 0 rows launch nothing (tdx_rmsnorm_bwd still zeroes
- * dweight). Row strides are in elements, 0 = dense; a stride below the row's length is
- * TDX_ERR_INVALID_ARG. Unless said otherwise pointers are 16-byte aligned and rows and strides are
- * multiples of 16 bytes (TDX_ERR_ALIGNMENT).
+ * and indexes read on the device are bounds-checked there. Rows of 0 elements are invalid; 0 rows
+ * launch nothing (tdx_rmsnorm_bwd still zeroes dweight), and their tensors may be NULL. Row strides are
+ * in elements, 0 = dense; a stride below the row's length is TDX_ERR_INVALID_ARG. Unless said otherwise
+ * pointers are 16-byte aligned and rows and strides are multiples of 16 bytes (TDX_ERR_ALIGNMENT).
  *
  * Root-mean-square norm of x + residual:
  *   h = x + residual (x alone if residual is NULL), rstd = 1 / sqrt(mean(h^2) + eps),

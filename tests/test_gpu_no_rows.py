@@ -67,3 +67,12 @@ def test_combine(dtype):
     tdx.check(tdx.tdx_moe_combine(Z, none, empty(0, k, dtype=F32), empty(0, H), 4, 0, H, k, code))
     tdx.check(tdx.tdx_moe_combine_bwd(empty(0, H, dtype=dtype), Z, none, None, Z, empty(0, k, dtype=F32), 4, 0, H, k, code))
     assert bool((Z == 3).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_gradient(dtype):
+    code, H = tdx.TDX_BF16 if dtype == BF else tdx.TDX_FP32, 64
+    e, dw = empty(0, H, dtype=dtype), full(H)
+    ws = torch.empty(tdx.tdx_rmsnorm_bwd_workspace_size(0, H, code), dtype=torch.uint8, device="cuda")
+    tdx.check(tdx.tdx_rmsnorm_bwd(e, e, full(H, dtype=dtype), empty(0, dtype=F32), e, e, dw, ws, 0, H, code))
+    assert bool((dw == 0).all())

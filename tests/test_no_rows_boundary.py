@@ -37,3 +37,15 @@ def test_combine(tdx):
     assert tdx.tdx_moe_combine_bwd(0, FAKE, 0, 0, FAKE, 0, 8, 0, 64, 2, 0, None, 0) == ok
     assert tdx.tdx_moe_combine_bwd(0, 0, 0, 0, 0, 0, 0, 0, 64, 2, 0, None, 0) == ok
     assert tdx.tdx_moe_combine_bwd(FAKE, 0, FAKE, FAKE, 0, FAKE, 8, 4, 64, 2, 0, None, 0) == inv
+
+
+def test_row_wise_operators(tdx):
+    ok, inv = tdx.TDX_OK, tdx.TDX_ERR_INVALID_ARG
+    assert tdx.tdx_rmsnorm(0, 0, FAKE, 0, 0, 0, 0, 0, 64, 0, None, 0) == ok
+    assert tdx.tdx_rmsnorm(0, 0, 0, 0, 0, 0, 0, 0, 64, 0, None, 0) == inv                # the weight has no rows
+    assert tdx.tdx_rmsnorm_bwd(0, 0, FAKE, 0, 0, 0, 0, FAKE, 0, 64, 0, None, 0, workspace_bytes=1 << 30) == inv
+    assert tdx.tdx_moe_route(0, 0, 0, 0, FAKE, 0, 64, 8, 0, None, 0) == ok
+    assert tdx.tdx_moe_route_bwd(0, 0, 0, 0, 0, 64, 8, 0, None, 0) == ok
+    assert tdx.tdx_swiglu(0, 0, 0, 0, 0, 64, 0, None, 0) == ok
+    assert tdx.tdx_swiglu(0, 0, 0, 0, 0, 64, 0, tdx.make_act_opts(topk=8), 0) == ok
+    assert tdx.tdx_swiglu_bwd(0, 0, 0, 0, 64, 0, None, 0) == ok
