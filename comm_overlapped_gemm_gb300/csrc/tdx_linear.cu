@@ -141,8 +141,10 @@ tdx_status run(Form form, Group group, bool fp8, LinParams& p, const Operand& a,
   static LinLaunch* const launch[2][4] = {
       {launch_linear_nn, launch_linear_nt, launch_linear_tn, launch_linear_e4m3},
       {launch_linear_nn_long, launch_linear_nt_long, launch_linear_tn_long, launch_linear_e4m3_long}};
-  // more slices in a tile than one segment (kSums: a run may have all rows)
-  const bool longer = p.out_type == TDX_FP32 && (p.K + bk - 1) / bk > kLinSegment;
+  // more slices in a tile than one segment, fp32; in a CTA's part of it, others (kSums: a run may have all rows)
+  p.segment = p.out_type == TDX_FP32 ? kLinSegment : kLongSegment / bk;
+  const int most_k = p.out_type == TDX_FP32 || group == kSums ? p.K : p.K / p.split;
+  const bool longer = (most_k + bk - 1) / bk > p.segment;
   return launch[longer][fp8 ? 3 : form](group, shape.pair, p, static_cast<int>(most), st);
 }
 

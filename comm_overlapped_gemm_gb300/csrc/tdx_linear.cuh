@@ -467,7 +467,7 @@ __device__ __forceinline__ void lin_short(const LinParams& p, const LinRow& lr, 
 }
 
 // ------------------------------------------------------------------------------------------ kernel
-template <bool FP8, Form FORM, Group GROUP, bool PAIR, bool LONG>
+template <bool FP8, Form FORM, Group GROUP, bool PAIR, Sum SUM>
 __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid_constant__ LinParams p) {
   using C = LinCfg<FP8, FORM, GROUP, PAIR>;
   constexpr int BN = C::BN;
@@ -635,21 +635,28 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
         if (!lin_wait(p.status, tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, abort_flag)) break;
         tc_fence_after();
         uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
-        // slice kb, once `full` is: into the accumulator, and its slot is free when that is done
-        auto multiply = [&](int kb, uint32_t full, uint32_t parity, uint32_t a, uint32_t b, uint32_t empty) {
-          if (!lin_wait(p.status, full, parity, abort_flag)) return false;
-          tc_fence_after();
-          const int in_segment = LONG ? (kb - t.kb0) % kLinSegment : kb - t.kb0;
-          if (LONG && in_segment == 0 && kb > t.kb0) {
-            // the epilogue takes what is summed so far; on with the other accumulator
+        int start = t.kb0;   // first slice in the accumulator
+        // Other kinds than kOnce: the epilogue takes what is summed so far, slices from kb on are summed anew. kSegments
+        // goes on with the other accumulator; kLongSegments with the same, as the epilogue has the other one in use:
+        // its turn passes without a product.
+        auto next_segment = [&](int kb) {
+          for (int turn = 0; turn < (SUM == kLongSegments ? 2 : 1); ++turn) {
             if constexpr (PAIR) tc_commit_pair_multicast(tfull0 + 8 * acc, static_cast<uint16_t>(0x3));
             else tc_commit(tfull0 + 8 * acc);
             ++local;
             acc = local & 1;
             if (!lin_wait(p.status, tempty0 + 8 * acc, ((local >> 1) & 1) ^ 1u, abort_flag)) return false;
-            tc_fence_after();
-            d = tmem_base + static_cast<uint32_t>(acc * BN);
           }
+          tc_fence_after();
+          d = tmem_base + static_cast<uint32_t>(acc * BN);
+          start = kb;
+          return true;
+        };
+        // slice kb, once `full` is: into the accumulator, and its slot is free when that is done
+        auto multiply = [&](int kb, uint32_t full, uint32_t parity, uint32_t a, uint32_t b, uint32_t empty) {
+          if (!lin_wait(p.status, full, parity, abort_flag)) return false;
+          tc_fence_after();
+          const int in_segment = kb - (SUM == kOnce ? t.kb0 : start);
 #pragma unroll
           for (int k = 0; k < C::BK / C::UMMA_K; ++k) {
             const uint64_t ad = C::A_MN ? smem_desc(a + k * C::UMMA_K * 128, C::BOX_BYTES, 1024, 2u)
@@ -671,14 +678,25 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
         };
         const bool tail = GROUP == kSums && t.kb1 > t.kb0 && t.kb1 * C::BK > t.klen;
         const int whole = tail ? t.kb1 - 1 : t.kb1;
-        for (int kb = t.kb0; kb < whole; ++kb) {
-          if (!multiply(kb, full0 + 8 * stage, phase, a0 + stage * C::A_BYTES, b0 + stage * C::B_BYTES, empty0 + 8 * stage)) {
-            stop = true;
-            break;
+        int kb = t.kb0;
+        auto ring = [&](int to) {
+          for (; kb < to; ++kb) {
+            if (!multiply(kb, full0 + 8 * stage, phase, a0 + stage * C::A_BYTES, b0 + stage * C::B_BYTES, empty0 + 8 * stage)) {
+              stop = true;
+              break;
+            }
+            if (++stage == C::STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
+        };
+        if constexpr (SUM == kOnce) {
+          ring(whole);
+        } else {
+          while (kb < whole && !stop) {
+            ring(min(whole, start + p.segment));
+            if (!stop && kb < t.kb1 && kb == start + p.segment) stop = !next_segment(kb);
           }
         }
         if constexpr (GROUP == kSums) {
@@ -747,20 +765,23 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
           else mbar_arrive(tempty0 + 8 * acc);
         }
       };
-      if constexpr (LONG) {
+      // The columns that this warp sums are those it reads again below, as its own stores alone are ordered before its
+      // loads: of a gated tile a quarter of the gates and the same of the other half; of a cluster's partial its half.
+      const bool apart = p.gated && (PAIR || S == 1);
+      const int base = apart ? half * (BN / 4) : half * (BN / 2), skip = apart ? BN / 4 : 0;
+      auto full = [&] {
+        return __all_sync(0xFFFFFFFFu, lin_wait(p.status, tfull0 + 8 * (local & 1), (local >> 1) & 1, abort_flag));
+      };
+      if constexpr (SUM == kSegments) {
         // The tensor cores truncate every addition to an accumulator, always toward zero: 9e-10 relative for each
         // K, 1e-6 at 1024 and 9e-6 at 65536 against 4e-7 for sums rounded to nearest. A result that stays fp32 takes
         // the sum of segments of kLinSegment slices, added here in fp32; the last one's accumulator gets the total.
-        const int segments = (t.kb1 - t.kb0 + kLinSegment - 1) / kLinSegment;
+        const int segments = (t.kb1 - t.kb0 + p.segment - 1) / p.segment;
         if (segments > 1) {
           float sum[BN / 2];
-          // The columns that this warp reads again below, as its own stores alone are ordered before its loads: of a
-          // gated tile a quarter of the gates and the same of the other half; of a cluster's partial its half.
-          const bool apart = p.gated && (PAIR || S == 1);
-          const int base = apart ? half * (BN / 4) : half * (BN / 2), skip = apart ? BN / 4 : 0;
 #pragma unroll 1
           for (int g = 0; g < segments && ok; ++g, local += g < segments) {
-            ok = __all_sync(0xFFFFFFFFu, lin_wait(p.status, tfull0 + 8 * (local & 1), (local >> 1) & 1, abort_flag));
+            ok = full();
             if (!ok) break;
             tc_fence_after();
             const uint32_t at = tmem_base + static_cast<uint32_t>((local & 1) * BN) + lanes + base;
@@ -787,10 +808,48 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
             }
           }
         } else {
-          ok = __all_sync(0xFFFFFFFFu, lin_wait(p.status, tfull0 + 8 * (local & 1), (local >> 1) & 1, abort_flag));
+          ok = full();
         }
       } else {
-        ok = __all_sync(0xFFFFFFFFu, lin_wait(p.status, tfull0 + 8 * (local & 1), (local >> 1) & 1, abort_flag));
+        ok = full();
+      }
+      if constexpr (SUM == kLongSegments) {
+        // A result of 8 or 16 bits (half a step 4e-3) loses by truncation only in very long sums: 4e-3 at 10^6 of one
+        // sign. Its segments are so long that their additions need not overlap the next one's products: the sums so
+        // far wait in the other accumulator, and the last segment's gets the total. In instances of their own, as small
+        // tiles wait for the others' code: 1 x 4096 x 8192 14.5 us, 14.7 with this in them.
+        const int all = t.kb1 - t.kb0;   // left: slices from the present segment's first on
+#pragma unroll 1
+        for (int left = all; ok && all > p.segment && left > 0; left -= p.segment) {
+          const bool last = left <= p.segment;
+          tc_fence_after();
+          const uint32_t mine = tmem_base + static_cast<uint32_t>((local & 1) * BN) + lanes + base;
+          const uint32_t other = tmem_base + static_cast<uint32_t>((~local & 1) * BN) + lanes + base;
+          __syncwarp();
+#pragma unroll 1
+          for (int i = 0; i < BN / 2; i += 16) {
+            const uint32_t c = i + (i >= BN / 4 ? skip : 0);
+            uint32_t r[16], q[16];
+            tmem_ld_32x32b_x16(mine + c, r);
+            tmem_ld_wait(r);
+            if (left < all) {
+              tmem_ld_32x32b_x16(other + c, q);
+              tmem_ld_wait(q);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(q[k]) + __uint_as_float(r[k]));
+            }
+            tmem_st_32x32b_x16((last ? mine : other) + c, r);
+          }
+          tmem_st_wait();
+          if (left < all) release(~local & 1);   // the turn that passed
+          if (!last) {
+            release(local & 1);
+            for (int turn = 0; turn < 2 && ok; ++turn) {
+              ++local;
+              ok = full();
+            }
+          }
+        }
       }
       if (!ok) break;
       const int acc = local & 1;
@@ -840,9 +899,9 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
       } else if (box && p.steps == 0 && p.out_type == TDX_BF16) {
         if (add != nullptr) run(std::false_type{}, std::true_type{}, S0{});
         else run(std::false_type{}, std::false_type{}, S0{});
-      } else if (LinSteps<FORM>::kForward && !LONG && box && p.steps == 1 && add == nullptr) {
+      } else if (LinSteps<FORM>::kForward && SUM == kOnce && box && p.steps == 1 && add == nullptr) {
         run(std::false_type{}, std::false_type{}, std::integral_constant<int, LinSteps<FORM>::kForward ? 1 : 0>{});
-      } else if (LinSteps<FORM>::kForward && !LONG && box && p.steps == 2 && add == nullptr) {
+      } else if (LinSteps<FORM>::kForward && SUM == kOnce && box && p.steps == 2 && add == nullptr) {
         run(std::false_type{}, std::false_type{}, std::integral_constant<int, LinSteps<FORM>::kForward ? 2 : 0>{});
       } else
       // a rolled loop over 16 columns: unrolled over the tile its code came from L2 anew with every tile
@@ -948,10 +1007,10 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
 }
 
 // -------------------------------------------------------------------------------------------- host
-template <bool FP8, Form FORM, Group GROUP, bool PAIR, bool LONG>
+template <bool FP8, Form FORM, Group GROUP, bool PAIR, Sum SUM>
 tdx_status launch_linear_t(const LinParams& p, int want, cudaStream_t stream) {
   using C = LinCfg<FP8, FORM, GROUP, PAIR>;
-  auto* kernel = tdx_linear_kernel<FP8, FORM, GROUP, PAIR, LONG>;
+  auto* kernel = tdx_linear_kernel<FP8, FORM, GROUP, PAIR, SUM>;
   // per device: raised shared-memory limit and, for pairs, the clusters that are resident together
   static std::atomic<int> ready[64];
   int dev = 0;
@@ -992,10 +1051,10 @@ tdx_status launch_linear_t(const LinParams& p, int want, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? TDX_OK : TDX_ERR_CUDA;
 }
 
-template <bool FP8, Form FORM, Group GROUP, bool LONG>
+template <bool FP8, Form FORM, Group GROUP, Sum SUM>
 tdx_status launch_linear_g(const LinParams& p, bool pair, int want, cudaStream_t stream) {
-  return pair ? launch_linear_t<FP8, FORM, GROUP, true, LONG>(p, want, stream)
-              : launch_linear_t<FP8, FORM, GROUP, false, LONG>(p, want, stream);
+  return pair ? launch_linear_t<FP8, FORM, GROUP, true, SUM>(p, want, stream)
+              : launch_linear_t<FP8, FORM, GROUP, false, SUM>(p, want, stream);
 }
 
 }  // namespace tdx

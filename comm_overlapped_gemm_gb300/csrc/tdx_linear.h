@@ -10,8 +10,11 @@ namespace tdx {
 
 enum Form { NN, NT, TN };                 // see tdx_linear.cuh
 enum Group { kFlat, kRows, kSums };
+// A tile's sum over K: on the tensor cores alone; in segments of kLinSegment slices, for fp32 results; in segments of
+// kLongSegment of K, for others
+enum Sum { kOnce, kSegments, kLongSegments };
 constexpr uint64_t kLinTimeoutNs = 4000000000ull;
-constexpr int kLinSegment = 14;   // K slices summed on the tensor cores alone, for fp32 results
+constexpr int kLinSegment = 14, kLongSegment = 65536;
 constexpr int kMostSplit = 8;    // CTAs of a cluster that share a tile, the portable limit
 constexpr int kFewRows = 16;   // most rows of the small boxes of A
 
@@ -37,6 +40,7 @@ struct LinParams {
   int tiles_m, tiles_n, items, group_n;
   int few_rows;             // rows of tm_few's boxes: kFewRows, or all rows of a smaller A
   int split;                // CTAs that share a tile's K slices (single CTAs)
+  int segment;              // K slices of a segment
   int keep_a, keep_b;       // L2 policies of the operands' loads (policy_of)
   int gated;                // act == TDX_ACT_SWIGLU
   tdx_activation act;
@@ -58,8 +62,7 @@ struct LinParams {
   uint32_t* status;
 };
 
-// Instances by operand type, form and group; each form's in a file of its own, those that sum segments in fp32
-// (for fp32 results) in another. `want`: clusters of work.
+// Instances by operand type, form and group; each form's in a file of its own, those that add segments in another. `want`: clusters of work.
 using LinLaunch = tdx_status(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream);
 LinLaunch launch_linear_nn, launch_linear_nt, launch_linear_tn, launch_linear_e4m3;
 LinLaunch launch_linear_nn_long, launch_linear_nt_long, launch_linear_tn_long, launch_linear_e4m3_long;

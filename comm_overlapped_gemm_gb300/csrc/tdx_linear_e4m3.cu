@@ -4,8 +4,8 @@
 namespace tdx {
 
 tdx_status launch_linear_e4m3(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream) {
-  return g == kFlat ? launch_linear_g<true, NN, kFlat, false>(p, pair, want, stream)
-                    : launch_linear_g<true, NN, kRows, false>(p, pair, want, stream);
+  return g == kFlat ? launch_linear_g<true, NN, kFlat, kOnce>(p, pair, want, stream)
+                    : launch_linear_g<true, NN, kRows, kOnce>(p, pair, want, stream);
 }
 
 }  // namespace tdx

@@ -11,7 +11,7 @@ int lin_clusters(int split) {
   const int known = cache[dev][split].load(std::memory_order_relaxed);
   if (known > 0) return known;
   using C = LinCfg<false, NN, kFlat, false>;
-  auto* kernel = tdx_linear_kernel<false, NN, kFlat, false, false>;
+  auto* kernel = tdx_linear_kernel<false, NN, kFlat, false, kOnce>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess) return guess;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
@@ -32,8 +32,8 @@ int lin_clusters(int split) {
 }
 
 tdx_status launch_linear_nn(Group g, bool pair, const LinParams& p, int want, cudaStream_t stream) {
-  return g == kFlat ? launch_linear_g<false, NN, kFlat, false>(p, pair, want, stream)
-                    : launch_linear_g<false, NN, kRows, false>(p, pair, want, stream);
+  return g == kFlat ? launch_linear_g<false, NN, kFlat, kOnce>(p, pair, want, stream)
+                    : launch_linear_g<false, NN, kRows, kOnce>(p, pair, want, stream);
 }
 
 }  // namespace tdx

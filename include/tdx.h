@@ -503,8 +503,9 @@ tdx_status tdx_linear_opts_default(tdx_linear_opts* opts);
  * columns are multiples of 16.
  * Activations take approximate exponentials for bf16 and e4m3 outputs, within 2^-22 * (4 + |x|) of the
  * value (TDX_ACT_GELU_TANH: |x| the exponent's size, 1.6 |x + 0.045 x^3|), and exact ones for fp32; a
- * sigmoid below 2^-128 is 0. fp32 results add up segments of at most 896 (bf16; e4m3 1792) of K in fp32, as
- * the tensor cores truncate theirs; other results are one sum on the tensor cores. */
+ * sigmoid below 2^-128 is 0. The tensor cores truncate their sums' additions, so sums over K (and of a
+ * gradient's rows or columns) are added up in fp32 from segments: fp32 results of at most 896 (bf16;
+ * e4m3 1792), others of at most 65536. */
 tdx_status tdx_linear(const void* A, const void* B, const void* bias, const void* residual,
                       const float* row_scale, void* C, void* z, int M, int K, int N, tdx_dtype dtype,
                       const tdx_linear_opts* opts, void* stream);
