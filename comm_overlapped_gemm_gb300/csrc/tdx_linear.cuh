@@ -79,13 +79,14 @@ struct LinCfg {
 };
 
 // ------------------------------------------------------------------------------------ bounded waits
+template <uint64_t LIMIT>
 static __device__ __noinline__ bool lin_wait_slow(uint32_t* status, uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 15u) == 0u) {
       if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > kLinTimeoutNs) {
+      if (globaltimer_ns() - t0 > LIMIT) {
         if (status != nullptr) *status = TDX_ERR_TIMEOUT;
         *abort_flag = 1;
         return false;
@@ -93,8 +94,9 @@ static __device__ __noinline__ bool lin_wait_slow(uint32_t* status, uint32_t bar
     }
   }
 }
+template <uint64_t LIMIT = kLinTimeoutNs>
 __device__ __forceinline__ bool lin_wait(uint32_t* status, uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  return mbar_try_wait(bar, parity) || lin_wait_slow(status, bar, parity, abort_flag);
+  return mbar_try_wait(bar, parity) || lin_wait_slow<LIMIT>(status, bar, parity, abort_flag);
 }
 
 // ------------------------------------------------------------------------------------------- tiles
@@ -721,7 +723,8 @@ __global__ void __launch_bounds__(kNumThreads, 1) tdx_linear_kernel(const __grid
       const LinTile t = lin_tile<C, GROUP, PAIR>(p, off, cum, it, crank);
       const int valid = t.klen - (t.kb1 - 1) * C::BK;
       if (t.kb1 == t.kb0 || valid >= C::BK) continue;
-      const bool ok = lin_wait(p.status, tail_in, tails, abort_flag);
+      // tiles without a tail go by unseen: this may wait for as long as they take (a loader that gave up sets the flag)
+      const bool ok = lin_wait<kLinTailTimeoutNs>(p.status, tail_in, tails, abort_flag);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tails ^= 1u;
       // a K row is one 128-byte line of every box (the swizzle permutes 16-byte units inside a line)

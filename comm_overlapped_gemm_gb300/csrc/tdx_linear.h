@@ -13,7 +13,8 @@ enum Group { kFlat, kRows, kSums };
 // A tile's sum over K: on the tensor cores alone; in segments of kLinSegment slices, for fp32 results; in segments of
 // kLongSegment of K, for others
 enum Sum { kOnce, kSegments, kLongSegments };
-constexpr uint64_t kLinTimeoutNs = 4000000000ull;
+// Longest waits: for a slice, a sum or an epilogue; and for a tail, which waits for the tiles in front of its own
+constexpr uint64_t kLinTimeoutNs = 4000000000ull, kLinTailTimeoutNs = 60000000000ull;
 constexpr int kLinSegment = 14, kLongSegment = 65536;
 constexpr int kMostSplit = 8;    // CTAs of a cluster that share a tile, the portable limit
 constexpr int kFewRows = 16;   // most rows of the small boxes of A

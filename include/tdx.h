@@ -462,8 +462,8 @@ tdx_status tdx_swiglu_bwd(const void* y, const void* dout, void* dy, int R, int 
  * Row strides are in elements, 0 = dense; below the row's length: TDX_ERR_INVALID_ARG. Outputs overlap
  * no input unless said so. Sizes K, N, E, H, topk are at least 1; M, R or T of 0 launch nothing but
  * the zeroing that the formula asks for, and tensors of that many rows may then be NULL, as an empty
- * tensor's address is. A wait inside a kernel that runs out (4 s) ends that kernel's
- * work and sets opts->device_status. */
+ * tensor's address is. A wait inside a kernel that runs out (4 s for what
+ * takes milliseconds) ends that kernel's work and sets opts->device_status. */
 typedef enum {
   TDX_ACT_NONE = 0,
   TDX_ACT_RELU = 1,

@@ -161,3 +161,24 @@ def test_long_and_short_tiles_in_turn():
     for e in range(E):   # sums of integers below 2^24: exact
         want = X[at[e]:at[e + 1]].double().t() @ dY[at[e]:at[e + 1]].double()
         assert torch.equal(dB[e].float(), want.float().to(BF).float()), e
+
+
+def test_kernels_of_seconds():
+    """A weight gradient over 2^30 rows of one expert, whose tile takes over 4 s, and one with rows for the same CTA
+    after it: no wait runs out. Sums of ones in steps of 2^16: exact."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    R, K, N, E = 1 << 30, 8, 8, 512
+    off = torch.full((E + 1,), R - 128, dtype=torch.int32, device="cuda")
+    off[0] = 0
+    off[sms + 1:] = R - 59            # 69 rows: a whole slice of 64 and a tail
+    X = torch.ones(R, K, dtype=BF, device="cuda")
+    X[R - 128:] = 3.0
+    dB, status = torch.full((E, K, N), 5.0, dtype=BF, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = tdx.make_linear_opts(device_status=status)
+    tdx.check(tdx.tdx_grouped_gemm_bwd(X, X, off, None, None, dB, R, K, N, E, 0, o))
+    assert int(status) == 0
+    want = torch.zeros(E)
+    want[0], want[sms] = R - 128, 9 * 69
+    assert torch.equal(dB, want.to(BF).cuda()[:, None, None].expand(E, K, N))
