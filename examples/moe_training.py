@@ -61,7 +61,10 @@ class MoeBlock:
                       for name, w in (("norm", norm), ("router", router), ("up", up), ("down", down))}
         self.norm_opts = tdx.make_norm_opts(eps=eps)
         self.opts = tdx.make_opts(epoch=tdx.TDX_EPOCH_DEVICE)
-        self.bwd_opts = tdx.make_linear_opts(dw_dtype=tdx.TDX_FP32, accumulate=1)
+        # set if a wait inside a product's kernel runs out: without it nothing would tell
+        self.word = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.fwd_opts = tdx.make_linear_opts(device_status=self.word)
+        self.bwd_opts = tdx.make_linear_opts(dw_dtype=tdx.TDX_FP32, accumulate=1, device_status=self.word)
         up_size, down_size = (1, n, H, 2 * I, E, topk, BF16, self.opts), (1, n, I, H, E, topk, BF16, self.opts)
         self.ws_up = workspace(tdx.tdx_moe_workspace_size(*up_size))
         self.ws_down = workspace(tdx.tdx_moe_combine_workspace_size(*down_size))
@@ -83,8 +86,8 @@ class MoeBlock:
         n, H, E, I, k = self.n, self.H, self.E, self.I, self.k
         tdx.check(tdx.tdx_rmsnorm(x, residual, self.norm, self.h, self.y, None, self.rstd, n, H, BF16, self.norm_opts,
                                   stream), "tdx_rmsnorm")
-        tdx.check(tdx.tdx_linear(self.y, self.router, None, None, None, self.logits, None, n, H, E, BF16, None, stream),
-                  "tdx_linear")
+        tdx.check(tdx.tdx_linear(self.y, self.router, None, None, None, self.logits, None, n, H, E, BF16,
+                                 self.fwd_opts, stream), "tdx_linear")
         tdx.check(tdx.tdx_moe_route(self.logits, None, self.idx, self.gates, None, n, E, k, BF16, None, stream),
                   "tdx_moe_route")
         tdx.check(tdx.tdx_moe_dispatch_gemm([self.y], [self.idx], self.up, self.expert_in, self.dest, self.offsets,
@@ -125,6 +128,7 @@ class MoeBlock:
             st, detail = tdx.tdx_read_device_status(ws)
             if st != tdx.TDX_OK:
                 raise tdx.TdxError(st, f"device status {detail}")
+        tdx.check(int(self.word), "device status of the products")
 
 
 def random_block(n, H, I, E, topk, seed=0):

@@ -488,7 +488,8 @@ typedef struct tdx_linear_opts {
   int64_t ld_residual;       /* of residual; tdx_linear_bwd: of dres */
   int64_t ld_z;              /* of z; backward: of dz or dY (tdx_linear_act_bwd: of z and dz) */
   uint32_t* device_status;   /* optional device word, set to TDX_ERR_TIMEOUT if a wait ran out and
-                                otherwise left as it is */
+                                otherwise left as it is. NULL: nothing tells that outputs are
+                                incomplete; one word may serve any number of calls */
 } tdx_linear_opts;
 tdx_status tdx_linear_opts_default(tdx_linear_opts* opts);
 

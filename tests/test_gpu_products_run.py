@@ -321,3 +321,18 @@ def test_two_threads():
     assert not bad
     for b, w in zip(blocks, want):
         assert all(torch.equal(x, y) for x, y in zip(b.results(), w))
+
+
+def test_moe_block_tells_of_a_wait_that_ran_out():
+    """Every product of the example has its status word, and status() reads it."""
+    block, x, residual, d_out, d_h = example().random_block(64, 128, 64, 8, 2, seed=3)
+    block.forward(x, residual)
+    block.backward(d_out, d_h)
+    block.status()
+    assert all(o.device_status == block.word.data_ptr() for o in (block.fwd_opts, block.bwd_opts))
+    block.word.fill_(tdx.TDX_ERR_TIMEOUT)
+    with pytest.raises(tdx.TdxError):
+        block.status()
+    block.word.zero_()
+    block.forward(x, residual)
+    block.status()
