@@ -80,7 +80,16 @@ tdx_status stride_ok(int64_t ld, int64_t len, size_t elt, int64_t* out) {
   return *out * static_cast<int64_t>(elt) < kMostBytes ? TDX_OK : TDX_ERR_UNSUPPORTED;
 }
 
-// The run of one product: p holds sizes (M, N, K, cols, E, offsets) and the epilogue
+// Elements from one expert's matrix (K rows of ld) to the next one's; 0 where there is no next one
+tdx_status expert_step(int E, int K, int64_t ld, int64_t elt, int64_t* step) {
+  *step = 0;
+  if (E <= 1) return TDX_OK;
+  if (ld > kMostBytes / K || K * ld * elt >= kMostBytes) return TDX_ERR_UNSUPPORTED;
+  *step = K * ld;
+  return TDX_OK;
+}
+
+// The run of one product: p holds sizes (M, K, cols, E, offsets) and the epilogue
 tdx_status run(Form form, Group group, bool fp8, LinParams& p, const Operand& a, const Operand& b, cudaStream_t st) {
   const int bk = fp8 ? 128 : 64;
   const int64_t rows = p.M, E = p.E;
@@ -176,11 +185,10 @@ tdx_status forward(const void* A, const int32_t* offsets, const void* B, const v
       !aligned(z, 16) || !aligned(row_scale, 4) || !aligned(expert_scale, 4) || !aligned(offsets, 4) ||
       !aligned(o.device_status, 4))
     return TDX_ERR_ALIGNMENT;
-  const int64_t step = K * ld_b;
-  if (E > 1 && (ld_b > kMostBytes / K || step * elt >= kMostBytes)) return TDX_ERR_UNSUPPORTED;
+  int64_t step;
+  if ((s = expert_step(E, K, ld_b, elt, &step)) != TDX_OK) return s;
   if (M == 0) return TDX_OK;
   p.M = M;
-  p.N = N;
   p.K = K;
   p.cols = static_cast<int>(cols);
   p.E = E > 0 ? E : 1;
@@ -227,8 +235,8 @@ tdx_status backward(const void* dz, const void* A, const int32_t* offsets, const
   if (!aligned(dz, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(dres, 16) || !aligned(dA, 16) ||
       !aligned(dB, 16) || !aligned(offsets, 4) || !aligned(o.device_status, 4))
     return TDX_ERR_ALIGNMENT;
-  const int64_t step = K * ld_b;
-  if (E > 1 && (ld_b > kMostBytes / K || step * 2 >= kMostBytes)) return TDX_ERR_UNSUPPORTED;
+  int64_t step;
+  if ((s = expert_step(E, K, ld_b, 2, &step)) != TDX_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   LinParams p;
   std::memset(&p, 0, sizeof(p));
@@ -243,7 +251,7 @@ tdx_status backward(const void* dz, const void* A, const int32_t* offsets, const
     LinParams q = p;
     q.overlap = both ? kOverlapFirst : kOverlapNone;
     q.M = M;
-    q.N = q.cols = K;
+    q.cols = K;
     q.K = N;
     q.residual = static_cast<const bf16*>(dres);
     q.ld_res = ld_res;
@@ -256,7 +264,7 @@ tdx_status backward(const void* dz, const void* A, const int32_t* offsets, const
   if (dB != nullptr) {
     LinParams q = p;
     q.M = K;
-    q.N = q.cols = N;
+    q.cols = N;
     q.K = M;
     q.out = dB;
     q.ld_out = ld_b;

@@ -34,8 +34,8 @@ struct LinParams {
   CUtensorMap tm_a, tm_b;   // operands
   CUtensorMap tm_few;       // A in boxes of few rows
   CUtensorMap tm_c;         // output in boxes of 32 rows of 128 bytes
-  int M, N, K;              // output rows, accumulator columns, summed length (kRows: M, kSums: K over all runs)
-  int cols;                 // output columns: N, or N / 2 for SWIGLU
+  int M, K;                 // output rows, summed length (kRows: M, kSums: K over all runs)
+  int cols;                 // output columns: those of the product, or half of them for SWIGLU
   int E;
   const int32_t* offsets;
   int tiles_m, tiles_n, items, group_n;
