@@ -485,10 +485,12 @@ void first_wave_chunks(KParams& kp, const Plan& pl, int grid, int self_rank, boo
 // options, tiling, alignment); fills the plan. Launches nothing.
 tdx_status ag_check(const void* const* shards, const void* B, const void* C, int W, int M_local, int K, int N,
                     tdx_dtype dtype, const tdx_opts& o, Plan* pl) {
-  if (shards == nullptr || B == nullptr || C == nullptr) return TDX_ERR_INVALID_ARG;
-  if (W < 1 || W > kMaxW) return TDX_ERR_INVALID_ARG;
+  if (shards == nullptr || W < 1 || W > kMaxW) return TDX_ERR_INVALID_ARG;
+  // tensors without elements have no address
+  const bool m = M_local != 0, k = K != 0, n = N != 0;
+  if ((k && n && B == nullptr) || (m && n && C == nullptr)) return TDX_ERR_INVALID_ARG;
   for (int r = 0; r < W; ++r)
-    if (shards[r] == nullptr) return TDX_ERR_INVALID_ARG;
+    if (m && k && shards[r] == nullptr) return TDX_ERR_INVALID_ARG;
   if (o.self_rank < 0 || o.self_rank >= W) return TDX_ERR_INVALID_ARG;
   if (o.out_dtype != TDX_BF16 && o.out_dtype != TDX_FP32) return TDX_ERR_INVALID_ARG;
   if (o.mode < TDX_FUSED || o.mode > TDX_CONSUMER_ONLY) return TDX_ERR_INVALID_ARG;
@@ -635,8 +637,11 @@ tdx_status rs_call(const void* const* A_parts, const void* const* B_parts, void*
   const tdx_opts o = opts ? *opts : defaults();
   if (A_parts == nullptr || B_parts == nullptr || out_shards == nullptr) return TDX_ERR_INVALID_ARG;
   if (W < 1 || W > kMaxW) return TDX_ERR_INVALID_ARG;
+  // tensors without elements have no address
+  const bool m = M != 0, k = K != 0, n = N != 0;
   for (int r = 0; r < W; ++r)
-    if (A_parts[r] == nullptr || B_parts[r] == nullptr || out_shards[r] == nullptr) return TDX_ERR_INVALID_ARG;
+    if ((m && k && A_parts[r] == nullptr) || (k && n && B_parts[r] == nullptr) || (m && n && out_shards[r] == nullptr))
+      return TDX_ERR_INVALID_ARG;
   if (o.mode < TDX_FUSED || o.mode > TDX_MOVE_ONLY) return TDX_ERR_INVALID_ARG;
   if (o.out_dtype != TDX_BF16) return TDX_ERR_UNSUPPORTED;
   Plan pl;
@@ -1032,11 +1037,12 @@ tdx_status tdx_moe_gemm_combine(const void* Hd, const int32_t* const* topk_idx, 
                                 int W, int T, int F, int H, int E, int topk, tdx_dtype dtype, const tdx_opts* opts,
                                 void* stream) {
   const tdx_opts o = opts ? *opts : defaults();
-  if (Hd == nullptr || topk_idx == nullptr || B_experts == nullptr || gates == nullptr || out == nullptr)
+  // tensors of T = 0 tokens have no address
+  if ((T != 0 && Hd == nullptr) || topk_idx == nullptr || B_experts == nullptr || gates == nullptr || out == nullptr)
     return TDX_ERR_INVALID_ARG;
   if (W < 1 || W > kMaxW) return TDX_ERR_INVALID_ARG;
   for (int s = 0; s < W; ++s)
-    if (topk_idx[s] == nullptr || gates[s] == nullptr || out[s] == nullptr) return TDX_ERR_INVALID_ARG;
+    if (T != 0 && (topk_idx[s] == nullptr || gates[s] == nullptr || out[s] == nullptr)) return TDX_ERR_INVALID_ARG;
   if (o.mode < TDX_FUSED || o.mode > TDX_CONSUMER_ONLY) return TDX_ERR_INVALID_ARG;
   if (o.mode == TDX_CONSUMER_ONLY || o.producer != TDX_PRODUCER_SM) return TDX_ERR_UNSUPPORTED;
   MoePlan pl;
@@ -1140,11 +1146,12 @@ tdx_status tdx_moe_dispatch_gemm(const void* const* X, const int32_t* const* top
                                  int T, int H, int F, int E, int topk, tdx_dtype dtype, const tdx_opts* opts,
                                  void* stream) {
   const tdx_opts o = opts ? *opts : defaults();
-  if (X == nullptr || topk_idx == nullptr || B_experts == nullptr || Y == nullptr || dest == nullptr)
+  // tensors of T = 0 tokens have no address
+  if (X == nullptr || topk_idx == nullptr || B_experts == nullptr || (T != 0 && (Y == nullptr || dest == nullptr)))
     return TDX_ERR_INVALID_ARG;
   if (W < 1 || W > kMaxW) return TDX_ERR_INVALID_ARG;
   for (int s = 0; s < W; ++s)
-    if (X[s] == nullptr || topk_idx[s] == nullptr) return TDX_ERR_INVALID_ARG;
+    if (T != 0 && (X[s] == nullptr || topk_idx[s] == nullptr)) return TDX_ERR_INVALID_ARG;
   if (o.mode < TDX_FUSED || o.mode > TDX_CONSUMER_ONLY) return TDX_ERR_INVALID_ARG;
   if (o.mode == TDX_CONSUMER_ONLY || o.producer != TDX_PRODUCER_SM) return TDX_ERR_UNSUPPORTED;
   MoePlan pl;

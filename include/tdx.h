@@ -32,6 +32,7 @@
  *    never trap: a failed wait makes the kernel stop issuing work, drain what it started and exit.
  *  - Threading: a workspace is used by one call at a time (calls that overlap on the GPU and share a
  *    workspace race). Different workspaces may be used concurrently.
+ *  - A tensor without elements may be NULL, as an empty tensor's address is.
  *  - No fallback: shapes the kernels cannot tile return TDX_ERR_UNSUPPORTED; nothing runs on the CPU.
  */
 #ifndef TDX_H_

@@ -76,3 +76,34 @@ def test_norm_gradient(dtype):
     ws = torch.empty(tdx.tdx_rmsnorm_bwd_workspace_size(0, H, code), dtype=torch.uint8, device="cuda")
     tdx.check(tdx.tdx_rmsnorm_bwd(e, e, full(H, dtype=dtype), empty(0, dtype=F32), e, e, dw, ws, 0, H, code))
     assert bool((dw == 0).all())
+
+
+def test_dispatch_without_tokens():
+    """The offsets of no rows, and what follows them: zeros."""
+    H, F, E, k = 64, 128, 8, 2
+    B, off = full(E, H, F, dtype=BF), torch.full((E + 1,), 9, dtype=torch.int32, device="cuda")
+    o = tdx.make_opts()
+    ws = torch.empty(tdx.tdx_moe_workspace_size(1, 0, H, F, E, k, 0, o), dtype=torch.uint8, device="cuda")
+    tdx.check(tdx.tdx_workspace_init(ws))
+    ids = empty(0, k, dtype=torch.int32)
+    tdx.check(tdx.tdx_moe_dispatch_gemm([empty(0, H)], [ids], B, empty(0, F), ids, off, ws, 1, 0, H, F, E, k, 0, o))
+    assert bool((off == 0).all())
+    dB = full(E, H, F)
+    tdx.check(tdx.tdx_grouped_gemm_bwd(empty(0, F), empty(0, H), off, B, empty(0, H), dB, 0, H, F, E, 0,
+                                       tdx.make_linear_opts(dw_dtype=tdx.TDX_FP32)))
+    assert bool((dB == 0).all())
+
+
+@pytest.mark.parametrize("K", [0, 64])
+def test_all_gather_without_rows_or_columns(K):
+    """K = 0: C is zeroed."""
+    W, M, N = 2, 64, 64
+    C = full(W * M, N, dtype=BF)
+    ws = torch.empty(tdx.tdx_workspace_size(tdx.OP_AG, W, M, K, N, 0), dtype=torch.uint8, device="cuda")
+    tdx.check(tdx.tdx_workspace_init(ws))
+    if K == 0:
+        tdx.check(tdx.tdx_ag_gemm([empty(M, 0)] * W, empty(0, N), C, ws, W, M, 0, N, 0))
+        assert bool((C == 0).all())
+    else:
+        tdx.check(tdx.tdx_ag_gemm([empty(0, K)] * W, full(K, N, dtype=BF), empty(0, N), ws, W, 0, K, N, 0))
+    torch.cuda.synchronize()
