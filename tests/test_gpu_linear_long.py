@@ -182,3 +182,33 @@ def test_kernels_of_seconds():
     want = torch.zeros(E)
     want[0], want[sms] = R - 128, 9 * 69
     assert torch.equal(dB, want.to(BF).cuda()[:, None, None].expand(E, K, N))
+
+
+@pytest.mark.parametrize("acc", [0, 1])
+def test_weight_gradients_of_long_runs_on_pairs(acc):
+    """Tiles of pairs whose runs are long and short, with tails, beside the input gradient; and one layer's."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    counts, K, N = [70001, 30, 131079], 2048, 2056
+    R, E = sum(counts), len(counts)
+
+    def ints8(*shape):
+        return torch.randint(-4, 5, shape, generator=g, device="cuda", dtype=torch.int8).to(BF)
+
+    X, dY, B = ints8(R, K), ints8(R, N), ints8(E, K, N)
+    off = torch.tensor([0] + counts).cumsum(0).to(torch.int32).cuda()
+    at = off.tolist()
+    old = ints8(E, K, N)
+    dB, dX = old.clone(), torch.empty_like(X)
+    o = tdx.make_linear_opts(accumulate=acc)
+    tdx.check(tdx.tdx_grouped_gemm_bwd(dY, X, off, B, dX, dB, R, K, N, E, 0, o))
+    some = torch.tensor([0, 1, 127, 128, 255, 256, 1000, 1023, 1024, 2000, 2047], device="cuda")
+    for e in range(E):   # sums of integers below 2^24: exact
+        rows = slice(at[e], at[e + 1])
+        want = X[rows][:, some].double().t() @ dY[rows].double() + acc * old[e][some].double()
+        assert torch.equal(dB[e][some].float(), want.float().to(BF).float()), e
+        last = slice(at[e + 1] - 20, at[e + 1])
+        assert torch.equal(dX[last].float(), (dY[last].double() @ B[e].double().t()).float().to(BF).float()), e
+    dB = old[0].clone()
+    tdx.check(tdx.tdx_linear_bwd(dY, X, None, None, None, dB, R, K, N, 0, o))
+    want = X[:, some].double().t() @ dY.double() + acc * old[0][some].double()
+    assert torch.equal(dB[some].float(), want.float().to(BF).float())
